@@ -30,6 +30,16 @@ EXPORTS = ("lamb_create", "lamb_step", "lamb_destroy", "lamb_last_error", "lamb_
            "lamb_split_norms", "lamb_split_moments", "lamb_split_apply",
            "lamb_get_info", "lamb_set_speculative", "lamb_state_buffers")
 
+# Every symbol include/train_ops.h declares.
+TRAIN_EXPORTS = ("train_embed", "train_embed_grad_workspace", "train_embed_grad",
+                 "train_clip_create", "train_clip_norm", "train_clip_grads",
+                 "train_clip_partial", "train_clip_finish", "train_clip_destroy")
+TRAIN_BF16 = 0
+TRAIN_FP16 = 1
+TRAIN_FP32 = 2
+TRAIN_INT32 = 0
+TRAIN_INT64 = 1
+
 
 class LambHParams(ctypes.Structure):
     _fields_ = [("beta1", ctypes.c_float), ("beta2", ctypes.c_float), ("eps", ctypes.c_float),
@@ -138,6 +148,25 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.lamb_grad_norm_noalloc.argtypes = [i32, P, P, i32, f32, f32, P, P]
         lib.lamb_plan_limits.restype = None
         lib.lamb_plan_limits.argtypes = [ctypes.POINTER(i64)] * 4
+        lib.train_embed.restype = ctypes.c_int
+        lib.train_embed.argtypes = [P, i32, i64, i64, i64, P, i32, i64, i64, f32, P, i32, i64, P]
+        lib.train_embed_grad_workspace.restype = ctypes.c_int
+        lib.train_embed_grad_workspace.argtypes = [i64, i64, i64, ctypes.POINTER(i64)]
+        lib.train_embed_grad.restype = ctypes.c_int
+        lib.train_embed_grad.argtypes = [P, i32, i64, P, i32, i64, i64, i64, f32, i32, P, i32,
+                                         i64, i64, i64, P, i64, P]
+        lib.train_clip_create.restype = ctypes.c_int
+        lib.train_clip_create.argtypes = [ctypes.POINTER(P), i32, P, P, P, P, P, P]
+        lib.train_clip_norm.restype = ctypes.c_int
+        lib.train_clip_norm.argtypes = [P, f32, P]
+        lib.train_clip_grads.restype = ctypes.c_int
+        lib.train_clip_grads.argtypes = [P, f32, f32, P]
+        lib.train_clip_partial.restype = ctypes.c_int
+        lib.train_clip_partial.argtypes = [P, P]
+        lib.train_clip_finish.restype = ctypes.c_int
+        lib.train_clip_finish.argtypes = [P, P, f32, f32, P]
+        lib.train_clip_destroy.restype = ctypes.c_int
+        lib.train_clip_destroy.argtypes = [P]
         _lib = lib
         return lib
 

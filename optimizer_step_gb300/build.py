@@ -1,6 +1,6 @@
 """Build the in-tree CUDA library ``liblamb_gb300.so`` for sm_103a.
 
-Three translation units are compiled in parallel with nvcc and linked into one
+The translation units are compiled in parallel with nvcc and linked into one
 shared object with the CUDA runtime linked statically, so the library loads
 (and its symbols can be inspected) on a machine without a GPU.
 """
@@ -20,8 +20,9 @@ LIB = os.path.join(PKG, "liblamb_gb300.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["lamb_kernels.cu", "lamb_api.cpp", "lamb_plan.cpp", "lamb_noalloc.cu",
-           "lamb_ptrs.cu"]
-HEADERS = [os.path.join(INCLUDE, "lamb.h"), os.path.join(CSRC, "lamb_internal.h")]
+           "lamb_ptrs.cu", "train_embed.cu", "train_clip.cu"]
+HEADERS = [os.path.join(INCLUDE, "lamb.h"), os.path.join(INCLUDE, "train_ops.h"),
+           os.path.join(CSRC, "lamb_internal.h"), os.path.join(CSRC, "train_internal.h")]
 
 
 def _nvcc() -> str:

@@ -1,0 +1,158 @@
+"""The embedding lookup with scaling and its gradient by sorted tokens:
+marshalling of torch tensors to the C ABI of ``include/train_ops.h``.
+
+Both run on the current torch stream of the tensors' device, allocate nothing
+but their result and workspace through torch, and never wait for the GPU.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from ._lib import check
+
+_TYPES = {torch.bfloat16: _lib.TRAIN_BF16, torch.float16: _lib.TRAIN_FP16,
+          torch.float32: _lib.TRAIN_FP32}
+_ID_TYPES = {torch.int32: _lib.TRAIN_INT32, torch.int64: _lib.TRAIN_INT64}
+
+
+def _matrix(name, t, device):
+    """(type, dim, row stride) of a tensor whose last dimension is dense and
+    whose leading ones step evenly from row to row."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a tensor")
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    shape = t.shape
+    if not shape:
+        raise ValueError(f"{name}: needs at least one dimension")
+    dim = shape[-1]
+    if t.is_contiguous():
+        return code, dim, dim
+    if dim > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be dense")
+    stride = None  # of one row to the next
+    span = 1       # rows below the dimension looked at
+    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 0:
+            return code, dim, dim
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * span:
+            raise ValueError(f"{name}: rows must step evenly through its leading dimensions")
+        span *= n
+    if stride is None:
+        stride = dim
+    if stride < dim:
+        raise ValueError(f"{name}: rows overlap")
+    return code, dim, stride
+
+
+def _token_ids(ids, device):
+    if not isinstance(ids, torch.Tensor):
+        raise TypeError("ids: expected a tensor")
+    code = _ID_TYPES.get(ids.dtype)
+    if code is None:
+        raise TypeError(f"ids: expected int32 or int64, got {ids.dtype}")
+    if ids.device != device:
+        raise ValueError(f"ids: on {ids.device}, expected {device}")
+    if not ids.is_contiguous():
+        raise ValueError("ids: must be contiguous")
+    return code
+
+
+def _on_device(device, call):
+    """Makes ``call(stream)`` with ``device`` current and its current stream."""
+    if device.index == torch.cuda.current_device():
+        check(call(torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            check(call(torch.cuda.current_stream().cuda_stream))
+
+
+def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_row: int = 0,
+          out: torch.Tensor | None = None, out_dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Rows of ``table`` that ``ids`` name, times ``scale``, rounded once.
+
+    ``table`` is ``[n_rows, dim]`` in bfloat16, float16 or float32; ``ids`` has
+    any shape, int32 or int64, and the result is ``ids.shape + (dim,)`` in
+    ``out_dtype`` (default: the table's), or is written to ``out``.  The table
+    may hold the slice of a vocabulary that starts at token ``first_row``: a
+    token outside the slice gives a row of zeros.
+    """
+    if not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise TypeError("table: expected a tensor of two dimensions")
+    device = table.device
+    if device.type != "cuda":
+        raise ValueError("table: must live on a CUDA device")
+    t_code, dim, t_stride = _matrix("table", table, device)
+    i_code = _token_ids(ids, device)
+    shape = ids.shape + (dim,)
+    if out is None:
+        out = torch.empty(shape, dtype=out_dtype or table.dtype, device=device)
+    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out: expected shape {tuple(shape)} and out_dtype's type")
+    o_code, _, o_stride = _matrix("out", out, device)
+    _on_device(device, lambda stream: _lib.load().train_embed(
+        table.data_ptr(), t_code, table.shape[0], dim, t_stride, ids.data_ptr(), i_code,
+        ids.numel(), first_row, scale, out.data_ptr(), o_code, o_stride, stream))
+    return out
+
+
+def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None = None,
+               scale: float = 1.0, first_row: int = 0, padding_id: int = -1,
+               accumulate: bool = False, out: torch.Tensor | None = None,
+               dtype: torch.dtype | None = None) -> torch.Tensor:
+    """Gradient of ``embed`` with respect to its table.
+
+    ``grad_out`` is ``ids.shape + (dim,)``.  The result, ``[n_rows, dim]`` in
+    ``dtype`` (default: ``grad_out``'s), or ``out``, is the sum of the rows of
+    ``grad_out`` of each token times ``scale``: in fp32, in an order that only
+    the ids fix, rounded once.  Rows without a token become zero, or with
+    ``accumulate`` the sums are added to what ``out`` holds and those rows stay
+    as they are.  Tokens outside the slice that starts at ``first_row``, and
+    ``padding_id`` (negative: none), add nothing.
+    """
+    if not isinstance(grad_out, torch.Tensor):
+        raise TypeError("grad_out: expected a tensor")
+    device = grad_out.device
+    if device.type != "cuda":
+        raise ValueError("grad_out: must live on a CUDA device")
+    g_code, dim, g_stride = _matrix("grad_out", grad_out, device)
+    i_code = _token_ids(ids, device)
+    if grad_out.shape != ids.shape + (dim,):
+        raise ValueError("grad_out: expected ids.shape + (dim,)")
+    if out is None:
+        if n_rows is None:
+            raise ValueError("n_rows or out must be given")
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((n_rows, dim), dtype=dtype or grad_out.dtype, device=device)
+    elif (out.dim() != 2 or out.shape[1] != dim or n_rows not in (None, out.shape[0])
+          or (dtype is not None and out.dtype != dtype)):
+        raise ValueError("out: expected [n_rows, dim] of dtype's type")
+    o_code, _, o_stride = _matrix("out", out, device)
+    lib = _lib.load()
+    n_ids, rows = ids.numel(), out.shape[0]
+    need = ctypes.c_int64()
+    check(lib.train_embed_grad_workspace(n_ids, rows, dim, ctypes.byref(need)))
+
+    def call(stream):
+        workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
+        return lib.train_embed_grad(
+            grad_out.data_ptr(), g_code, g_stride, ids.data_ptr(), i_code, n_ids, first_row,
+            padding_id, scale, 1 if accumulate else 0, out.data_ptr(), o_code, rows, dim,
+            o_stride, workspace.data_ptr(), need.value, stream)
+
+    _on_device(device, call)
+    return out
+
+
+__all__ = ["embed", "embed_grad"]

@@ -1,0 +1,142 @@
+"""Global gradient norm over many tensors, and clipping: marshalling of torch
+tensors to the ``train_clip_*`` calls of ``include/train_ops.h``."""
+from __future__ import annotations
+
+import ctypes
+from typing import Sequence
+
+import numpy as np
+import torch
+
+from . import _lib
+from ._lib import check
+from .embedding import _TYPES
+
+
+def _checked(name, tensors, device):
+    for i, t in enumerate(tensors):
+        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
+            raise TypeError(f"{name}[{i}]: expected a bfloat16, float16 or float32 tensor")
+        if t.device != device:
+            raise ValueError(f"{name}[{i}]: on {t.device}, expected {device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}]: must be contiguous")
+
+
+def _arrays(tensors):
+    n = len(tensors)
+    types = np.fromiter((_TYPES[t.dtype] for t in tensors), dtype=np.int32, count=n)
+    ptrs = np.fromiter((t.data_ptr() for t in tensors), dtype=np.uint64, count=n)
+    return types, ptrs
+
+
+class GradClip:
+    """The global norm of a fixed list of grads, and clipping by it.
+
+    ``grads``: contiguous CUDA tensors on one device, bfloat16, float16 and
+    float32 in any mix and of any size.  ``out`` (default: the grads
+    themselves): tensors of the same sizes that receive the clipped grads,
+    each of any of the three types.  ``stream`` defaults to the current torch
+    stream at construction; every call runs on it and returns without waiting.
+
+    The calls return ``stats``, a float32 CUDA tensor that the next call
+    overwrites: the norm of ``g / loss_scale`` (inf if a grad is inf or NaN),
+    the factor that the grads are multiplied by (0 then), and 1.0 if a grad is
+    inf or NaN, else 0.0.
+    """
+
+    def __init__(self, grads: Sequence[torch.Tensor],
+                 out: Sequence[torch.Tensor] | None = None, stream=None):
+        self._lib = _lib.load()
+        self._h = None
+        grads = list(grads)
+        for i, t in enumerate(grads[:1]):
+            if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+                raise ValueError("grads must live on a CUDA device")
+        self.device = grads[0].device if grads else torch.device("cuda",
+                                                                 torch.cuda.current_device())
+        _checked("grads", grads, self.device)
+        n = len(grads)
+        sizes = np.fromiter((t.numel() for t in grads), dtype=np.int64, count=n)
+        types, ptrs = _arrays(grads)
+        out_types = out_ptrs = None
+        if out is not None:
+            out = list(out)
+            if len(out) != n:
+                raise ValueError(f"out: expected {n} tensors, got {len(out)}")
+            _checked("out", out, self.device)
+            for i, (a, b) in enumerate(zip(out, grads)):
+                if a.numel() != b.numel():
+                    raise ValueError(f"out[{i}]: expected {b.numel()} elements")
+            out_types, out_ptrs = _arrays(out)
+        self._keep = (grads, out)
+        address = lambda a: None if a is None else a.ctypes.data
+        with torch.cuda.device(self.device):
+            self.stream = stream if stream is not None else torch.cuda.current_stream()
+            with torch.cuda.stream(self.stream):
+                self.stats = torch.zeros(3, dtype=torch.float32, device=self.device)
+            h = ctypes.c_void_p()
+            check(self._lib.train_clip_create(
+                ctypes.byref(h), n, address(sizes), address(types), address(ptrs),
+                address(out_ptrs), address(out_types),
+                ctypes.c_void_p(self.stream.cuda_stream)))
+        self._h = h
+        self._stats_ptr = self.stats.data_ptr()
+
+    def _handle(self):
+        if self._h is None:
+            raise RuntimeError("handle is closed")
+        return self._h
+
+    def norm(self, loss_scale: float = 1.0) -> torch.Tensor:
+        """The norm alone; the factor in ``stats`` is ``1 / loss_scale``."""
+        check(self._lib.train_clip_norm(self._handle(), loss_scale, self._stats_ptr))
+        return self.stats
+
+    def clip(self, max_norm: float, loss_scale: float = 1.0) -> torch.Tensor:
+        """Divides the grads by ``loss_scale`` and clips their global norm to
+        ``max_norm`` (<= 0: no clipping), rounding once.  If a grad is inf or
+        NaN the outputs stay as they are."""
+        check(self._lib.train_clip_grads(self._handle(), max_norm, loss_scale, self._stats_ptr))
+        return self.stats
+
+    def _exchange(self, exchange):
+        if (not isinstance(exchange, torch.Tensor) or exchange.dtype != torch.float64
+                or exchange.device != self.device or exchange.numel() != 2
+                or not exchange.is_contiguous()):
+            raise ValueError(f"exchange: need a contiguous float64 tensor of 2 elements on "
+                             f"{self.device}")
+        return exchange.data_ptr()
+
+    def partial(self, exchange: torch.Tensor) -> torch.Tensor:
+        """This rank's ``{sum of g^2, 1 if a grad is inf or NaN}`` into
+        ``exchange``, to be summed over the ranks before ``finish``."""
+        check(self._lib.train_clip_partial(self._handle(), self._exchange(exchange)))
+        return exchange
+
+    def finish(self, exchange: torch.Tensor, max_norm: float,
+               loss_scale: float = 1.0) -> torch.Tensor:
+        """``clip`` by the norm that the summed ``exchange`` gives."""
+        check(self._lib.train_clip_finish(self._handle(), self._exchange(exchange), max_norm,
+                                          loss_scale, self._stats_ptr))
+        return self.stats
+
+    def close(self) -> None:
+        if self._h is not None:
+            h, self._h = self._h, None
+            check(self._lib.train_clip_destroy(h))
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+__all__ = ["GradClip"]
