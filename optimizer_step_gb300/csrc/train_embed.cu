@@ -46,29 +46,36 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a) {
 // G[v, :] = scale * sum over the positions i with row(ids[i]) = v of dy[i, :].
 // The positions are sorted by row (stably, so ascending within a row), and the
 // sorted list is cut into blocks of C positions.  A warp takes one block and
-// a slab of up to 256 columns, streams the rows of dy that its positions name
-// and adds each run of equal rows in registers.  A run that ends in the next
-// block at the latest is finished by the warp of the block it starts in.  A
-// longer one (a frequent token) is cut at the block boundaries: each piece's
-// fp32 sum goes to a slot of the workspace, and join_kernel adds the pieces in
-// order.  So no warp adds more than 2 C rows whatever the tokens are, only
-// long runs pay for slots, and the order of every sum depends on the ids and
-// the sizes alone.
+// a slab of up to 512 columns, streams the rows of dy that its positions name
+// through a ring of shared memory and adds each run of equal rows in
+// registers.  A run that ends in the next block at the latest is finished by
+// the warp of the block it starts in.  A longer one (a frequent token) is cut
+// at the block boundaries: each piece's fp32 sum goes to a slot of the
+// workspace, and join_kernel adds the pieces in order.  So no warp adds more
+// than 2 C rows whatever the tokens are, only long runs pay for slots, and
+// the order of every sum depends on the ids and the sizes alone.
 
 constexpr int kWarp = 32;
 constexpr unsigned kAll = 0xffffffffu;
 
+// One sorted position: the row that its token names (n_rows for a token that
+// adds nothing) and the position.
+struct __align__(8) Place {
+  uint32_t key, pos;
+};
+
 struct GradArgs {
   const void* dy;
   void* grad;
-  const uint32_t* keys;  // sorted rows; n_rows for tokens that add nothing
-  const uint32_t* pos;   // their positions
-  float* slots;          // [2 * block + (0: run from an earlier block, 1: starts here)][slot_dim]
-  int64_t dy_stride, grad_stride, n_rows, dim, slot_dim;
+  const void* ids;
+  const Place* places;  // sorted
+  float* slots;         // [2 * block + (0: run from an earlier block, 1: starts here)][slot_dim]
+  int64_t dy_stride, grad_stride, n_rows, dim, slot_dim, first_row, padding;
   int64_t n;
   int64_t n_blocks;
-  int64_t sum_units, fill_units;  // warps that add, warps that write zero rows
-  int32_t block, slabs;           // C, slabs of columns
+  int64_t units;         // blocks times slabs
+  int64_t rows_per_cta;  // of fill_kernel
+  int32_t block, slabs;  // C, slabs of columns
   float scale;
   int32_t accumulate, out_type;
 };
@@ -79,125 +86,86 @@ __device__ __forceinline__ void pdl_trigger() {
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
-
-// VEC neighbouring elements, aligned to their size together (at most 16 bytes
-// at a time).
-template <int DT, int VEC>
-struct Pack {
-  using T = typename TypeOf<DT>::T;
-  static constexpr int kBytes = VEC * int(sizeof(T));
-  static constexpr int kWords = (kBytes + 3) / 4;
-  uint32_t w[kWords];
-
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-      }
-    } else if constexpr (kBytes == 8) {
-      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = q.x, w[1] = q.y;
-    } else if constexpr (kBytes == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-      w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
-    }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (DT == TRAIN_FP32) return __uint_as_float(w[i]);
-    const uint32_t x = (i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu;
-    return to_float<DT == TRAIN_FP32 ? TRAIN_BF16 : DT>(uint16_t(x));
-  }
-};
-
-// Loads and stores of VEC neighbouring values of a type known at run time.
-template <int VEC>
-__device__ __forceinline__ void load_values(const void* p, int type, float (&x)[VEC]) {
-  if (type == TRAIN_FP32) {
-    const float* q = static_cast<const float*>(p);
-    if constexpr (VEC >= 4) {
-#pragma unroll
-      for (int i = 0; i < VEC; i += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(q + i);
-        x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) x[i] = q[i];
-    }
-    return;
-  }
-  uint16_t h[VEC];
-  const uint16_t* q = static_cast<const uint16_t*>(p);
-  if constexpr (VEC == 8) *reinterpret_cast<uint4*>(h) = *reinterpret_cast<const uint4*>(q);
-  else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(h) = *reinterpret_cast<const uint2*>(q);
-  else if constexpr (VEC == 2)
-    *reinterpret_cast<uint32_t*>(h) = *reinterpret_cast<const uint32_t*>(q);
-  else h[0] = q[0];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    x[i] = type == TRAIN_BF16 ? to_float<TRAIN_BF16>(h[i]) : to_float<TRAIN_FP16>(h[i]);
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return uint32_t(__cvta_generic_to_shared(p));
 }
-
-template <int VEC>
-__device__ __forceinline__ void store_values(void* p, int type, const float (&x)[VEC]) {
-  if (type == TRAIN_FP32) {
-    float* q = static_cast<float*>(p);
-    if constexpr (VEC >= 4) {
-#pragma unroll
-      for (int i = 0; i < VEC; i += 4)
-        *reinterpret_cast<float4*>(q + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) q[i] = x[i];
-    }
-    return;
-  }
-  alignas(16) uint16_t h[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i)
-    h[i] = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[i]) : from_float<TRAIN_FP16>(x[i]);
-  uint16_t* q = static_cast<uint16_t*>(p);
-  if constexpr (VEC == 8) *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(h);
-  else if constexpr (VEC == 4) *reinterpret_cast<uint2*>(q) = *reinterpret_cast<const uint2*>(h);
-  else if constexpr (VEC == 2)
-    *reinterpret_cast<uint32_t*>(q) = *reinterpret_cast<const uint32_t*>(h);
-  else q[0] = h[0];
+// 16 bytes from global to shared memory, asynchronously; the bytes from
+// `bytes` on are not read and become zero.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
 }
 
 __device__ __forceinline__ char* grad_at(const GradArgs& a, int64_t row, int64_t col) {
   return static_cast<char*>(a.grad) + (row * a.grad_stride + col) * size_of(a.out_type);
 }
 
-// grad[row, col ..] = round(old + scale * sum)
-template <int VEC>
-__device__ __forceinline__ void finish_row(const GradArgs& a, int64_t row, int64_t col,
-                                           const float* acc) {
-  void* p = grad_at(a, row, col);
-  float x[VEC];
-  if (a.accumulate) {
-    load_values<VEC>(p, a.out_type, x);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = fmaf(a.scale, acc[i], x[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) x[i] = a.scale * acc[i];
+// Eight neighbouring values, 16-byte aligned (each half, if 32 bits wide).
+__device__ __forceinline__ void load8(const void* p, int type, float (&x)[8]) {
+  if (type == TRAIN_FP32) {
+    const float4 u = static_cast<const float4*>(p)[0], v = static_cast<const float4*>(p)[1];
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+    return;
   }
-  store_values<VEC>(p, a.out_type, x);
+  const uint4 q = *static_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == TRAIN_BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      x[2 * i] = to_float<TRAIN_FP16>(uint16_t(w[i] & 0xffffu));
+      x[2 * i + 1] = to_float<TRAIN_FP16>(uint16_t(w[i] >> 16));
+    }
+  }
 }
 
-// First index with keys[index] >= row.
-__device__ __forceinline__ int64_t lower_bound(const uint32_t* keys, int64_t n, uint32_t row) {
+__device__ __forceinline__ void store8(void* p, int type, const float (&x)[8]) {
+  if (type == TRAIN_FP32) {
+    static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[2 * i])
+                                           : from_float<TRAIN_FP16>(x[2 * i]);
+    const uint32_t hi = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[2 * i + 1])
+                                           : from_float<TRAIN_FP16>(x[2 * i + 1]);
+    w[i] = lo | hi << 16;
+  }
+  *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float load1(const void* p, int type) {
+  if (type == TRAIN_FP32) return *static_cast<const float*>(p);
+  const uint16_t h = *static_cast<const uint16_t*>(p);
+  return type == TRAIN_BF16 ? to_float<TRAIN_BF16>(h) : to_float<TRAIN_FP16>(h);
+}
+
+__device__ __forceinline__ void store1(void* p, int type, float x) {
+  if (type == TRAIN_FP32) *static_cast<float*>(p) = x;
+  else if (type == TRAIN_BF16) *static_cast<uint16_t*>(p) = from_float<TRAIN_BF16>(x);
+  else *static_cast<uint16_t*>(p) = from_float<TRAIN_FP16>(x);
+}
+
+// First index whose row is at least `row`.
+__device__ __forceinline__ int64_t lower_bound(const Place* places, int64_t n, uint32_t row) {
   int64_t lo = 0, hi = n;
   while (lo < hi) {
     const int64_t mid = (lo + hi) >> 1;
-    if (keys[mid] < row) lo = mid + 1;
+    if (places[mid].key < row) lo = mid + 1;
     else hi = mid;
   }
   return lo;
@@ -215,196 +183,360 @@ __device__ __forceinline__ void warp_zero(char* p, int64_t bytes, int lane) {
     *reinterpret_cast<uint16_t*>(q + i) = 0;
 }
 
-// Zeros the rows r0 .. r0 + 31 that no token names.
-__device__ __forceinline__ void fill_rows(const GradArgs& a, int64_t r0, int lane) {
-  const int64_t row = r0 + lane;
-  bool idle = row < a.n_rows;
-  if (idle) {
-    const int64_t at = lower_bound(a.keys, a.n, uint32_t(row));
-    idle = at >= a.n || a.keys[at] != uint32_t(row);
+// Zeros the rows that no token names, a range of rows a CTA.  SCAN: the CTA
+// marks its rows by a walk over all ids, so it needs no sorted list and runs
+// while the tokens are being sorted.  Else it looks its rows up in that list.
+constexpr int kFillThreads = 512;
+constexpr int kFillRows = 4096;  // at most, a CTA
+
+template <bool SCAN, class ID>
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ uint32_t named[kFillRows / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = int64_t(blockIdx.x) * a.rows_per_cta;
+  const int64_t count = min(a.rows_per_cta, a.n_rows - r0);
+  pdl_trigger();
+  for (int i = threadIdx.x; i < kFillRows / 32; i += kFillThreads) named[i] = 0u;
+  __syncthreads();
+  if (SCAN) {
+    const ID* ids = static_cast<const ID*>(a.ids);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < a.n; i += kFillThreads) {
+      const ID id = ids[i];
+      const uint64_t r = uint64_t(int64_t(id)) - uint64_t(a.first_row) - uint64_t(r0);
+      if (r < uint64_t(count) && int64_t(id) != a.padding)
+        atomicOr(&named[r / 32], 1u << (r & 31));
+    }
+  } else {
+    pdl_wait();
+    const int64_t lo = lower_bound(a.places, a.n, uint32_t(r0));
+    const int64_t hi = lower_bound(a.places, a.n, uint32_t(r0 + count));
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kFillThreads) {
+      const uint32_t r = a.places[i].key - uint32_t(r0);
+      atomicOr(&named[r / 32], 1u << (r & 31));
+    }
   }
-  unsigned todo = __ballot_sync(kAll, idle);
-  while (todo) {
-    const int k = __ffs(todo) - 1;
-    todo &= todo - 1;
-    warp_zero(grad_at(a, r0 + k, 0), a.dim * size_of(a.out_type), lane);
-  }
+  __syncthreads();
+  for (int64_t r = warp; r < count; r += kFillThreads / kWarp)
+    if (!((named[r / 32] >> (r & 31)) & 1u))
+      warp_zero(grad_at(a, r0 + r, 0), a.dim * size_of(a.out_type), lane);
+  // What follows waits for this kernel; it must find the sort finished too.
+  if (SCAN) pdl_wait();
 }
 
-// VEC neighbouring columns a load, GROUPS loads a lane and row; a warp covers
-// 32 * VEC * GROUPS columns.
-template <int IN, int VEC, int GROUPS>
-__global__ void __launch_bounds__(kThreads) sum_kernel(const __grid_constant__ GradArgs a) {
-  using TI = typename TypeOf<IN>::T;
-  constexpr int kCols = VEC * GROUPS;
-  constexpr int kRows = 8;  // rows of dy in flight
+// The ring of one warp: kStages rows' pieces of a slab in flight.  The copies
+// are asynchronous (16 bytes a lane), so they hold no registers, and the rows
+// of the grad that accumulation needs come through the same ring behind the
+// last row of their run: nothing waits for them when the run is finished.
+constexpr int kStages = 8;
+constexpr int kStageBytes = 1024 + 32;  // a piece and its ends' alignment
+constexpr int kMaxBlock = 128;
+constexpr int kSumWarps = 4;
+
+struct WarpSmem {
+  alignas(16) unsigned char ring[kStages][kStageBytes];
+  uint32_t key[2 * kMaxBlock + 4];
+  uint32_t pos[2 * kMaxBlock];
+};
+
+// COLS columns a lane: 16 where no 32-bit type comes through the ring, else 8.
+// ALIGNED: rows of dy and of the grad start at multiples of 16 bytes and dim is
+// a multiple of 8; a lane holds groups of 8 neighbours and copies exactly what
+// it reads.  Else a lane holds every 32nd column, and the 16-byte granules
+// that cover a piece are copied, its neighbours' bytes with it.
+template <int IN, int COLS, bool ALIGNED>
+__global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
+    const __grid_constant__ GradArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  constexpr int kSlab = kWarp * COLS;
   const int lane = threadIdx.x & 31;
-  const int64_t unit = int64_t(blockIdx.x) * (kThreads / kWarp) + (threadIdx.x >> 5);
+  WarpSmem& s = reinterpret_cast<WarpSmem*>(raw)[threadIdx.x >> 5];
+  const int64_t unit = int64_t(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
   pdl_trigger();
   pdl_wait();
-  if (unit >= a.sum_units) {
-    if (unit < a.sum_units + a.fill_units) fill_rows(a, (unit - a.sum_units) * kWarp, lane);
-    return;
-  }
+  if (unit >= a.units) return;
   const int64_t b = unit / a.slabs;
-  const int64_t col0 = (unit % a.slabs) * (kWarp * kCols) + lane * VEC;
-  const int64_t C = a.block, n = a.n;
-  const int64_t lo = b * C, hi = min(lo + C, n);
+  const int64_t col0 = (unit % a.slabs) * kSlab;
+  const int cols = int(min(int64_t(kSlab), a.dim - col0));
+  const int64_t n = a.n, lo = b * a.block;
+  const int C = a.block;
   const uint32_t none = uint32_t(a.n_rows);
-  const uint32_t first = a.keys[lo], last = a.keys[hi - 1];
+
+  // The block and the next one: rows behind the list count as `none`.
+  for (int i = lane; i < 2 * C; i += kWarp) {
+    Place p{none, 0u};
+    if (lo + i < n) p = a.places[lo + i];
+    s.key[i] = p.key;
+    s.pos[i] = p.pos;
+  }
+  const uint32_t after = lo + 2 * C < n ? a.places[lo + 2 * C].key : none;
+  const uint32_t before = lo > 0 ? a.places[lo - 1].key : none;
+  const uint32_t far_before = lo > C ? a.places[lo - C - 1].key : none;
+  if (lane == 0) s.key[2 * C] = after;
+  __syncwarp();
+  const uint32_t first = s.key[0], last = s.key[C - 1];
   if (first == none) return;
   // The run that reaches in from the block before: a piece of a long run, or
   // finished by its own block.
-  const bool from_before = lo > 0 && a.keys[lo - 1] == first;
-  const bool head_piece = from_before && ((hi < n && a.keys[hi] == first) ||
-                                          (lo > C && a.keys[lo - C - 1] == first));
+  const bool from_before = before == first;
+  const bool head_piece = from_before && (s.key[C] == first || far_before == first);
   // The run that starts here and reaches out: into the next block at most, or
   // long.
   const bool reaches_out =
-      hi < n && last != none && a.keys[hi] == last && !(from_before && first == last);
-  const bool tail_piece = reaches_out && hi + C < n && a.keys[hi + C] == last;
-  const int64_t end = reaches_out && !tail_piece ? min(hi + C, n) : hi;
-  bool skip = from_before && !head_piece;  // until the first other row
-  bool head = head_piece;                  // adding the piece from before
-  float acc[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
+      last != none && s.key[C] == last && !(from_before && first == last);
+  const bool tail_piece = reaches_out && after == last;
+  const int end = reaches_out && !tail_piece ? 2 * C : C;
+  // Positions [x, stop) of the window are added here.
+  int x = 0, stop = 0;
+  for (int i0 = 0; i0 < end; i0 += kWarp) {
+    const int i = i0 + lane;
+    const uint32_t key = i < end ? s.key[i] : none;
+    const bool skipped = from_before && !head_piece && key == first;
+    const bool wanted = key != none && !skipped && (i < C || key == last);
+    const unsigned use = __ballot_sync(kAll, wanted), skip = __ballot_sync(kAll, skipped);
+    x += __popc(skip);
+    stop += __popc(skip | use);
+  }
+  if (x >= stop) return;
 
-  for (int64_t x0 = lo; x0 < end; x0 += kWarp) {
-    const int64_t x = x0 + lane;
-    uint32_t key = none, next = none, at = 0;
-    if (x < end) {
-      key = a.keys[x];
-      at = a.pos[x];
-      if (x + 1 < n) next = a.keys[x + 1];
-    }
-    // Positions to add: real rows, not those of a run finished elsewhere; past
-    // hi only those of the run that reaches out.
-    const bool wanted = key != none && !(skip && key == first) && (x < hi || key == last);
-    const unsigned use = __ballot_sync(kAll, wanted);
-    const unsigned ends = __ballot_sync(kAll, wanted && key != next);
-    if (skip && !__all_sync(kAll, key == first)) skip = false;
-    int k = use ? __ffs(use) - 1 : kWarp;
-    const int stop = use ? kWarp - __clz(use) : 0;
-    while (k < stop) {
-      // The wanted positions are neighbours: kRows of them at a time.
-      Pack<IN, VEC> q[kRows][GROUPS];
+  const char* const dy = static_cast<const char*>(a.dy);
+  char* const grad = static_cast<char*>(a.grad);
+  const int out_size = size_of(a.out_type);
+  // A run's last position here.  Only final sums need the old row.
+  const auto ends = [&](int i) { return s.key[i] != s.key[i + 1]; };
+  const auto is_head = [&](uint32_t key) { return head_piece && key == first; };
+
+  // Starts the copy of the piece [col0, col0 + cols) of a row at `row`.
+  const auto copy_piece = [&](unsigned char* dst, const char* row, int size, const char* begin,
+                              const char* limit) {
+    const char* src = row + col0 * size;
+    if constexpr (ALIGNED) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        const uint32_t p = __shfl_sync(kAll, at, (k + r) & 31);
-        const TI* src = static_cast<const TI*>(a.dy) + int64_t(p) * a.dy_stride + col0;
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          if (k + r < stop && col0 + g * (kWarp * VEC) < a.dim)
-            q[r][g].load(src + g * (kWarp * VEC));
-          else
-            q[r][g].clear();
+      for (int g = 0; g < COLS / 8; ++g) {
+        const int c = g * 8 * kWarp + lane * 8;
+        if (c < cols) {
+          copy16(dst + c * size, src + c * size, 16);
+          if (size == 4) copy16(dst + c * size + 16, src + c * size + 16, 16);
         }
       }
+    } else {
+      const int shift = int(reinterpret_cast<uintptr_t>(src) & 15);
+      const int granules = (shift + cols * size + 15) / 16;
+      for (int g = lane; g < granules; g += kWarp) {
+        const char* q = src - shift + 16 * g;
+        if (q >= begin) {
+          const int64_t left = limit - q;
+          copy16(dst + 16 * g, q, left < 16 ? int(left) : 16);
+        } else {
+          // In front of the matrix: only what belongs to it.
+          for (int i = int(begin - q); i < 16; i += 2)
+            if (q + i < limit)
+              *reinterpret_cast<uint16_t*>(dst + 16 * g + i) =
+                  *reinterpret_cast<const uint16_t*>(q + i);
+        }
+      }
+    }
+  };
+  const char* const dy_limit = dy + ((n - 1) * a.dy_stride + a.dim) * size_of(IN);
+  const char* const grad_limit = grad + ((a.n_rows - 1) * a.grad_stride + a.dim) * out_size;
+
+  // The next piece to fetch: position at, or the old row behind it.
+  int at = x;
+  bool old_next = false;
+  const auto fetch = [&](int stage) {
+    if (at < stop) {
+      if (!old_next) {
+        copy_piece(s.ring[stage], dy + int64_t(s.pos[at]) * a.dy_stride * size_of(IN),
+                   size_of(IN), dy, dy_limit);
+        old_next = a.accumulate && ends(at) && !is_head(s.key[at]);
+        if (!old_next) ++at;
+      } else {
+        copy_piece(s.ring[stage], grad_at(a, s.key[at], 0), out_size, grad, grad_limit);
+        old_next = false;
+        ++at;
+      }
+    }
+    copy_commit();
+  };
+  // A lane's values of the piece in a stage; `row` gives its alignment.
+  const auto read_piece = [&](int stage, const char* row, int type, float (&v)[COLS]) {
+    if constexpr (ALIGNED) {
 #pragma unroll
-      for (int r = 0; r < kRows; ++r) {
-        if (k + r < stop) {
+      for (int g = 0; g < COLS / 8; ++g) {
+        float u[8];
+        load8(s.ring[stage] + (g * 8 * kWarp + lane * 8) * size_of(type), type, u);
 #pragma unroll
-          for (int g = 0; g < GROUPS; ++g)
+        for (int i = 0; i < 8; ++i) v[8 * g + i] = u[i];
+      }
+    } else {
+      const int shift = int(reinterpret_cast<uintptr_t>(row + col0 * size_of(type)) & 15);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[g * VEC + i] += q[r][g].get(i);
-          if ((ends >> (k + r)) & 1u) {
-            const int64_t row = __shfl_sync(kAll, key, k + r);
+      for (int i = 0; i < COLS; ++i)
+        v[i] = load1(s.ring[stage] + shift + (lane + kWarp * i) * size_of(type), type);
+    }
+  };
+
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  float acc[COLS];
 #pragma unroll
-            for (int g = 0; g < GROUPS; ++g) {
-              const int64_t col = col0 + g * (kWarp * VEC);
-              if (col < a.dim) {
-                if (head) {
-                  float* s = a.slots + 2 * b * a.slot_dim + col;
+  for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+  int stage = 0;
+  const auto next_stage = [&] {
+    // One more piece into the stage read last, then wait for the oldest.
+    __syncwarp();
+    fetch(stage == 0 ? kStages - 1 : stage - 1);
+    copy_wait<kStages - 1>();
+    __syncwarp();
+  };
+  const auto done_stage = [&] { stage = stage == kStages - 1 ? 0 : stage + 1; };
+  const auto write_slot = [&](int which) {
+    float* slot = a.slots + (2 * b + which) * a.slot_dim + col0;
+    if constexpr (ALIGNED) {
 #pragma unroll
-                  for (int i = 0; i < VEC; ++i) s[i] = acc[g * VEC + i];
-                } else {
-                  finish_row<VEC>(a, row, col, acc + g * VEC);
-                }
-              }
-            }
+      for (int g = 0; g < COLS / 8; ++g) {
+        const int c = g * 8 * kWarp + lane * 8;
+        if (c < cols) {
+          float u[8];
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) acc[i] = 0.0f;
-            head = false;
+          for (int i = 0; i < 8; ++i) u[i] = acc[8 * g + i];
+          store8(slot + c, TRAIN_FP32, u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < COLS; ++i)
+        if (lane + kWarp * i < cols) slot[lane + kWarp * i] = acc[i];
+    }
+  };
+
+  for (; x < stop; ++x) {
+    next_stage();
+    float v[COLS];
+    read_piece(stage, dy + int64_t(s.pos[x]) * a.dy_stride * size_of(IN), IN, v);
+    done_stage();
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) acc[i] += v[i];
+    if (!ends(x)) continue;
+    const uint32_t key = s.key[x];
+    if (is_head(key)) {
+      write_slot(0);
+    } else {
+      char* row = grad_at(a, key, 0);
+      if (a.accumulate) {
+        next_stage();
+        read_piece(stage, row, a.out_type, v);
+        done_stage();
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) acc[i] = fmaf(a.scale, acc[i], v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) acc[i] *= a.scale;
+      }
+      if constexpr (ALIGNED) {
+#pragma unroll
+        for (int g = 0; g < COLS / 8; ++g) {
+          const int c = g * 8 * kWarp + lane * 8;
+          if (c < cols) {
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = acc[8 * g + i];
+            store8(row + (col0 + c) * out_size, a.out_type, u);
           }
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i)
+          if (lane + kWarp * i < cols)
+            store1(row + (col0 + lane + kWarp * i) * out_size, a.out_type, acc[i]);
       }
-      k += kRows;
     }
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
   }
   // What is left in the registers is a piece of a run that goes on.
-  if (head || tail_piece) {
-    float* s = a.slots + (2 * b + (head ? 0 : 1)) * a.slot_dim;
-#pragma unroll
-    for (int g = 0; g < GROUPS; ++g) {
-      const int64_t col = col0 + g * (kWarp * VEC);
-      if (col < a.dim) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) s[col + i] = acc[g * VEC + i];
-      }
-    }
-  }
+  if (!ends(stop - 1)) write_slot(is_head(s.key[stop - 1]) ? 0 : 1);
 }
 
-// Adds the pieces of every long run, in order.  A CTA takes 32 columns (grid
-// x) and every gridDim.y-th long run: its warps add neighbouring shares of the
-// pieces, and the first warp adds the warps' sums.
-constexpr int kJoinWarps = 16;
+// Adds the pieces of every long run, in order.  A CTA takes a slab of 128
+// columns and every gridDim.y-th long run: its warps add neighbouring shares
+// of the pieces (8 at least), and the first warp adds the warps' sums.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 128;
 
 __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(
     const __grid_constant__ GradArgs a) {
-  __shared__ float part[kJoinWarps][kWarp];
-  __shared__ int64_t found[kJoinWarps * kWarp];
-  __shared__ int count;
+  __shared__ float4 part[kJoinWarps][kWarp];
+  __shared__ uint32_t found[kJoinWarps * kWarp];
+  __shared__ int rank[kJoinWarps];
+  constexpr int kThreads = kJoinWarps * kWarp;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = int64_t(blockIdx.x) * kWarp + lane;
+  const int64_t col = int64_t(blockIdx.x) * kJoinCols + 4 * lane;  // slots: whole groups of 8
   const int64_t C = a.block, n = a.n;
   const uint32_t none = uint32_t(a.n_rows);
-  int64_t seen = 0;
+  unsigned seen = 0;
   pdl_wait();
-  for (int64_t b0 = 0; b0 < a.n_blocks; b0 += kJoinWarps * kWarp) {
+  for (int64_t b0 = 0; b0 < a.n_blocks; b0 += kThreads) {
     // Blocks in which a long run starts, in ascending order.
     const int64_t b = b0 + threadIdx.x;
     bool starts = false;
     if (b < a.n_blocks && (b + 2) * C < n) {
-      const uint32_t last = a.keys[(b + 1) * C - 1];
-      starts = last != none && a.keys[(b + 2) * C] == last &&
-               (b == 0 || a.keys[b * C - 1] != last);
+      const uint32_t last = a.places[(b + 1) * C - 1].key;
+      const uint32_t out = a.places[(b + 2) * C].key;
+      const uint32_t in = b == 0 ? none : a.places[b * C - 1].key;
+      starts = last != none && out == last && in != last;
     }
-    int at = __syncthreads_count(starts);
-    if (at == 0) continue;
-    // Rank of this block among them: blocks of the warps before, then lanes.
     const unsigned mask = __ballot_sync(kAll, starts);
-    if (lane == 0) part[warp][0] = float(__popc(mask));
+    if (lane == 0) rank[warp] = __popc(mask);
     __syncthreads();
-    int before = __popc(mask & ((1u << lane) - 1u));
-    for (int w = 0; w < warp; ++w) before += int(part[w][0]);
-    if (starts) found[before] = b;
-    if (threadIdx.x == 0) count = at;
+    int place = __popc(mask & ((1u << lane) - 1u)), all = 0;
+    for (int w = 0; w < kJoinWarps; ++w) {
+      if (w < warp) place += rank[w];
+      all += rank[w];
+    }
+    if (starts) found[place] = uint32_t(b);
     __syncthreads();
-    const int all = count;
     for (int k = 0; k < all; ++k, ++seen) {
       if (seen % gridDim.y != blockIdx.y) continue;
       const int64_t from = found[k];
-      const uint32_t row = a.keys[(from + 1) * C - 1];
-      const int64_t run_end = lower_bound(a.keys, n, row + 1);
-      const int64_t pieces = (run_end - 1) / C - from + 1;
-      const int64_t share = (pieces + kJoinWarps - 1) / kJoinWarps;
-      const int64_t p0 = warp * share, p1 = min(p0 + share, pieces);
-      float acc = 0.0f;
-      if (col < a.dim) {
-#pragma unroll 8
-        for (int64_t p = p0; p < p1; ++p)
-          acc += a.slots[(2 * (from + p) + (p == 0 ? 1 : 0)) * a.slot_dim + col];
+      const uint32_t row = a.places[(from + 1) * C - 1].key;
+      // The run covers the start of every block it has a piece in but its first.
+      int64_t pieces = 1;
+      for (int64_t q = from + 1;; q += kThreads) {
+        const int64_t at = (q + threadIdx.x) * C;
+        const int more = __syncthreads_count(at < n && a.places[at < n ? at : 0].key == row);
+        pieces += more;
+        if (more < kThreads) break;
       }
-      __syncthreads();
+      int64_t share = (pieces + kJoinWarps - 1) / kJoinWarps;
+      if (share < 8) share = 8;
+      const int64_t p0 = warp * share, p1 = min(p0 + share, pieces);
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (col < a.slot_dim) {
+#pragma unroll 8
+        for (int64_t p = p0; p < p1; ++p) {
+          const float4 v = *reinterpret_cast<const float4*>(
+              a.slots + (2 * (from + p) + (p == 0 ? 1 : 0)) * a.slot_dim + col);
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+      }
       part[warp][lane] = acc;
       __syncthreads();
       if (warp == 0 && col < a.dim) {
-        float total[1] = {0.0f};
-        for (int w = 0; w < kJoinWarps; ++w) total[0] += part[w][lane];
-        finish_row<1>(a, row, col, total);
+        for (int w = 1; w < kJoinWarps && w * share < pieces; ++w) {
+          const float4 v = part[w][lane];
+          acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (col + i < a.dim) {
+            char* g = grad_at(a, row, col + i);
+            const float old = a.accumulate ? load1(g, a.out_type) : 0.0f;
+            store1(g, a.out_type, a.accumulate ? fmaf(a.scale, x[i], old) : a.scale * x[i]);
+          }
+        }
       }
+      __syncthreads();
     }
     __syncthreads();
   }
@@ -421,8 +553,7 @@ constexpr int kDigits = 256;
 struct SortArgs {
   const void* ids;
   int64_t n, first_row, n_rows, padding;
-  uint32_t* keys;
-  uint32_t* pos;
+  Place* places;  // the result
   int32_t bits, passes;  // of the keys; digits of (bits + passes - 1) / passes bits
 };
 
@@ -508,17 +639,16 @@ __device__ __forceinline__ void digit_bases(RankSmem& s, uint32_t all, uint32_t 
 }
 
 // Up to 8 * 1024 * ITEMS positions in one cluster: every CTA holds a tile of
-// 1024 * ITEMS elements in registers and shared memory, the CTAs exchange their
-// digit counts, and each pass scatters through distributed shared memory; the
-// last one writes to global memory.
+// 1024 * ITEMS elements, the CTAs exchange their digit counts, and each pass
+// scatters through distributed shared memory; the last one writes to global
+// memory.
 template <int ITEMS, class ID>
 __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
     const __grid_constant__ SortArgs a) {
   constexpr int kTile = kSortThreads * ITEMS;
   extern __shared__ __align__(16) unsigned char raw[];
   RankSmem& s = *reinterpret_cast<RankSmem*>(raw);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(raw + sizeof(RankSmem));
-  uint32_t* pos = keys + kTile;
+  Place* tile = reinterpret_cast<Place*>(raw + sizeof(RankSmem));
   cg::cluster_group cluster = cg::this_cluster();
   const int me = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -526,32 +656,30 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
   const int width = (a.bits + a.passes - 1) / a.passes;
   const uint32_t mask = (1u << width) - 1u;
   const int local0 = warp * (kWarp * ITEMS) + lane;
-  uint32_t key[ITEMS], at[ITEMS], digit[ITEMS], rank[ITEMS];
+  Place x[ITEMS];
 #pragma unroll
   for (int j = 0; j < ITEMS; ++j) {
     const int64_t i = int64_t(me) * kTile + local0 + kWarp * j;
-    at[j] = uint32_t(i);
     // Behind the last token: the largest digits, so these stay behind it.
-    key[j] = i < a.n ? key_of<ID>(a, i) : 0xffffffffu;
+    x[j].key = i < a.n ? key_of<ID>(a, i) : 0xffffffffu;
+    x[j].pos = uint32_t(i);
   }
   for (int p = 0; p < a.passes; ++p) {
     if (p > 0) {
 #pragma unroll
-      for (int j = 0; j < ITEMS; ++j) {
-        key[j] = keys[local0 + kWarp * j];
-        at[j] = pos[local0 + kWarp * j];
-      }
+      for (int j = 0; j < ITEMS; ++j) x[j] = tile[local0 + kWarp * j];
     }
+    uint32_t digit[ITEMS], rank[ITEMS];
 #pragma unroll
-    for (int j = 0; j < ITEMS; ++j) digit[j] = (key[j] >> (p * width)) & mask;
+    for (int j = 0; j < ITEMS; ++j) digit[j] = (x[j].key >> (p * width)) & mask;
     rank_digits<ITEMS>(s, digit, rank);
     cluster.sync();  // the counts are there, and the tiles have been read
     uint32_t all = 0, mine = 0;
     if (threadIdx.x < kDigits) {
       for (int r = 0; r < ctas; ++r) {
-        const uint32_t x = cluster.map_shared_rank(s.total, r)[threadIdx.x];
-        if (r < me) mine += x;
-        all += x;
+        const uint32_t c = cluster.map_shared_rank(s.total, r)[threadIdx.x];
+        if (r < me) mine += c;
+        all += c;
       }
     }
     digit_bases(s, all, mine);
@@ -559,15 +687,8 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
 #pragma unroll
     for (int j = 0; j < ITEMS; ++j) {
       const uint32_t to = s.base[digit[j]] + s.warp_count[warp][digit[j]] + rank[j];
-      if (out) {
-        if (to < a.n) {
-          a.keys[to] = key[j];
-          a.pos[to] = at[j];
-        }
-      } else {
-        cluster.map_shared_rank(keys, int(to / kTile))[to % kTile] = key[j];
-        cluster.map_shared_rank(pos, int(to / kTile))[to % kTile] = at[j];
-      }
+      if (!out) cluster.map_shared_rank(tile, int(to / kTile))[to % kTile] = x[j];
+      else if (to < a.n) a.places[to] = x[j];
     }
     cluster.sync();  // the tiles are written, and the counts have been read
   }
@@ -580,10 +701,8 @@ constexpr int kGlobalTile = kSortThreads * kTileItems;
 
 struct PassArgs {
   SortArgs s;
-  const uint32_t* keys_in;  // NULL: from the ids
-  const uint32_t* pos_in;
-  uint32_t* keys_out;
-  uint32_t* pos_out;
+  const Place* in;  // NULL: from the ids
+  Place* out;
   uint32_t* counts;  // [digit][tile]
   uint32_t* totals;  // [digit]
   int64_t tiles;
@@ -591,29 +710,25 @@ struct PassArgs {
 };
 
 template <class ID>
-__device__ __forceinline__ void load_tile(const PassArgs& a, uint32_t (&key)[kTileItems],
-                                          uint32_t (&at)[kTileItems],
+__device__ __forceinline__ void load_tile(const PassArgs& a, Place (&x)[kTileItems],
                                           uint32_t (&digit)[kTileItems]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int j = 0; j < kTileItems; ++j) {
     const int64_t i = int64_t(blockIdx.x) * kGlobalTile + warp * (kWarp * kTileItems) +
                       kWarp * j + lane;
-    key[j] = 0xffffffffu;
-    at[j] = 0;
-    if (i < a.s.n) {
-      key[j] = a.keys_in ? a.keys_in[i] : key_of<ID>(a.s, i);
-      at[j] = a.keys_in ? a.pos_in[i] : uint32_t(i);
-    }
-    digit[j] = (key[j] >> a.shift) & ((1u << a.width) - 1u);
+    x[j] = Place{0xffffffffu, 0u};
+    if (i < a.s.n) x[j] = a.in ? a.in[i] : Place{key_of<ID>(a.s, i), uint32_t(i)};
+    digit[j] = (x[j].key >> a.shift) & ((1u << a.width) - 1u);
   }
 }
 
 template <class ID>
 __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ PassArgs a) {
   __shared__ RankSmem s;
-  uint32_t key[kTileItems], at[kTileItems], digit[kTileItems], rank[kTileItems];
-  load_tile<ID>(a, key, at, digit);
+  Place x[kTileItems];
+  uint32_t digit[kTileItems], rank[kTileItems];
+  load_tile<ID>(a, x, digit);
   rank_digits<kTileItems>(s, digit, rank);
   __syncthreads();
   if (threadIdx.x < kDigits) a.counts[threadIdx.x * a.tiles + blockIdx.x] = s.total[threadIdx.x];
@@ -651,8 +766,9 @@ template <class ID>
 __global__ void __launch_bounds__(kSortThreads) scatter_kernel(
     const __grid_constant__ PassArgs a) {
   __shared__ RankSmem s;
-  uint32_t key[kTileItems], at[kTileItems], digit[kTileItems], rank[kTileItems];
-  load_tile<ID>(a, key, at, digit);
+  Place x[kTileItems];
+  uint32_t digit[kTileItems], rank[kTileItems];
+  load_tile<ID>(a, x, digit);
   rank_digits<kTileItems>(s, digit, rank);
   uint32_t all = 0, mine = 0;
   if (threadIdx.x < kDigits) {
@@ -664,10 +780,7 @@ __global__ void __launch_bounds__(kSortThreads) scatter_kernel(
 #pragma unroll
   for (int j = 0; j < kTileItems; ++j) {
     const uint32_t to = s.base[digit[j]] + s.warp_count[warp][digit[j]] + rank[j];
-    if (to < a.s.n) {
-      a.keys_out[to] = key[j];
-      a.pos_out[to] = at[j];
-    }
+    if (to < a.s.n) a.out[to] = x[j];
   }
 }
 
@@ -723,35 +836,18 @@ int check_ids(const void* ids, int32_t ids_dtype, int64_t n_ids, int64_t first_r
 
 void (*const embed_kernels[3][3][2])(EmbedArgs) = PICK(embed_kernel);
 
-// sum_kernel by the type of dy and the shape of a lane's columns.
+// sum_kernel by the type of dy, the columns a lane holds and the alignment.
 using SumKernel = void (*)(GradArgs);
-#define SUM_SHAPES(in)                                                                     \
-  {sum_kernel<in, 8, 1>, sum_kernel<in, 4, 2>, sum_kernel<in, 2, 4>, sum_kernel<in, 1, 8>, \
-   sum_kernel<in, 4, 1>, sum_kernel<in, 2, 1>, sum_kernel<in, 1, 1>}
-const SumKernel sum_kernels[3][7] = {SUM_SHAPES(TRAIN_BF16), SUM_SHAPES(TRAIN_FP16),
-                                     SUM_SHAPES(TRAIN_FP32)};
-const int kShapeVec[7] = {8, 4, 2, 1, 4, 2, 1};
-const int kShapeCols[7] = {8, 8, 8, 8, 4, 2, 1};
+const SumKernel sum_kernels[3][2][2] = {
+    {{sum_kernel<TRAIN_BF16, 8, false>, sum_kernel<TRAIN_BF16, 8, true>},
+     {sum_kernel<TRAIN_BF16, 16, false>, sum_kernel<TRAIN_BF16, 16, true>}},
+    {{sum_kernel<TRAIN_FP16, 8, false>, sum_kernel<TRAIN_FP16, 8, true>},
+     {sum_kernel<TRAIN_FP16, 16, false>, sum_kernel<TRAIN_FP16, 16, true>}},
+    {{sum_kernel<TRAIN_FP32, 8, false>, sum_kernel<TRAIN_FP32, 8, true>}, {nullptr, nullptr}}};
 
-// Where a lane's loads are as wide as the alignment lets them be, and a warp
-// covers no more than twice the columns there are.
-int pick_shape(int vec, int64_t dim) {
-  if (vec >= 4 && dim > 64 && dim <= 128) return 4;
-  if (vec >= 2 && dim > 32 && dim <= 64) return 5;
-  if (dim <= 32) return 6;
-  return vec == 8 ? 0 : vec == 4 ? 1 : vec == 2 ? 2 : 3;
-}
-
-// The widest of 8, 4, 2 and 1 neighbouring elements that every row can be
-// cut into, each piece aligned to its size or to 16 bytes.
-int vector_width(const void* p, int32_t dtype, int64_t dim, int64_t stride) {
-  for (int v = 8; v > 1; v /= 2) {
-    const int bytes = v * size_of(dtype) < 16 ? v * size_of(dtype) : 16;
-    if (dim % v == 0 && reinterpret_cast<uintptr_t>(p) % uintptr_t(bytes) == 0 &&
-        (stride * size_of(dtype)) % bytes == 0)
-      return v;
-  }
-  return 1;
+// Every row starts at a multiple of 16 bytes.
+bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size_of(dtype) % 16 == 0;
 }
 
 constexpr int64_t kClusterCapacity = 8 * kSortThreads * 16;
@@ -759,15 +855,14 @@ constexpr int64_t kClusterCapacity = 8 * kSortThreads * 16;
 // How the gradient's work is cut; depends on the sizes alone.
 struct GradPlan {
   int64_t block, n_blocks, slot_dim, tiles;
-  int64_t keys, pos, keys2, pos2, counts, totals, slots, bytes;  // offsets in the workspace
+  int64_t places, places2, counts, totals, slots, bytes;  // offsets in the workspace
 };
 
-GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
+GradPlan grad_plan(int64_t n, int64_t dim) {
   GradPlan p{};
-  (void)n_rows;
-  // Blocks of 64 positions where they make work for 4096 warps, else 32, else 16.
-  const int64_t slabs = (dim + 255) / 256;
-  p.block = 64;
+  // Blocks of 128 positions where they make work for 4096 warps, else fewer.
+  const int64_t slabs = (dim + 511) / 512;
+  p.block = kMaxBlock;
   while (p.block > 16 && n / p.block * slabs < 4096) p.block /= 2;
   p.n_blocks = (n + p.block - 1) / p.block;
   p.slot_dim = (dim + 7) / 8 * 8;
@@ -777,12 +872,10 @@ GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
     at += (bytes + 255) / 256 * 256;
     return here;
   };
-  p.keys = take(4 * n);
-  p.pos = take(4 * n);
+  p.places = take(int64_t(sizeof(Place)) * n);
   if (n > kClusterCapacity) {
     p.tiles = (n + kGlobalTile - 1) / kGlobalTile;
-    p.keys2 = take(4 * n);
-    p.pos2 = take(4 * n);
+    p.places2 = take(int64_t(sizeof(Place)) * n);
     p.counts = take(4 * kDigits * p.tiles);
     p.totals = take(4 * kDigits);
   }
@@ -839,12 +932,15 @@ cudaError_t launch_cluster_sort(const SortArgs& a, cudaStream_t s) {
 
 template <class ID>
 cudaError_t launch_sort(const SortArgs& a, const GradPlan& p, char* ws, cudaStream_t s) {
+  // As many CTAs as the cluster takes, so that each has few elements to rank
+  // and to scatter.
+  if (a.n <= 8 * kSortThreads) return launch_cluster_sort<1, ID>(a, s);
+  if (a.n <= 8 * kSortThreads * 2) return launch_cluster_sort<2, ID>(a, s);
   if (a.n <= 8 * kSortThreads * 4) return launch_cluster_sort<4, ID>(a, s);
   if (a.n <= 8 * kSortThreads * 8) return launch_cluster_sort<8, ID>(a, s);
   if (a.n <= kClusterCapacity) return launch_cluster_sort<16, ID>(a, s);
-  // The last pass writes to keys and pos.
-  uint32_t* k[2] = {a.keys, reinterpret_cast<uint32_t*>(ws + p.keys2)};
-  uint32_t* q[2] = {a.pos, reinterpret_cast<uint32_t*>(ws + p.pos2)};
+  // The last pass writes to places.
+  Place* q[2] = {a.places, reinterpret_cast<Place*>(ws + p.places2)};
   PassArgs b{};
   b.s = a;
   b.counts = reinterpret_cast<uint32_t*>(ws + p.counts);
@@ -853,10 +949,8 @@ cudaError_t launch_sort(const SortArgs& a, const GradPlan& p, char* ws, cudaStre
   b.width = (a.bits + a.passes - 1) / a.passes;
   for (int i = 0; i < a.passes; ++i) {
     const int to = (a.passes - 1 - i) & 1;
-    b.keys_in = i == 0 ? nullptr : k[to ^ 1];
-    b.pos_in = i == 0 ? nullptr : q[to ^ 1];
-    b.keys_out = k[to];
-    b.pos_out = q[to];
+    b.in = i == 0 ? nullptr : q[to ^ 1];
+    b.out = q[to];
     b.shift = i * b.width;
     const dim3 grid{unsigned(p.tiles)};
     cudaError_t ce = launch(count_kernel<ID>, grid, kSortThreads, 0, s, false, 1, b);
@@ -897,7 +991,7 @@ LAMB_API int train_embed_grad_workspace(int64_t n_ids, int64_t n_rows, int64_t d
   if (n_ids < 0 || n_rows < 0 || dim < 0 || n_ids > kMaxCount || n_rows > kMaxCount ||
       dim > kMaxCount)
     return fail(LAMB_ERR_INVALID, "sizes must be in [0, 2^31 - 1]");
-  *bytes = grad_plan(n_ids, n_rows, dim).bytes;
+  *bytes = grad_plan(n_ids, dim).bytes;
   return LAMB_OK;
 }
 
@@ -923,15 +1017,17 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
   if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16)
     return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
   if (n_rows == 0 || dim == 0 || (accumulate && n_ids == 0)) return LAMB_OK;
-  const GradPlan p = grad_plan(n_ids, n_rows, dim);
+  const GradPlan p = grad_plan(n_ids, dim);
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t ce = cudaSuccess;
   GradArgs a{};
   a.dy = grad_out;
   a.grad = grad;
-  a.keys = reinterpret_cast<const uint32_t*>(ws + p.keys);
-  a.pos = reinterpret_cast<const uint32_t*>(ws + p.pos);
+  a.ids = ids;
+  a.first_row = first_row;
+  a.padding = padding_id;
+  a.places = reinterpret_cast<const Place*>(ws + p.places);
   a.slots = reinterpret_cast<float*>(ws + p.slots);
   a.dy_stride = grad_out_stride;
   a.grad_stride = grad_stride;
@@ -951,8 +1047,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     t.first_row = first_row;
     t.n_rows = n_rows;
     t.padding = padding_id;
-    t.keys = reinterpret_cast<uint32_t*>(ws + p.keys);
-    t.pos = reinterpret_cast<uint32_t*>(ws + p.pos);
+    t.places = reinterpret_cast<Place*>(ws + p.places);
     while ((n_rows >> t.bits) != 0) ++t.bits;  // the largest key is n_rows
     t.passes = (t.bits + 7) / 8;
     ce = ids_dtype == TRAIN_INT64 ? launch_sort<int64_t>(t, p, ws, s)
@@ -960,23 +1055,40 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     if (ce != cudaSuccess)
       return fail(LAMB_ERR_CUDA, std::string("sorting the tokens: ") + cudaGetErrorString(ce));
   }
-  const int vec_dy = vector_width(grad_out, grad_out_dtype, dim, grad_out_stride);
-  const int vec_grad = vector_width(grad, grad_dtype, dim, grad_stride);
-  const int shape = pick_shape(n_ids > 0 && vec_dy < vec_grad ? vec_dy : vec_grad, dim);
-  a.slabs = int32_t((dim + kWarp * kShapeCols[shape] - 1) / (kWarp * kShapeCols[shape]));
-  a.sum_units = p.n_blocks * a.slabs;
-  a.fill_units = accumulate ? 0 : (n_rows + kWarp - 1) / kWarp;
-  const int64_t warps = kThreads / kWarp;
-  const int64_t ctas = (a.sum_units + a.fill_units + warps - 1) / warps;
-  if (ctas > kMaxCount) return fail(LAMB_ERR_INVALID, "n_ids * dim is too large");
-  ce = launch(sum_kernels[grad_out_dtype][shape], dim3(unsigned(ctas)), kThreads, 0, s,
-              n_ids > 0 && n_ids <= kClusterCapacity, 1, a);
+  if (!accumulate) {
+    // Ids are read by every CTA, which the sort hides, unless there are too
+    // many of them or of the CTAs.
+    int64_t ctas = 304;
+    while (n_rows > ctas * kFillRows) ctas *= 2;
+    if (ctas > n_rows) ctas = n_rows;
+    a.rows_per_cta = (n_rows + ctas - 1) / ctas;
+    ctas = (n_rows + a.rows_per_cta - 1) / a.rows_per_cta;  // none without rows
+    const bool scan = n_ids <= kClusterCapacity && ctas <= 304;
+    const auto kernel = !scan ? fill_kernel<false, int32_t>
+                        : ids_dtype == TRAIN_INT64 ? fill_kernel<true, int64_t>
+                                                   : fill_kernel<true, int32_t>;
+    ce = launch(kernel, dim3(unsigned(ctas)), kFillThreads, 0, s, n_ids > 0, 1, a);
+  }
+  if (ce == cudaSuccess && n_ids > 0) {
+    const bool wide = grad_out_dtype == TRAIN_FP32 || (accumulate && grad_dtype == TRAIN_FP32);
+    const bool aligned = dim % 8 == 0 &&
+                         rows_aligned16(grad_out, grad_out_dtype, grad_out_stride) &&
+                         rows_aligned16(grad, grad_dtype, grad_stride);
+    const int64_t slab = wide ? 8 * kWarp : 16 * kWarp;
+    a.slabs = int32_t((dim + slab - 1) / slab);
+    a.units = p.n_blocks * a.slabs;
+    const int64_t ctas = (a.units + kSumWarps - 1) / kSumWarps;
+    if (ctas > kMaxCount) return fail(LAMB_ERR_INVALID, "n_ids * dim is too large");
+    const SumKernel kernel = sum_kernels[grad_out_dtype][wide ? 0 : 1][aligned ? 1 : 0];
+    ce = launch(kernel, dim3(unsigned(ctas)), kSumWarps * kWarp, kSumWarps * sizeof(WarpSmem), s,
+                true, 1, a);
+  }
   if (ce == cudaSuccess && n_ids > 2 * p.block) {
-    // A CTA for every 32 columns, and enough in all to fill the GPU.
-    const int64_t x = (dim + kWarp - 1) / kWarp;
-    const int64_t y = x >= 512 ? 1 : 512 / x;
-    ce = launch(join_kernel, dim3(unsigned(x), unsigned(y < p.n_blocks ? y : p.n_blocks)),
-                kJoinWarps * kWarp, 0, s, true, 1, a);
+    // A CTA for every 128 columns, and enough in all to fill the GPU.
+    const int64_t x = (dim + kJoinCols - 1) / kJoinCols;
+    int64_t y = x >= 608 ? 1 : 608 / x;
+    if (y > p.n_blocks / 2) y = p.n_blocks / 2 > 0 ? p.n_blocks / 2 : 1;
+    ce = launch(join_kernel, dim3(unsigned(x), unsigned(y)), kJoinWarps * kWarp, 0, s, true, 1, a);
   }
   return ce == cudaSuccess
              ? LAMB_OK
