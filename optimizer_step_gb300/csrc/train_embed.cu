@@ -64,18 +64,29 @@ struct __align__(8) Place {
   uint32_t key, pos;
 };
 
+// A run that is cut into pieces: the block it starts in, its row, the pieces.
+struct __align__(16) LongRun {
+  uint32_t block, row, pieces, unused;
+};
+
 struct GradArgs {
   const void* dy;
   void* grad;
   const void* ids;
   const Place* places;  // sorted
   float* slots;         // [2 * block + (0: run from an earlier block, 1: starts here)][slot_dim]
-  uint32_t* long_runs;  // [0]: how many, then the blocks they start in, in any order
+  uint32_t* n_long;     // long runs in the list
+  LongRun* long_runs;   // in any order
   int64_t dy_stride, grad_stride, n_rows, dim, slot_dim, first_row, padding;
   int64_t n;
   int64_t n_blocks;
   int64_t units;         // blocks times slabs
-  int64_t rows_per_cta;  // of fill_kernel
+  // Rows that no token names.  A CTA of fill_kernel marks the named ones among
+  // rows_per_cta rows and zeroes the others of the first fill_first of them;
+  // CTAs of sum_kernel zero the rest, fill_each rows a CTA.
+  uint32_t* named;  // a bit a row
+  int64_t rows_per_cta, fill_first, fill_rest, fill_each;
+  uint32_t fill_ctas;    // of sum_kernel
   int32_t block, slabs;  // C, slabs of columns
   float scale;
   int32_t accumulate, out_type;
@@ -184,9 +195,14 @@ __device__ __forceinline__ void warp_zero(char* p, int64_t bytes, int lane) {
     *reinterpret_cast<uint16_t*>(q + i) = 0;
 }
 
-// Zeros the rows that no token names, a range of rows a CTA.  SCAN: the CTA
-// marks its rows by a walk over all ids, so it needs no sorted list and runs
-// while the tokens are being sorted.  Else it looks its rows up in that list.
+// Marks the rows that tokens name and zeroes some of the others, a range of
+// rows a CTA.  SCAN: the CTA finds its rows by a walk over all ids, so it needs
+// no sorted list and runs while the tokens are being sorted.  Else it looks
+// its rows up in that list.
+//
+// What is written alone goes out at 5.4 TB/s on GB300, and written while other
+// rows are read at 6.5 to 6.8; so this kernel zeroes what fits into the time of
+// the sort, and CTAs among those of sum_kernel zero the rest.
 constexpr int kFillThreads = 512;
 constexpr int kFillRows = 4096;  // at most, a CTA
 
@@ -218,11 +234,34 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
     }
   }
   __syncthreads();
-  for (int64_t r = warp; r < count; r += kFillThreads / kWarp)
+  for (int64_t i = threadIdx.x; 32 * i < count; i += kFillThreads)
+    a.named[r0 / 32 + i] = named[i];
+  const int64_t first = min(count, a.fill_first);
+  for (int64_t r = warp; r < first; r += kFillThreads / kWarp)
     if (!((named[r / 32] >> (r & 31)) & 1u))
       warp_zero(grad_at(a, r0 + r, 0), a.dim * size_of(a.out_type), lane);
   // What follows waits for this kernel; it must find the sort finished too.
   if (SCAN) pdl_wait();
+}
+
+// The rows that fill_kernel has left, in a CTA of sum_kernel: fill_each of
+// them, `index` counting from the first.
+__device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / kWarp;
+  const int64_t left = a.rows_per_cta - a.fill_first;
+  const int64_t q1 = min((index + 1) * a.fill_each, a.fill_rest);
+  for (int64_t q0 = index * a.fill_each; q0 < q1; q0 += kWarp) {
+    const int64_t q = q0 + lane;
+    const int64_t row = q / left * a.rows_per_cta + a.fill_first + q % left;
+    const bool idle =
+        q < q1 && row < a.n_rows && !((a.named[row / 32] >> (row & 31)) & 1u);
+    unsigned todo = __ballot_sync(kAll, idle);
+    for (int k = 0; todo; ++k) {
+      const int64_t r = __shfl_sync(kAll, row, __ffs(todo) - 1);
+      todo &= todo - 1;
+      if (k % warps == warp) warp_zero(grad_at(a, r, 0), a.dim * size_of(a.out_type), lane);
+    }
+  }
 }
 
 // The ring of one warp: kStages rows' pieces of a slab in flight.  The copies
@@ -236,7 +275,7 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
 #define KSW 4
 #endif
 #ifndef KMB
-#define KMB 128
+#define KMB 64
 #endif
 #ifndef KU
 #define KU 4096
@@ -264,9 +303,16 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
   constexpr int kSlab = kWarp * COLS;
   const int lane = threadIdx.x & 31;
   WarpSmem& s = reinterpret_cast<WarpSmem*>(raw)[threadIdx.x >> 5];
-  const int64_t unit = int64_t(blockIdx.x) * kSumWarps + (threadIdx.x >> 5);
+  // The CTAs that write zero rows are spread evenly among the others.
+  const uint32_t fill0 = uint32_t(uint64_t(blockIdx.x) * a.fill_ctas / gridDim.x);
+  const uint32_t fill1 = uint32_t((uint64_t(blockIdx.x) + 1) * a.fill_ctas / gridDim.x);
+  const int64_t unit = int64_t(blockIdx.x - fill0) * kSumWarps + (threadIdx.x >> 5);
   pdl_trigger();
   pdl_wait();
+  if (fill1 != fill0) {
+    fill_rest(a, fill0);
+    return;
+  }
   if (unit >= a.units) return;
   const int64_t b = unit / a.slabs;
   const int64_t col0 = (unit % a.slabs) * kSlab;
@@ -468,8 +514,17 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
   }
   // What is left in the registers is a piece of a run that goes on.
   if (!ends(stop - 1)) write_slot(is_head(s.key[stop - 1]) ? 0 : 1);
-  if (tail_piece && col0 == 0 && lane == 0)
-    a.long_runs[1 + atomicAdd(a.long_runs, 1u)] = uint32_t(b);
+  if (tail_piece && col0 == 0) {
+    // The run covers the start of every block it has a piece in but its first.
+    uint32_t pieces = 1;
+    for (int64_t q = b + 1;; q += kWarp) {
+      const int64_t i = (q + lane) * C;
+      const int more = __popc(__ballot_sync(kAll, i < n && a.places[i < n ? i : 0].key == last));
+      pieces += more;
+      if (more < kWarp) break;
+    }
+    if (lane == 0) a.long_runs[atomicAdd(a.n_long, 1u)] = LongRun{uint32_t(b), last, pieces, 0u};
+  }
 }
 
 // Adds the pieces of every long run, in order.  A CTA takes a slab of 128
@@ -481,23 +536,13 @@ constexpr int kJoinCols = 128;
 __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(
     const __grid_constant__ GradArgs a) {
   __shared__ float4 part[kJoinWarps][kWarp];
-  constexpr int kThreads = kJoinWarps * kWarp;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = int64_t(blockIdx.x) * kJoinCols + 4 * lane;  // slots: whole groups of 8
-  const int64_t C = a.block, n = a.n;
   pdl_wait();
-  const uint32_t runs = *a.long_runs;
+  const uint32_t runs = *a.n_long;
   for (uint32_t k = blockIdx.y; k < runs; k += gridDim.y) {
-    const int64_t from = a.long_runs[1 + k];
-    const uint32_t row = a.places[(from + 1) * C - 1].key;
-    // The run covers the start of every block it has a piece in but its first.
-    int64_t pieces = 1;
-    for (int64_t q = from + 1;; q += kThreads) {
-      const int64_t at = (q + threadIdx.x) * C;
-      const int more = __syncthreads_count(at < n && a.places[at < n ? at : 0].key == row);
-      pieces += more;
-      if (more < kThreads) break;
-    }
+    const LongRun run = a.long_runs[k];
+    const int64_t from = run.block, pieces = run.pieces;
     int64_t share = (pieces + kJoinWarps - 1) / kJoinWarps;
     if (share < 8) share = 8;
     const int64_t p0 = warp * share, p1 = min(p0 + share, pieces);
@@ -521,7 +566,7 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (col + i < a.dim) {
-          char* g = grad_at(a, row, col + i);
+          char* g = grad_at(a, run.row, col + i);
           const float old = a.accumulate ? load1(g, a.out_type) : 0.0f;
           store1(g, a.out_type, a.accumulate ? fmaf(a.scale, x[i], old) : a.scale * x[i]);
         }
@@ -543,7 +588,7 @@ struct SortArgs {
   const void* ids;
   int64_t n, first_row, n_rows, padding;
   Place* places;        // the result
-  uint32_t* long_runs;  // the first kernel clears its count
+  uint32_t* n_long;     // the first kernel clears it
   int32_t bits, passes;  // of the keys; digits of (bits + passes - 1) / passes bits
 };
 
@@ -649,7 +694,7 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
   const int me = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_trigger();
-  if (me == 0 && threadIdx.x == 0) *a.long_runs = 0u;
+  if (me == 0 && threadIdx.x == 0) *a.n_long = 0u;
   const int width = (a.bits + a.passes - 1) / a.passes;
   const uint32_t mask = (1u << width) - 1u;
   const int local0 = warp * (kWarp * ITEMS) + lane;
@@ -736,7 +781,7 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_consta
   __shared__ RankSmem s;
   Place x[kTileItems];
   uint32_t digit[kTileItems], rank[kTileItems];
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.s.long_runs = 0u;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.s.n_long = 0u;
   load_tile<ID>(a, x, digit);
   rank_digits<kTileItems>(s, digit, rank);
   __syncthreads();
@@ -859,15 +904,21 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size_of(dtype) % 16 == 0;
 }
 
+// Zeros written while the tokens are being sorted.
+#ifndef KFB
+#define KFB 48e6
+#endif
+constexpr double kFillBytes = KFB;
+
 constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
 
 // How the gradient's work is cut; depends on the sizes alone.
 struct GradPlan {
   int64_t block, n_blocks, slot_dim, tiles;
-  int64_t places, places2, counts, totals, long_runs, slots, bytes;  // offsets in the workspace
+  int64_t places, places2, counts, totals, n_long, long_runs, named, slots, bytes;  // in the workspace
 };
 
-GradPlan grad_plan(int64_t n, int64_t dim) {
+GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
   GradPlan p{};
   // Blocks of 128 positions where they make work for 4096 warps, else fewer.
   const int64_t slabs = (dim + 511) / 512;
@@ -888,7 +939,9 @@ GradPlan grad_plan(int64_t n, int64_t dim) {
     p.counts = take(4 * kDigits * p.tiles);
     p.totals = take(4 * kDigits);
   }
-  p.long_runs = take(4 * (1 + p.n_blocks));
+  p.n_long = take(4);
+  p.long_runs = take(int64_t(sizeof(LongRun)) * (p.n_blocks / 2 + 1));
+  p.named = take(4 * ((n_rows + 31) / 32));
   p.slots = at;
   if (n > 2 * p.block) take(2 * p.n_blocks * p.slot_dim * 4);
   p.bytes = at;
@@ -1002,7 +1055,7 @@ LAMB_API int train_embed_grad_workspace(int64_t n_ids, int64_t n_rows, int64_t d
   if (n_ids < 0 || n_rows < 0 || dim < 0 || n_ids > kMaxCount || n_rows > kMaxCount ||
       dim > kMaxCount)
     return fail(LAMB_ERR_INVALID, "sizes must be in [0, 2^31 - 1]");
-  *bytes = grad_plan(n_ids, dim).bytes;
+  *bytes = grad_plan(n_ids, n_rows, dim).bytes;
   return LAMB_OK;
 }
 
@@ -1028,7 +1081,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
   if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16)
     return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
   if (n_rows == 0 || dim == 0 || (accumulate && n_ids == 0)) return LAMB_OK;
-  const GradPlan p = grad_plan(n_ids, dim);
+  const GradPlan p = grad_plan(n_ids, n_rows, dim);
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t ce = cudaSuccess;
@@ -1040,7 +1093,9 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
   a.padding = padding_id;
   a.places = reinterpret_cast<const Place*>(ws + p.places);
   a.slots = reinterpret_cast<float*>(ws + p.slots);
-  a.long_runs = reinterpret_cast<uint32_t*>(ws + p.long_runs);
+  a.n_long = reinterpret_cast<uint32_t*>(ws + p.n_long);
+  a.long_runs = reinterpret_cast<LongRun*>(ws + p.long_runs);
+  a.named = reinterpret_cast<uint32_t*>(ws + p.named);
   a.dy_stride = grad_out_stride;
   a.grad_stride = grad_stride;
   a.n_rows = n_rows;
@@ -1060,7 +1115,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     t.n_rows = n_rows;
     t.padding = padding_id;
     t.places = reinterpret_cast<Place*>(ws + p.places);
-    t.long_runs = reinterpret_cast<uint32_t*>(ws + p.long_runs);
+    t.n_long = reinterpret_cast<uint32_t*>(ws + p.n_long);
     while ((n_rows >> t.bits) != 0) ++t.bits;  // the largest key is n_rows
     t.passes = (t.bits + 7) / 8;
     ce = ids_dtype == TRAIN_INT64 ? launch_sort<int64_t>(t, p, ws, s)
@@ -1073,10 +1128,22 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     // many of them or of the CTAs.
     int64_t ctas = 304;
     while (n_rows > ctas * kFillRows) ctas *= 2;
-    if (ctas > n_rows) ctas = n_rows;
-    a.rows_per_cta = (n_rows + ctas - 1) / ctas;
-    ctas = (n_rows + a.rows_per_cta - 1) / a.rows_per_cta;  // none without rows
+    a.rows_per_cta = ((n_rows + ctas - 1) / ctas + 31) / 32 * 32;
+    ctas = (n_rows + a.rows_per_cta - 1) / a.rows_per_cta;
     const bool scan = n_ids <= kClusterCapacity && ctas <= 304;
+    a.fill_first = a.rows_per_cta;
+    if (scan && n_ids > 0) {
+      // What is written while the tokens are sorted; the rest among the sums.
+      const double row_bytes = double(dim) * size_of(grad_dtype);
+      const double part = kFillBytes / (double(n_rows) * row_bytes);
+      if (part < 1.0) a.fill_first = int64_t(part * double(a.rows_per_cta));
+      const int64_t most = int64_t(512e3 / row_bytes) + 1;  // of one CTA
+      if (a.fill_first > most) a.fill_first = most;
+      if (a.fill_first > a.rows_per_cta) a.fill_first = a.rows_per_cta;
+      a.fill_rest = ctas * (a.rows_per_cta - a.fill_first);
+      a.fill_each = int64_t(64e3 / row_bytes) + 1;
+      a.fill_ctas = uint32_t((a.fill_rest + a.fill_each - 1) / a.fill_each);
+    }
     const auto kernel = !scan ? fill_kernel<false, int32_t>
                         : ids_dtype == TRAIN_INT64 ? fill_kernel<true, int64_t>
                                                    : fill_kernel<true, int32_t>;
@@ -1090,7 +1157,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     const int64_t slab = wide ? 8 * kWarp : 16 * kWarp;
     a.slabs = int32_t((dim + slab - 1) / slab);
     a.units = p.n_blocks * a.slabs;
-    const int64_t ctas = (a.units + kSumWarps - 1) / kSumWarps;
+    const int64_t ctas = (a.units + kSumWarps - 1) / kSumWarps + a.fill_ctas;
     if (ctas > kMaxCount) return fail(LAMB_ERR_INVALID, "n_ids * dim is too large");
     const SumKernel kernel = sum_kernels[grad_out_dtype][wide ? 0 : 1][aligned ? 1 : 0];
     ce = launch(kernel, dim3(unsigned(ctas)), kSumWarps * kWarp, kSumWarps * sizeof(WarpSmem), s,
@@ -1099,7 +1166,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
   if (ce == cudaSuccess && n_ids > 2 * p.block) {
     // A CTA for every 128 columns, and enough in all to fill the GPU.
     const int64_t x = (dim + kJoinCols - 1) / kJoinCols;
-    int64_t y = x >= 608 ? 1 : 608 / x;
+    int64_t y = x >= 1216 ? 1 : 1216 / x;
     if (y > p.n_blocks / 2) y = p.n_blocks / 2 > 0 ? p.n_blocks / 2 : 1;
     ce = launch(join_kernel, dim3(unsigned(x), unsigned(y)), kJoinWarps * kWarp, 0, s, true, 1, a);
   }
