@@ -13,23 +13,33 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int64_t kMaxItem = 16384;
+// Bytes of grads in one piece of work: eight 16-byte loads a thread.
+constexpr int kLoads = 8;
+constexpr int64_t kItemBytes = kThreads * kLoads * 16;
+#ifndef KNORM
+#define KNORM 6
+#endif
+constexpr int kNormCtas = KNORM;  // per SM
 
 // One piece of a tensor: count elements from src, written to dst.
-struct Item {
+struct __align__(32) Item {
   const void* src;
   void* dst;
   int32_t count;
-  int16_t in, out;  // element types
+  int8_t in, out;  // element types
+  // Elements before the first 16-byte boundary of src, and whether dst is
+  // aligned too there (to the 16 bytes or less that a thread writes at a time).
+  int8_t head;
+  int8_t aligned;
+  int64_t unused;
 };
 
 // What the kernels of one call leave for one another.
 struct Scalars {
-  double sum;        // sum of g^2
-  float factor;      // c / S, 0 when a grad is not finite
-  uint32_t bad;      // a grad is inf or NaN
-  uint32_t ticket;   // CTAs of the norm kernel that have finished
-  uint32_t flag;     // OR of the CTAs' inf/NaN flags
+  float factor;     // c / S, 0 when a grad is not finite
+  uint32_t bad;     // a grad is inf or NaN
+  uint32_t ticket;  // CTAs of the norm kernel that have finished
+  uint32_t flag;    // OR of the CTAs' inf/NaN flags
 };
 
 struct Tables {
@@ -38,6 +48,13 @@ struct Tables {
   Scalars* sc;
   int64_t n_items;
 };
+
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 __device__ __forceinline__ double warp_sum(double x) {
 #pragma unroll
@@ -57,48 +74,146 @@ __device__ __forceinline__ double block_sum(double x, double* red) {
   return y;
 }
 
-__device__ __forceinline__ float load_any(const Item& it, int64_t i) {
-  if (it.in == TRAIN_FP32) return static_cast<const float*>(it.src)[i];
-  const uint16_t x = static_cast<const uint16_t*>(it.src)[i];
-  return it.in == TRAIN_BF16 ? to_float<TRAIN_BF16>(x) : to_float<TRAIN_FP16>(x);
+template <int DT>
+__device__ __forceinline__ float2 decode2(uint32_t w) {
+  if constexpr (DT == TRAIN_BF16)
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return make_float2(to_float<TRAIN_FP16>(uint16_t(w & 0xffffu)),
+                     to_float<TRAIN_FP16>(uint16_t(w >> 16)));
 }
 
-__device__ __forceinline__ void store_any(const Item& it, int64_t i, float x) {
-  if (it.out == TRAIN_FP32) static_cast<float*>(it.dst)[i] = x;
-  else if (it.out == TRAIN_BF16) static_cast<uint16_t*>(it.dst)[i] = from_float<TRAIN_BF16>(x);
-  else static_cast<uint16_t*>(it.dst)[i] = from_float<TRAIN_FP16>(x);
+struct Squares {
+  double sum;
+  uint32_t bad;
+};
+
+// The squares of one value, exactly enough for any finite one.
+__device__ __forceinline__ void add_square(Squares& s, float x) {
+  if (isfinite(x)) s.sum = fma(double(x), double(x), s.sum);
+  else s.bad = 1u;
 }
 
-// Forms the norm, the factor and the flag from the sum (one thread).
-__device__ void publish(Scalars* sc, float* stats, double sum, bool bad, float max_norm,
-                        float loss_scale) {
+// The squares of a thread's vectors (v, v + kThreads, ... below end) in fp64,
+// and whether one is inf or NaN.  The rare path: not inlined, and the values
+// are read again, so that the fast path carries neither fp64 code nor words
+// kept for it.
+template <int DT>
+__device__ __noinline__ Squares squares_fp64(const char* base, int v, int end) {
+  Squares s{0.0, 0u};
+  for (int u = 0; u < kLoads; ++u, v += kThreads) {
+    if (v >= end) break;
+    for (int i = 0; i < 16 / size_of(DT); ++i)
+      add_square(s, to_float<DT>(reinterpret_cast<const typename TypeOf<DT>::T*>(
+                        base + int64_t(v) * 16)[i]));
+  }
+  return s;
+}
+
+// A thread's share of the squares of one item.  They are summed in fp32, at
+// most 64 of them, and from there in fp64.  bf16 and fp32 grads span fp32's
+// exponents, so their squares may leave its range: a sum outside [2^-90,
+// 2^120] (some value not zero) is taken again in fp64.  Inside that range
+// nothing overflowed, and what underflowed weighs at most 2^-30 of the sum.
+// An inf or NaN makes its sum inf or NaN, which is never inside the range, so
+// the fast path does not test for them.  fp16 squares never leave it.
+template <int DT>
+__device__ __forceinline__ void item_squares(const Item& it, double& acc, uint32_t& bad) {
+  using T = typename TypeOf<DT>::T;
+  constexpr int kPer = 16 / size_of(DT);
+  const int head = it.head;
+  const int vecs = (it.count - head) / kPer;
+  const char* base = static_cast<const char*>(it.src) + head * size_of(DT);
+  const int v = threadIdx.x;
+  uint4 q[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    q[u] = make_uint4(0u, 0u, 0u, 0u);
+    if (v + u * kThreads < vecs)
+      q[u] = __ldg(reinterpret_cast<const uint4*>(base) + v + u * kThreads);
+  }
+  // What the 16-byte loads leave: up to 7 elements in front and behind.
+  const int rest = it.count - vecs * kPer;
+  if (threadIdx.x < rest) {
+    const int i = threadIdx.x < head ? int(threadIdx.x) : vecs * kPer + int(threadIdx.x);
+    Squares s{0.0, 0u};
+    add_square(s, to_float<DT>(static_cast<const T*>(it.src)[i]));
+    acc += s.sum;
+    bad |= s.bad;
+  }
+  float a = 0.0f, b = 0.0f;
+  uint32_t any = 0u;
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == TRAIN_FP32) {
+        const float x = __uint_as_float(w[i]);
+        if (i & 1) a = fmaf(x, x, a);
+        else b = fmaf(x, x, b);
+      } else {
+        const float2 x = decode2<DT>(w[i]);
+        a = fmaf(x.x, x.x, a);
+        b = fmaf(x.y, x.y, b);
+      }
+      if constexpr (DT != TRAIN_FP16) any |= w[i];
+    }
+  }
+  a += b;
+  any &= DT == TRAIN_FP32 ? 0x7fffffffu : 0x7fff7fffu;
+  if constexpr (DT == TRAIN_FP16) {
+    if (a <= 0x1p120f) acc += double(a);
+    else bad = 1u;
+  } else {
+    if (a <= 0x1p120f && (a >= 0x1p-90f || any == 0u)) {
+      acc += double(a);
+    } else {
+      const Squares s = squares_fp64<DT>(base, v, vecs);
+      acc += s.sum;
+      bad |= s.bad;
+    }
+  }
+}
+
+// Forms the norm, the factor and the flag from the sum.  Called by a warp: an
+// fp64 division costs about half a microsecond, so three lanes take one each.
+__device__ __forceinline__ void publish(Scalars* sc, float* stats, double sum, bool bad,
+                                        float max_norm, float loss_scale) {
+  const int lane = threadIdx.x & 31;
   const double root = sqrt(sum);
-  const double norm = root / double(loss_scale);
-  double factor = 1.0 / double(loss_scale);
-  if (max_norm > 0.0f && norm > double(max_norm)) factor = double(max_norm) / root;
+  const double top = lane == 0 ? root : lane == 1 ? double(max_norm) : 1.0;
+  const double q = top / (lane == 1 ? root : double(loss_scale));
+  const double norm = __shfl_sync(0xffffffffu, q, 0);
+  const double clipped = __shfl_sync(0xffffffffu, q, 1);  // max_norm / G / S
+  const double plain = __shfl_sync(0xffffffffu, q, 2);
+  if (lane != 0) return;
+  const double factor = max_norm > 0.0f && norm > double(max_norm) ? clipped : plain;
   sc->factor = bad ? 0.0f : float(factor);
   sc->bad = bad;
   stats[0] = bad ? __int_as_float(0x7f800000) : float(norm);
-  stats[1] = sc->factor;
+  stats[1] = bad ? 0.0f : float(factor);
   stats[2] = bad ? 1.0f : 0.0f;
 }
 
-// Sum of squares: each CTA walks its items; the last one to finish adds the
-// CTAs' sums in order and publishes.
+// Sum of squares: each CTA walks every gridDim.x-th item, all of them through
+// memory side by side; the last one to finish adds the CTAs' sums in order and
+// publishes.
 __global__ void __launch_bounds__(kThreads) norm_kernel(Tables T, float max_norm,
                                                         float loss_scale, float* stats,
                                                         double* exchange) {
   __shared__ double red[kWarps];
-  __shared__ uint32_t last;
+  __shared__ uint32_t last, any;
+  pdl_trigger();
   double acc = 0.0;
-  int bad = 0;
+  uint32_t bad = 0;
+  Item next{};
+  if (blockIdx.x < T.n_items) next = T.items[blockIdx.x];
   for (int64_t k = blockIdx.x; k < T.n_items; k += gridDim.x) {
-    const Item it = T.items[k];
-    for (int i = threadIdx.x; i < it.count; i += kThreads) {
-      const float x = load_any(it, i);
-      bad |= !isfinite(x);
-      acc += double(x) * double(x);
-    }
+    const Item it = next;
+    if (k + gridDim.x < T.n_items) next = T.items[k + gridDim.x];
+    if (it.in == TRAIN_BF16) item_squares<TRAIN_BF16>(it, acc, bad);
+    else if (it.in == TRAIN_FP32) item_squares<TRAIN_FP32>(it, acc, bad);
+    else item_squares<TRAIN_FP16>(it, acc, bad);
   }
   const double s = block_sum(acc, red);
   bad = __syncthreads_or(bad);
@@ -115,31 +230,116 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(Tables T, float max_norm
   for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) sum += __ldcg(&T.partial[i]);
   sum = block_sum(sum, red);
   if (threadIdx.x == 0) {
-    const bool any = atomicExch(&T.sc->flag, 0u) != 0;
+    any = atomicExch(&T.sc->flag, 0u);
     T.sc->ticket = 0;
     if (exchange) {
       exchange[0] = any ? 0.0 : sum;
       exchange[1] = any ? 1.0 : 0.0;
+    }
+  }
+  __syncthreads();
+  if (!exchange && threadIdx.x < 32) publish(T.sc, stats, sum, any != 0, max_norm, loss_scale);
+}
+
+__global__ void __launch_bounds__(32) finish_kernel(Tables T, const double* exchange,
+                                                    float max_norm, float loss_scale,
+                                                    float* stats) {
+  pdl_trigger();
+  publish(T.sc, stats, exchange[0], !(exchange[1] == 0.0), max_norm, loss_scale);
+}
+
+template <int IN>
+__device__ __forceinline__ float load_value(const Item& it, int i) {
+  return to_float<IN>(static_cast<const typename TypeOf<IN>::T*>(it.src)[i]);
+}
+template <int OUT>
+__device__ __forceinline__ void store_value(const Item& it, int i, float x) {
+  static_cast<typename TypeOf<OUT>::T*>(it.dst)[i] = from_float<OUT>(x);
+}
+
+// factor * src into dst: 16 bytes of src a thread and load, coalesced on both
+// sides, or element by element where src and dst are aligned differently.
+template <int IN, int OUT>
+__device__ __forceinline__ void item_scale(const Item& it, float factor) {
+  using TO = typename TypeOf<OUT>::T;
+  constexpr int kPer = 16 / size_of(IN);
+  if (!it.aligned) {
+#pragma unroll 8
+    for (int i = threadIdx.x; i < it.count; i += kThreads)
+      store_value<OUT>(it, i, factor * load_value<IN>(it, i));
+    return;
+  }
+  const int head = it.head;
+  const int vecs = (it.count - head) / kPer;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(it.src) +
+                                                    head * size_of(IN));
+  TO* dst = static_cast<TO*>(it.dst) + head;
+  uint4 q[kLoads];
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u)
+    if (int(threadIdx.x) + u * kThreads < vecs) q[u] = src[threadIdx.x + u * kThreads];
+  const int rest = it.count - vecs * kPer;
+  if (threadIdx.x < rest) {
+    const int i = threadIdx.x < head ? int(threadIdx.x) : vecs * kPer + int(threadIdx.x);
+    store_value<OUT>(it, i, factor * load_value<IN>(it, i));
+  }
+#pragma unroll
+  for (int u = 0; u < kLoads; ++u) {
+    const int v = threadIdx.x + u * kThreads;
+    if (v >= vecs) break;
+    const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+    float x[kPer];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (IN == TRAIN_FP32) {
+        x[i] = factor * __uint_as_float(w[i]);
+      } else {
+        const float2 d = decode2<IN>(w[i]);
+        x[2 * i] = factor * d.x;
+        x[2 * i + 1] = factor * d.y;
+      }
+    }
+    if constexpr (OUT == TRAIN_FP32) {
+#pragma unroll
+      for (int i = 0; i < kPer; i += 4)
+        reinterpret_cast<float4*>(dst + int64_t(v) * kPer)[i / 4] =
+            make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
     } else {
-      publish(T.sc, stats, sum, any, max_norm, loss_scale);
+      uint32_t y[kPer / 2];
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i)
+        y[i] = uint32_t(from_float<OUT>(x[2 * i])) | uint32_t(from_float<OUT>(x[2 * i + 1])) << 16;
+      if constexpr (kPer == 8)
+        *reinterpret_cast<uint4*>(dst + int64_t(v) * kPer) = make_uint4(y[0], y[1], y[2], y[3]);
+      else
+        *reinterpret_cast<uint2*>(dst + int64_t(v) * kPer) = make_uint2(y[0], y[1]);
     }
   }
 }
 
-__global__ void finish_kernel(Tables T, const double* exchange, float max_norm, float loss_scale,
-                              float* stats) {
-  publish(T.sc, stats, exchange[0], !(exchange[1] == 0.0), max_norm, loss_scale);
+template <int IN>
+__device__ __forceinline__ void item_scale_to(const Item& it, float factor) {
+  if (it.out == TRAIN_BF16) item_scale<IN, TRAIN_BF16>(it, factor);
+  else if (it.out == TRAIN_FP32) item_scale<IN, TRAIN_FP32>(it, factor);
+  else item_scale<IN, TRAIN_FP16>(it, factor);
 }
 
+// One item a CTA, so that the CTAs go through memory in the order they are
+// launched: on GB300 a copy runs at 7.1 TB/s this way and at 6.5 with a
+// persistent grid.  The last items come first: the norm kernel read them last,
+// and they may still be in L2.
 __global__ void __launch_bounds__(kThreads) scale_kernel(Tables T) {
+#ifndef KFWD
+  const Item it = T.items[T.n_items - 1 - blockIdx.x];
+#else
+  const Item it = T.items[blockIdx.x];
+#endif
+  pdl_wait();
   const float factor = T.sc->factor;
-  if (T.sc->bad) return;
-  for (int64_t k = blockIdx.x; k < T.n_items; k += gridDim.x) {
-    const Item it = T.items[k];
-    if (it.src == it.dst && factor == 1.0f) continue;
-    for (int i = threadIdx.x; i < it.count; i += kThreads)
-      store_any(it, i, factor * load_any(it, i));
-  }
+  if (T.sc->bad || (it.src == it.dst && factor == 1.0f)) return;
+  if (it.in == TRAIN_BF16) item_scale_to<TRAIN_BF16>(it, factor);
+  else if (it.in == TRAIN_FP32) item_scale_to<TRAIN_FP32>(it, factor);
+  else item_scale_to<TRAIN_FP16>(it, factor);
 }
 
 int fail(int code, const std::string& msg) {
@@ -202,11 +402,44 @@ int launch_norm(train_clip_handle* h, float max_norm, float loss_scale, float* s
   return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, "norm kernel");
 }
 
+// As a programmatic dependent of the kernel before it: its CTAs have their
+// items when that one ends.
 int launch_scale(train_clip_handle* h) {
   if (h->T.n_items == 0) return LAMB_OK;
-  scale_kernel<<<h->grid, kThreads, 0, h->stream>>>(h->T);
-  const cudaError_t ce = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(h->T.n_items));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = h->stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t ce = cudaLaunchKernelEx(&cfg, scale_kernel, h->T);
   return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, "scale kernel");
+}
+
+// Cuts one tensor into items whose first 16-byte loads are aligned: only its
+// first item has elements in front of them.
+void add_items(std::vector<Item>* items, const char* src, char* dst, int64_t n, int32_t in,
+               int32_t out) {
+  const int si = size_of(in), so = size_of(out);
+  const int64_t per = kItemBytes / si;
+  const int head = int((16 - reinterpret_cast<uintptr_t>(src) % 16) % 16) / si;
+  const int wide = 16 / si * so < 16 ? 16 / si * so : 16;  // bytes of dst written at a time
+  const bool aligned = reinterpret_cast<uintptr_t>(dst + head * so) % unsigned(wide) == 0;
+  for (int64_t b = 0; b < n;) {
+    Item it{};
+    it.src = src + b * si;
+    it.dst = dst + b * so;
+    it.head = int8_t(b == 0 ? (head < n ? head : n) : 0);
+    it.count = int32_t(n - b < per + it.head ? n - b : per + it.head);
+    it.in = int8_t(in);
+    it.out = int8_t(out);
+    it.aligned = aligned;
+    items->push_back(it);
+    b += it.count;
+  }
 }
 
 int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32_t* dtypes,
@@ -225,19 +458,17 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
     if (rc != LAMB_OK) return rc;
     if (dst == grads[i] && to != dtypes[i])
       return fail(LAMB_ERR_INVALID, "outs" + at + " is grads" + at + ", of another type");
-    for (int64_t b = 0; b < sizes[i]; b += kMaxItem) {
-      const int64_t c = sizes[i] - b < kMaxItem ? sizes[i] - b : kMaxItem;
-      items.push_back(Item{static_cast<const char*>(grads[i]) + b * size_of(dtypes[i]),
-                           static_cast<char*>(dst) + b * size_of(to), int32_t(c),
-                           int16_t(dtypes[i]), int16_t(to)});
-    }
+    add_items(&items, static_cast<const char*>(grads[i]), static_cast<char*>(dst), sizes[i],
+              dtypes[i], to);
+    if (items.size() > 0x7fffffff) return fail(LAMB_ERR_INVALID, "too many elements");
   }
   int dev = 0, sms = 0;
   cudaError_t ce = cudaGetDevice(&dev);
   if (ce == cudaSuccess)
     ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (ce != cudaSuccess) return cuda_fail(ce, "querying the device");
-  const int grid = sms * 4;
+  int64_t grid = int64_t(sms) * kNormCtas;
+  if (grid > int64_t(items.size())) grid = items.empty() ? 1 : int64_t(items.size());
   const size_t item_bytes = (items.size() * sizeof(Item) + 255) / 256 * 256;
   const size_t part_bytes = (size_t(grid) * sizeof(double) + 255) / 256 * 256;
   void* block = nullptr;
@@ -259,7 +490,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   h->device = dev;
   h->stream = s;
   h->block = block;
-  h->grid = grid;
+  h->grid = int(grid);
   h->T.items = reinterpret_cast<const Item*>(p);
   h->T.partial = reinterpret_cast<double*>(p + item_bytes);
   h->T.sc = reinterpret_cast<Scalars*>(p + item_bytes + part_bytes);
@@ -334,7 +565,7 @@ LAMB_API int train_clip_finish(train_clip_handle* h, const double* exchange, flo
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  finish_kernel<<<1, 1, 0, h->stream>>>(h->T, exchange, max_norm, loss_scale, stats);
+  finish_kernel<<<1, 32, 0, h->stream>>>(h->T, exchange, max_norm, loss_scale, stats);
   const cudaError_t ce = cudaGetLastError();
   if (ce != cudaSuccess) return cuda_fail(ce, "finish kernel");
   return launch_scale(h);

@@ -908,6 +908,9 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
 #ifndef KFB
 #define KFB 48e6
 #endif
+#ifndef KFE
+#define KFE 64e3
+#endif
 constexpr double kFillBytes = KFB;
 
 constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
@@ -1141,7 +1144,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
       if (a.fill_first > most) a.fill_first = most;
       if (a.fill_first > a.rows_per_cta) a.fill_first = a.rows_per_cta;
       a.fill_rest = ctas * (a.rows_per_cta - a.fill_first);
-      a.fill_each = int64_t(64e3 / row_bytes) + 1;
+      a.fill_each = int64_t(KFE / row_bytes) + 1;
       a.fill_ctas = uint32_t((a.fill_rest + a.fill_each - 1) / a.fill_each);
     }
     const auto kernel = !scan ? fill_kernel<false, int32_t>
