@@ -85,6 +85,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load the in-tree library (building it first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "liblamb_gb300.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["lamb_kernels.cu", "lamb_api.cpp", "lamb_plan.cpp", "lamb_noalloc.cu",
-           "lamb_ptrs.cu", "train_embed.cu", "train_clip.cu"]
+           "lamb_ptrs.cu", "train_embed.cu", "train_embed_grad.cu", "train_clip.cu"]
 HEADERS = [os.path.join(INCLUDE, "lamb.h"), os.path.join(INCLUDE, "train_ops.h"),
            os.path.join(CSRC, "lamb_internal.h"), os.path.join(CSRC, "train_internal.h")]
 

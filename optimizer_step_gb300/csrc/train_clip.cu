@@ -1,10 +1,8 @@
 // Global gradient norm over many tensors and clipping (train_ops.h).
 #include <cmath>
 #include <new>
-#include <string>
 #include <vector>
 
-#include "lamb_internal.h"
 #include "train_internal.h"
 
 using namespace traingb;
@@ -16,10 +14,10 @@ constexpr int kWarps = kThreads / 32;
 // Bytes of grads in one piece of work: eight 16-byte loads a thread.
 constexpr int kLoads = 8;
 constexpr int64_t kItemBytes = kThreads * kLoads * 16;
-#ifndef KNORM
-#define KNORM 6
-#endif
-constexpr int kNormCtas = KNORM;  // per SM
+// Half as many where everything fits into L2, so that a few items a CTA come
+// out more even.
+constexpr int64_t kSmallTotal = 128 << 20;
+constexpr int kNormCtas = 5;  // per SM
 
 // One piece of a tensor: count elements from src, written to dst.
 struct __align__(32) Item {
@@ -39,7 +37,6 @@ struct Scalars {
   float factor;     // c / S, 0 when a grad is not finite
   uint32_t bad;     // a grad is inf or NaN
   uint32_t ticket;  // CTAs of the norm kernel that have finished
-  uint32_t flag;    // OR of the CTAs' inf/NaN flags
 };
 
 struct Tables {
@@ -49,11 +46,14 @@ struct Tables {
   int64_t n_items;
 };
 
-__device__ __forceinline__ void pdl_trigger() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void pdl_wait() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+// 16 bytes, in order with the other loads of its kind: a thread's loads are all
+// on their way before the first value is used.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 q;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+               : "l"(p));
+  return q;
 }
 
 __device__ __forceinline__ double warp_sum(double x) {
@@ -62,15 +62,15 @@ __device__ __forceinline__ double warp_sum(double x) {
   return x;
 }
 
-// Fixed-shape block sum; the result is valid in every thread.
+// Fixed-shape block sum; the result is valid in the first warp.
 __device__ __forceinline__ double block_sum(double x, double* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   x = warp_sum(x);
   if (lane == 0) red[warp] = x;
   __syncthreads();
-  double y = lane < kWarps ? red[lane] : 0.0;
-  y = warp_sum(y);
-  __syncthreads();
+  double y = red[lane & (kWarps - 1)];
+#pragma unroll
+  for (int o = kWarps / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
   return y;
 }
 
@@ -128,8 +128,7 @@ __device__ __forceinline__ void item_squares(const Item& it, double& acc, uint32
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
     q[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (v + u * kThreads < vecs)
-      q[u] = __ldg(reinterpret_cast<const uint4*>(base) + v + u * kThreads);
+    if (v + u * kThreads < vecs) q[u] = load16(base + int64_t(v + u * kThreads) * 16);
   }
   // What the 16-byte loads leave: up to 7 elements in front and behind.
   const int rest = it.count - vecs * kPer;
@@ -175,39 +174,54 @@ __device__ __forceinline__ void item_squares(const Item& it, double& acc, uint32
   }
 }
 
-// Forms the norm, the factor and the flag from the sum.  Called by a warp: an
-// fp64 division costs about half a microsecond, so three lanes take one each.
-__device__ __forceinline__ void publish(Scalars* sc, float* stats, double sum, bool bad,
-                                        float max_norm, float loss_scale) {
-  const int lane = threadIdx.x & 31;
-  const double root = sqrt(sum);
-  const double top = lane == 0 ? root : lane == 1 ? double(max_norm) : 1.0;
-  const double q = top / (lane == 1 ? root : double(loss_scale));
-  const double norm = __shfl_sync(0xffffffffu, q, 0);
-  const double clipped = __shfl_sync(0xffffffffu, q, 1);  // max_norm / G / S
-  const double plain = __shfl_sync(0xffffffffu, q, 2);
-  if (lane != 0) return;
-  const double factor = max_norm > 0.0f && norm > double(max_norm) ? clipped : plain;
+// Forms the norm, the factor and the flag from the sum of squares (infinite if
+// a grad is inf or NaN).  fp64 square roots and divisions cost about half a
+// microsecond each on one thread, so there are none: with sum = m 4^k, m in
+// [1, 4), one Newton step y (3 - m y^2) / 2 takes the fp32 reciprocal square
+// root of m (off by 2^-22 at most) to 2^-42, and the norm m y 2^k / S and the
+// factor max_norm y / 2^k are products.
+struct Request {
+  double inv_scale;  // 1 / S
+  double max_norm;
+  float* stats;
+  double* exchange;  // not NULL: only the sum and the flag, here
+};
+
+__device__ __forceinline__ void publish(Scalars* sc, const Request& r, double sum) {
+  const bool bad = !(sum < __longlong_as_double(0x7ff0000000000000ll));
+  double root = 0.0, inverse = 0.0;
+  if (!bad && sum > 0.0) {
+    // Squares of fp32 numbers, so sum is a normal number.
+    const int64_t bits = __double_as_longlong(sum);
+    const int k = (int(bits >> 52) - 1023) >> 1;
+    const double m = __longlong_as_double(bits - (int64_t(2 * k) << 52));
+    double y = double(rsqrtf(float(m)));
+    y *= fma(-0.5 * m * y, y, 1.5);
+    root = m * y * __longlong_as_double(int64_t(1023 + k) << 52);
+    inverse = y * __longlong_as_double(int64_t(1023 - k) << 52);
+  }
+  const double norm = root * r.inv_scale;
+  const double factor = r.max_norm > 0.0 && norm > r.max_norm ? r.max_norm * inverse : r.inv_scale;
   sc->factor = bad ? 0.0f : float(factor);
   sc->bad = bad;
-  stats[0] = bad ? __int_as_float(0x7f800000) : float(norm);
-  stats[1] = bad ? 0.0f : float(factor);
-  stats[2] = bad ? 1.0f : 0.0f;
+  r.stats[0] = bad ? __int_as_float(0x7f800000) : float(norm);
+  r.stats[1] = bad ? 0.0f : float(factor);
+  r.stats[2] = bad ? 1.0f : 0.0f;
 }
 
 // Sum of squares: each CTA walks every gridDim.x-th item, all of them through
 // memory side by side; the last one to finish adds the CTAs' sums in order and
 // publishes.
-__global__ void __launch_bounds__(kThreads) norm_kernel(Tables T, float max_norm,
-                                                        float loss_scale, float* stats,
-                                                        double* exchange) {
+__global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Tables T,
+                                                        const __grid_constant__ Request r) {
   __shared__ double red[kWarps];
-  __shared__ uint32_t last, any;
+  __shared__ uint32_t last;
   pdl_trigger();
   double acc = 0.0;
   uint32_t bad = 0;
   Item next{};
   if (blockIdx.x < T.n_items) next = T.items[blockIdx.x];
+  pdl_wait();
   for (int64_t k = blockIdx.x; k < T.n_items; k += gridDim.x) {
     const Item it = next;
     if (k + gridDim.x < T.n_items) next = T.items[k + gridDim.x];
@@ -215,37 +229,39 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(Tables T, float max_norm
     else if (it.in == TRAIN_FP32) item_squares<TRAIN_FP32>(it, acc, bad);
     else item_squares<TRAIN_FP16>(it, acc, bad);
   }
+  // An inf or NaN grad makes the sum infinite; finite grads cannot.
+  if (bad) acc = __longlong_as_double(0x7ff0000000000000ll);
   const double s = block_sum(acc, red);
-  bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) {
-    T.partial[blockIdx.x] = s;
-    if (bad) atomicOr(&T.sc->flag, 1u);
-    __threadfence();
-    last = atomicAdd(&T.sc->ticket, 1u) == gridDim.x - 1;
+    __stcg(&T.partial[blockIdx.x], s);
+    uint32_t before;
+    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+                 : "=r"(before)
+                 : "l"(&T.sc->ticket)
+                 : "memory");
+    last = before == gridDim.x - 1;
   }
   __syncthreads();
   if (!last) return;
-  __threadfence();
   double sum = 0.0;
   for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) sum += __ldcg(&T.partial[i]);
   sum = block_sum(sum, red);
-  if (threadIdx.x == 0) {
-    any = atomicExch(&T.sc->flag, 0u);
-    T.sc->ticket = 0;
-    if (exchange) {
-      exchange[0] = any ? 0.0 : sum;
-      exchange[1] = any ? 1.0 : 0.0;
-    }
+  if (threadIdx.x != 0) return;
+  T.sc->ticket = 0;
+  if (r.exchange) {
+    const bool any = !(sum < __longlong_as_double(0x7ff0000000000000ll));
+    r.exchange[0] = any ? 0.0 : sum;
+    r.exchange[1] = any ? 1.0 : 0.0;
+  } else {
+    publish(T.sc, r, sum);
   }
-  __syncthreads();
-  if (!exchange && threadIdx.x < 32) publish(T.sc, stats, sum, any != 0, max_norm, loss_scale);
 }
 
-__global__ void __launch_bounds__(32) finish_kernel(Tables T, const double* exchange,
-                                                    float max_norm, float loss_scale,
-                                                    float* stats) {
+__global__ void finish_kernel(const __grid_constant__ Tables T,
+                              const __grid_constant__ Request r) {
   pdl_trigger();
-  publish(T.sc, stats, exchange[0], !(exchange[1] == 0.0), max_norm, loss_scale);
+  publish(T.sc, r,
+          r.exchange[1] == 0.0 ? r.exchange[0] : __longlong_as_double(0x7ff0000000000000ll));
 }
 
 template <int IN>
@@ -277,7 +293,7 @@ __device__ __forceinline__ void item_scale(const Item& it, float factor) {
   uint4 q[kLoads];
 #pragma unroll
   for (int u = 0; u < kLoads; ++u)
-    if (int(threadIdx.x) + u * kThreads < vecs) q[u] = src[threadIdx.x + u * kThreads];
+    if (int(threadIdx.x) + u * kThreads < vecs) q[u] = load16(src + threadIdx.x + u * kThreads);
   const int rest = it.count - vecs * kPer;
   if (threadIdx.x < rest) {
     const int i = threadIdx.x < head ? int(threadIdx.x) : vecs * kPer + int(threadIdx.x);
@@ -286,7 +302,7 @@ __device__ __forceinline__ void item_scale(const Item& it, float factor) {
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
     const int v = threadIdx.x + u * kThreads;
-    if (v >= vecs) break;
+    if (v >= vecs) continue;
     const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
     float x[kPer];
 #pragma unroll
@@ -329,22 +345,14 @@ __device__ __forceinline__ void item_scale_to(const Item& it, float factor) {
 // persistent grid.  The last items come first: the norm kernel read them last,
 // and they may still be in L2.
 __global__ void __launch_bounds__(kThreads) scale_kernel(Tables T) {
-#ifndef KFWD
   const Item it = T.items[T.n_items - 1 - blockIdx.x];
-#else
-  const Item it = T.items[blockIdx.x];
-#endif
+  pdl_trigger();
   pdl_wait();
   const float factor = T.sc->factor;
   if (T.sc->bad || (it.src == it.dst && factor == 1.0f)) return;
   if (it.in == TRAIN_BF16) item_scale_to<TRAIN_BF16>(it, factor);
   else if (it.in == TRAIN_FP32) item_scale_to<TRAIN_FP32>(it, factor);
   else item_scale_to<TRAIN_FP16>(it, factor);
-}
-
-int fail(int code, const std::string& msg) {
-  lambgb::set_last_error(msg);
-  return code;
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
@@ -395,36 +403,42 @@ int check_device(const void* p, size_t align, const char* name) {
 
 bool known(int32_t dt) { return dt == TRAIN_BF16 || dt == TRAIN_FP16 || dt == TRAIN_FP32; }
 
-int launch_norm(train_clip_handle* h, float max_norm, float loss_scale, float* stats,
-                double* exchange) {
-  norm_kernel<<<h->grid, kThreads, 0, h->stream>>>(h->T, max_norm, loss_scale, stats, exchange);
-  const cudaError_t ce = cudaGetLastError();
-  return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, "norm kernel");
-}
-
-// As a programmatic dependent of the kernel before it: its CTAs have their
-// items when that one ends.
-int launch_scale(train_clip_handle* h) {
-  if (h->T.n_items == 0) return LAMB_OK;
+// Launches, if asked as a programmatic dependent of the kernel before it, so
+// that its CTAs have their items when that one ends.
+template <class... A>
+int launch(train_clip_handle* h, const char* what, void (*kernel)(A...), int64_t grid,
+           bool dependent, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(h->T.n_items));
+  cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = h->stream;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const cudaError_t ce = cudaLaunchKernelEx(&cfg, scale_kernel, h->T);
-  return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, "scale kernel");
+  cfg.numAttrs = dependent ? 1 : 0;
+  const cudaError_t ce = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, what);
+}
+
+int launch_norm(train_clip_handle* h, const Request& r) {
+  // CTAs that start while another kernel holds part of the GPU are spread over
+  // the SMs unevenly.  Where each has one item that costs nothing and the early
+  // start saves 1.5 us; a walk over many items was up to 10% slower.
+  return launch(h, "norm kernel", norm_kernel, h->grid, h->T.n_items <= h->grid, h->T, r);
+}
+
+int launch_scale(train_clip_handle* h) {
+  if (h->T.n_items == 0) return LAMB_OK;
+  return launch(h, "scale kernel", scale_kernel, h->T.n_items, true, h->T);
 }
 
 // Cuts one tensor into items whose first 16-byte loads are aligned: only its
 // first item has elements in front of them.
 void add_items(std::vector<Item>* items, const char* src, char* dst, int64_t n, int32_t in,
-               int32_t out) {
+               int32_t out, int64_t item_bytes) {
   const int si = size_of(in), so = size_of(out);
-  const int64_t per = kItemBytes / si;
+  const int64_t per = item_bytes / si;
   const int head = int((16 - reinterpret_cast<uintptr_t>(src) % 16) % 16) / si;
   const int wide = 16 / si * so < 16 ? 16 / si * so : 16;  // bytes of dst written at a time
   const bool aligned = reinterpret_cast<uintptr_t>(dst + head * so) % unsigned(wide) == 0;
@@ -445,6 +459,10 @@ void add_items(std::vector<Item>* items, const char* src, char* dst, int64_t n, 
 int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32_t* dtypes,
            void* const* grads, void* const* outs, const int32_t* out_dtypes, void* stream) {
   std::vector<Item> items;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n && total < kSmallTotal; ++i)
+    if (sizes[i] > 0 && known(dtypes[i])) total += (sizes[i] < kSmallTotal ? sizes[i] : kSmallTotal) * size_of(dtypes[i]);
+  const int64_t item_bytes = total < kSmallTotal ? kItemBytes / 2 : kItemBytes;
   for (int32_t i = 0; i < n; ++i) {
     const std::string at = "[" + std::to_string(i) + "]";
     if (sizes[i] < 0) return fail(LAMB_ERR_INVALID, "sizes" + at + " < 0");
@@ -459,7 +477,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
     if (dst == grads[i] && to != dtypes[i])
       return fail(LAMB_ERR_INVALID, "outs" + at + " is grads" + at + ", of another type");
     add_items(&items, static_cast<const char*>(grads[i]), static_cast<char*>(dst), sizes[i],
-              dtypes[i], to);
+              dtypes[i], to, item_bytes);
     if (items.size() > 0x7fffffff) return fail(LAMB_ERR_INVALID, "too many elements");
   }
   int dev = 0, sms = 0;
@@ -469,17 +487,17 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   if (ce != cudaSuccess) return cuda_fail(ce, "querying the device");
   int64_t grid = int64_t(sms) * kNormCtas;
   if (grid > int64_t(items.size())) grid = items.empty() ? 1 : int64_t(items.size());
-  const size_t item_bytes = (items.size() * sizeof(Item) + 255) / 256 * 256;
+  const size_t table_bytes = (items.size() * sizeof(Item) + 255) / 256 * 256;
   const size_t part_bytes = (size_t(grid) * sizeof(double) + 255) / 256 * 256;
   void* block = nullptr;
-  ce = cudaMalloc(&block, item_bytes + part_bytes + sizeof(Scalars));
+  ce = cudaMalloc(&block, table_bytes + part_bytes + sizeof(Scalars));
   if (ce != cudaSuccess) return cuda_fail(ce, "allocating the work table");
   char* p = static_cast<char*>(block);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!items.empty())
     ce = cudaMemcpyAsync(p, items.data(), items.size() * sizeof(Item), cudaMemcpyHostToDevice, s);
   if (ce == cudaSuccess)
-    ce = cudaMemsetAsync(p + item_bytes, 0, part_bytes + sizeof(Scalars), s);
+    ce = cudaMemsetAsync(p + table_bytes, 0, part_bytes + sizeof(Scalars), s);
   if (ce == cudaSuccess) ce = cudaStreamSynchronize(s);
   train_clip_handle* h = ce == cudaSuccess ? new (std::nothrow) train_clip_handle : nullptr;
   if (!h) {
@@ -492,8 +510,8 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   h->block = block;
   h->grid = int(grid);
   h->T.items = reinterpret_cast<const Item*>(p);
-  h->T.partial = reinterpret_cast<double*>(p + item_bytes);
-  h->T.sc = reinterpret_cast<Scalars*>(p + item_bytes + part_bytes);
+  h->T.partial = reinterpret_cast<double*>(p + table_bytes);
+  h->T.sc = reinterpret_cast<Scalars*>(p + table_bytes + part_bytes);
   h->T.n_items = int64_t(items.size());
   *out = h;
   return LAMB_OK;
@@ -529,7 +547,7 @@ LAMB_API int train_clip_norm(train_clip_handle* h, float loss_scale, float* stat
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  return launch_norm(h, 0.0f, loss_scale, stats, nullptr);
+  return launch_norm(h, Request{1.0 / double(loss_scale), 0.0, stats, nullptr});
 }
 
 LAMB_API int train_clip_grads(train_clip_handle* h, float max_norm, float loss_scale,
@@ -541,7 +559,7 @@ LAMB_API int train_clip_grads(train_clip_handle* h, float max_norm, float loss_s
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  rc = launch_norm(h, max_norm, loss_scale, stats, nullptr);
+  rc = launch_norm(h, Request{1.0 / double(loss_scale), double(max_norm), stats, nullptr});
   return rc == LAMB_OK ? launch_scale(h) : rc;
 }
 
@@ -552,7 +570,7 @@ LAMB_API int train_clip_partial(train_clip_handle* h, double* exchange) {
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  return launch_norm(h, 0.0f, 1.0f, nullptr, exchange);
+  return launch_norm(h, Request{1.0, 0.0, nullptr, exchange});
 }
 
 LAMB_API int train_clip_finish(train_clip_handle* h, const double* exchange, float max_norm,
@@ -565,7 +583,9 @@ LAMB_API int train_clip_finish(train_clip_handle* h, const double* exchange, flo
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  finish_kernel<<<1, 32, 0, h->stream>>>(h->T, exchange, max_norm, loss_scale, stats);
+  finish_kernel<<<1, 1, 0, h->stream>>>(
+      h->T, Request{1.0 / double(loss_scale), double(max_norm), stats,
+                    const_cast<double*>(exchange)});
   const cudaError_t ce = cudaGetLastError();
   if (ce != cudaSuccess) return cuda_fail(ce, "finish kernel");
   return launch_scale(h);

@@ -1,0 +1,1040 @@
+// The gradient of the embedding lookup by sorted tokens (train_ops.h).
+#include <cooperative_groups.h>
+
+#include "train_internal.h"
+
+using namespace traingb;
+namespace cg = cooperative_groups;
+
+namespace {
+
+// G[v, :] = scale * sum over the positions i with row(ids[i]) = v of dy[i, :].
+// The positions are sorted by row (stably, so ascending within a row), and the
+// sorted list is cut into blocks of C positions.  A warp takes one block and
+// a slab of up to 512 columns, streams the rows of dy that its positions name
+// through a ring of shared memory and adds each run of equal rows in
+// registers.  A run that ends in the next block at the latest is finished by
+// the warp of the block it starts in.  A longer one (a frequent token) is cut
+// at the block boundaries: each piece's fp32 sum goes to a slot of the
+// workspace, and join_kernel adds the pieces in order.  So no warp adds more
+// than 2 C rows whatever the tokens are, only long runs pay for slots, and
+// the order of every sum depends on the ids and the sizes alone.
+
+// One sorted position: the row that its token names (n_rows for a token that
+// adds nothing) and the position.
+struct __align__(8) Place {
+  uint32_t key, pos;
+};
+
+// A run that is cut into pieces: the block it starts in, its row, the pieces.
+struct __align__(16) LongRun {
+  uint32_t block, row, pieces, unused;
+};
+
+struct GradArgs {
+  const void* dy;
+  void* grad;
+  const void* ids;
+  const Place* places;  // sorted
+  float* slots;         // [2 * block + (0: run from an earlier block, 1: starts here)][slot_dim]
+  uint32_t* n_long;     // long runs in the list
+  LongRun* long_runs;   // in any order
+  int64_t dy_stride, grad_stride, n_rows, dim, slot_dim, first_row, padding;
+  int64_t n;
+  int64_t n_blocks;
+  int64_t units;         // blocks times slabs
+  // Rows that no token names.  A CTA of fill_kernel marks the named ones among
+  // rows_per_cta rows and zeroes the others of the first fill_first of them;
+  // CTAs of sum_kernel zero the rest, fill_each rows a CTA.
+  uint32_t* named;  // a bit a row
+  int64_t rows_per_cta, fill_first, fill_rest, fill_each;
+  uint32_t fill_ctas;    // of sum_kernel
+  int32_t block, slabs;  // C, slabs of columns
+  float scale;
+  int32_t accumulate, out_type;
+};
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return uint32_t(__cvta_generic_to_shared(p));
+}
+// 16 bytes from global to shared memory, asynchronously; the bytes from
+// `bytes` on are not read and become zero.
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+__device__ __forceinline__ char* grad_at(const GradArgs& a, int64_t row, int64_t col) {
+  return static_cast<char*>(a.grad) + (row * a.grad_stride + col) * size_of(a.out_type);
+}
+
+// Eight neighbouring values, 16-byte aligned (each half, if 32 bits wide).
+__device__ __forceinline__ void load8(const void* p, int type, float (&x)[8]) {
+  if (type == TRAIN_FP32) {
+    const float4 u = static_cast<const float4*>(p)[0], v = static_cast<const float4*>(p)[1];
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+    return;
+  }
+  const uint4 q = *static_cast<const uint4*>(p);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == TRAIN_BF16) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      x[2 * i] = to_float<TRAIN_FP16>(uint16_t(w[i] & 0xffffu));
+      x[2 * i + 1] = to_float<TRAIN_FP16>(uint16_t(w[i] >> 16));
+    }
+  }
+}
+
+__device__ __forceinline__ void store8(void* p, int type, const float (&x)[8]) {
+  if (type == TRAIN_FP32) {
+    static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[2 * i])
+                                           : from_float<TRAIN_FP16>(x[2 * i]);
+    const uint32_t hi = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[2 * i + 1])
+                                           : from_float<TRAIN_FP16>(x[2 * i + 1]);
+    w[i] = lo | hi << 16;
+  }
+  *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float load1(const void* p, int type) {
+  if (type == TRAIN_FP32) return *static_cast<const float*>(p);
+  const uint16_t h = *static_cast<const uint16_t*>(p);
+  return type == TRAIN_BF16 ? to_float<TRAIN_BF16>(h) : to_float<TRAIN_FP16>(h);
+}
+
+__device__ __forceinline__ void store1(void* p, int type, float x) {
+  if (type == TRAIN_FP32) *static_cast<float*>(p) = x;
+  else if (type == TRAIN_BF16) *static_cast<uint16_t*>(p) = from_float<TRAIN_BF16>(x);
+  else *static_cast<uint16_t*>(p) = from_float<TRAIN_FP16>(x);
+}
+
+// First index whose row is at least `row`.
+__device__ __forceinline__ int64_t lower_bound(const Place* places, int64_t n, uint32_t row) {
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (places[mid].key < row) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// A warp writes zeros to bytes bytes at p.
+__device__ __forceinline__ void warp_zero(char* p, int64_t bytes, int lane) {
+  const int64_t head = min(int64_t((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15), bytes);
+  for (int64_t i = 2 * lane; i < head; i += 2 * kWarp) *reinterpret_cast<uint16_t*>(p + i) = 0;
+  char* q = p + head;
+  const int64_t body = (bytes - head) / 16;
+  for (int64_t i = lane; i < body; i += kWarp)
+    reinterpret_cast<uint4*>(q)[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = 16 * body + 2 * lane; i < bytes - head; i += 2 * kWarp)
+    *reinterpret_cast<uint16_t*>(q + i) = 0;
+}
+
+// Marks the rows that tokens name and zeroes some of the others, a range of
+// rows a CTA.  SCAN: the CTA finds its rows by a walk over all ids, so it needs
+// no sorted list and runs while the tokens are being sorted.  Else it looks
+// its rows up in that list.
+//
+// What is written alone goes out at 5.4 TB/s on GB300, and written while other
+// rows are read at 6.5 to 6.8; so this kernel zeroes what fits into the time of
+// the sort, and CTAs among those of sum_kernel zero the rest.
+constexpr int kFillThreads = 512;
+constexpr int kFillRows = 4096;  // at most, a CTA
+
+template <bool SCAN, class ID>
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ uint32_t named[kFillRows / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t r0 = int64_t(blockIdx.x) * a.rows_per_cta;
+  const int64_t count = min(a.rows_per_cta, a.n_rows - r0);
+  pdl_trigger();
+  for (int i = threadIdx.x; i < kFillRows / 32; i += kFillThreads) named[i] = 0u;
+  __syncthreads();
+  if (SCAN) {
+    const ID* ids = static_cast<const ID*>(a.ids);
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < a.n; i += kFillThreads) {
+      const ID id = ids[i];
+      const uint64_t r = uint64_t(int64_t(id)) - uint64_t(a.first_row) - uint64_t(r0);
+      if (r < uint64_t(count) && int64_t(id) != a.padding)
+        atomicOr(&named[r / 32], 1u << (r & 31));
+    }
+  } else {
+    pdl_wait();
+    const int64_t lo = lower_bound(a.places, a.n, uint32_t(r0));
+    const int64_t hi = lower_bound(a.places, a.n, uint32_t(r0 + count));
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kFillThreads) {
+      const uint32_t r = a.places[i].key - uint32_t(r0);
+      atomicOr(&named[r / 32], 1u << (r & 31));
+    }
+  }
+  __syncthreads();
+  for (int64_t i = threadIdx.x; 32 * i < count; i += kFillThreads)
+    a.named[r0 / 32 + i] = named[i];
+  const int64_t first = min(count, a.fill_first);
+  for (int64_t r = warp; r < first; r += kFillThreads / kWarp)
+    if (!((named[r / 32] >> (r & 31)) & 1u))
+      warp_zero(grad_at(a, r0 + r, 0), a.dim * size_of(a.out_type), lane);
+  // What follows waits for this kernel; it must find the sort finished too.
+  if (SCAN) pdl_wait();
+}
+
+// The rows that fill_kernel has left, in a CTA of sum_kernel: fill_each of
+// them, `index` counting from the first.
+__device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / kWarp;
+  const int64_t left = a.rows_per_cta - a.fill_first;
+  const int64_t q1 = min((index + 1) * a.fill_each, a.fill_rest);
+  for (int64_t q0 = index * a.fill_each; q0 < q1; q0 += kWarp) {
+    const int64_t q = q0 + lane;
+    const int64_t row = q / left * a.rows_per_cta + a.fill_first + q % left;
+    const bool idle =
+        q < q1 && row < a.n_rows && !((a.named[row / 32] >> (row & 31)) & 1u);
+    unsigned todo = __ballot_sync(kAll, idle);
+    for (int k = 0; todo; ++k) {
+      const int64_t r = __shfl_sync(kAll, row, __ffs(todo) - 1);
+      todo &= todo - 1;
+      if (k % warps == warp) warp_zero(grad_at(a, r, 0), a.dim * size_of(a.out_type), lane);
+    }
+  }
+}
+
+// The ring of one warp: kStages rows' pieces of a slab in flight.  The copies
+// are asynchronous (16 bytes a lane), so they hold no registers, and the rows
+// of the grad that accumulation needs come through the same ring behind the
+// last row of their run: nothing waits for them when the run is finished.
+#ifndef KST
+#define KST 8
+#endif
+#ifndef KSW
+#define KSW 4
+#endif
+#ifndef KMB
+#define KMB 64
+#endif
+#ifndef KU
+#define KU 4096
+#endif
+constexpr int kStages = KST;
+constexpr int kStageBytes = 1024 + 32;  // a piece and its ends' alignment
+constexpr int kMaxBlock = KMB;
+constexpr int kSumWarps = KSW;
+
+struct WarpSmem {
+  alignas(16) unsigned char ring[kStages][kStageBytes];
+  uint32_t key[2 * kMaxBlock + 4];
+  uint32_t pos[2 * kMaxBlock];
+};
+
+// COLS columns a lane: 16 where no 32-bit type comes through the ring, else 8.
+// ALIGNED: rows of dy and of the grad start at multiples of 16 bytes and dim is
+// a multiple of 8; a lane holds groups of 8 neighbours and copies exactly what
+// it reads.  Else a lane holds every 32nd column, and the 16-byte granules
+// that cover a piece are copied, its neighbours' bytes with it.
+template <int IN, int COLS, bool ALIGNED>
+__global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
+    const __grid_constant__ GradArgs a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  constexpr int kSlab = kWarp * COLS;
+  const int lane = threadIdx.x & 31;
+  WarpSmem& s = reinterpret_cast<WarpSmem*>(raw)[threadIdx.x >> 5];
+  // The CTAs that write zero rows are spread evenly among the others.
+  const uint32_t fill0 = uint32_t(uint64_t(blockIdx.x) * a.fill_ctas / gridDim.x);
+  const uint32_t fill1 = uint32_t((uint64_t(blockIdx.x) + 1) * a.fill_ctas / gridDim.x);
+  const int64_t unit = int64_t(blockIdx.x - fill0) * kSumWarps + (threadIdx.x >> 5);
+  pdl_trigger();
+  pdl_wait();
+  if (fill1 != fill0) {
+    fill_rest(a, fill0);
+    return;
+  }
+  if (unit >= a.units) return;
+  const int64_t b = unit / a.slabs;
+  const int64_t col0 = (unit % a.slabs) * kSlab;
+  const int cols = int(min(int64_t(kSlab), a.dim - col0));
+  const int64_t n = a.n, lo = b * a.block;
+  const int C = a.block;
+  const uint32_t none = uint32_t(a.n_rows);
+
+  // The block and the next one: rows behind the list count as `none`.
+  for (int i = lane; i < 2 * C; i += kWarp) {
+    Place p{none, 0u};
+    if (lo + i < n) p = a.places[lo + i];
+    s.key[i] = p.key;
+    s.pos[i] = p.pos;
+  }
+  const uint32_t after = lo + 2 * C < n ? a.places[lo + 2 * C].key : none;
+  const uint32_t before = lo > 0 ? a.places[lo - 1].key : none;
+  const uint32_t far_before = lo > C ? a.places[lo - C - 1].key : none;
+  if (lane == 0) s.key[2 * C] = after;
+  __syncwarp();
+  const uint32_t first = s.key[0], last = s.key[C - 1];
+  if (first == none) return;
+  // The run that reaches in from the block before: a piece of a long run, or
+  // finished by its own block.
+  const bool from_before = before == first;
+  const bool head_piece = from_before && (s.key[C] == first || far_before == first);
+  // The run that starts here and reaches out: into the next block at most, or
+  // long.
+  const bool reaches_out =
+      last != none && s.key[C] == last && !(from_before && first == last);
+  const bool tail_piece = reaches_out && after == last;
+  const int end = reaches_out && !tail_piece ? 2 * C : C;
+  // Positions [x, stop) of the window are added here.
+  int x = 0, stop = 0;
+  for (int i0 = 0; i0 < end; i0 += kWarp) {
+    const int i = i0 + lane;
+    const uint32_t key = i < end ? s.key[i] : none;
+    const bool skipped = from_before && !head_piece && key == first;
+    const bool wanted = key != none && !skipped && (i < C || key == last);
+    const unsigned use = __ballot_sync(kAll, wanted), skip = __ballot_sync(kAll, skipped);
+    x += __popc(skip);
+    stop += __popc(skip | use);
+  }
+  if (x >= stop) return;
+
+  const char* const dy = static_cast<const char*>(a.dy);
+  char* const grad = static_cast<char*>(a.grad);
+  const int out_size = size_of(a.out_type);
+  // A run's last position here.  Only final sums need the old row.
+  const auto ends = [&](int i) { return s.key[i] != s.key[i + 1]; };
+  const auto is_head = [&](uint32_t key) { return head_piece && key == first; };
+
+  // Starts the copy of the piece [col0, col0 + cols) of a row at `row`.
+  const auto copy_piece = [&](unsigned char* dst, const char* row, int size, const char* begin,
+                              const char* limit) {
+    const char* src = row + col0 * size;
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int g = 0; g < COLS / 8; ++g) {
+        const int c = g * 8 * kWarp + lane * 8;
+        if (c < cols) {
+          copy16(dst + c * size, src + c * size, 16);
+          if (size == 4) copy16(dst + c * size + 16, src + c * size + 16, 16);
+        }
+      }
+    } else {
+      const int shift = int(reinterpret_cast<uintptr_t>(src) & 15);
+      const int granules = (shift + cols * size + 15) / 16;
+      for (int g = lane; g < granules; g += kWarp) {
+        const char* q = src - shift + 16 * g;
+        if (q >= begin) {
+          const int64_t left = limit - q;
+          copy16(dst + 16 * g, q, left < 16 ? int(left) : 16);
+        } else {
+          // In front of the matrix: only what belongs to it.
+          for (int i = int(begin - q); i < 16; i += 2)
+            if (q + i < limit)
+              *reinterpret_cast<uint16_t*>(dst + 16 * g + i) =
+                  *reinterpret_cast<const uint16_t*>(q + i);
+        }
+      }
+    }
+  };
+  const char* const dy_limit = dy + ((n - 1) * a.dy_stride + a.dim) * size_of(IN);
+  const char* const grad_limit = grad + ((a.n_rows - 1) * a.grad_stride + a.dim) * out_size;
+
+  // The next piece to fetch: position at, or the old row behind it.
+  int at = x;
+  bool old_next = false;
+  const auto fetch = [&](int stage) {
+    if (at < stop) {
+      if (!old_next) {
+        copy_piece(s.ring[stage], dy + int64_t(s.pos[at]) * a.dy_stride * size_of(IN),
+                   size_of(IN), dy, dy_limit);
+        old_next = a.accumulate && ends(at) && !is_head(s.key[at]);
+        if (!old_next) ++at;
+      } else {
+        copy_piece(s.ring[stage], grad_at(a, s.key[at], 0), out_size, grad, grad_limit);
+        old_next = false;
+        ++at;
+      }
+    }
+    copy_commit();
+  };
+  // A lane's values of the piece in a stage; `row` gives its alignment.
+  const auto read_piece = [&](int stage, const char* row, int type, float (&v)[COLS]) {
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int g = 0; g < COLS / 8; ++g) {
+        float u[8];
+        load8(s.ring[stage] + (g * 8 * kWarp + lane * 8) * size_of(type), type, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * g + i] = u[i];
+      }
+    } else {
+      const int shift = int(reinterpret_cast<uintptr_t>(row + col0 * size_of(type)) & 15);
+#pragma unroll
+      for (int i = 0; i < COLS; ++i)
+        v[i] = load1(s.ring[stage] + shift + (lane + kWarp * i) * size_of(type), type);
+    }
+  };
+
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  float acc[COLS];
+#pragma unroll
+  for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+  int stage = 0;
+  const auto next_stage = [&] {
+    // One more piece into the stage read last, then wait for the oldest.
+    __syncwarp();
+    fetch(stage == 0 ? kStages - 1 : stage - 1);
+    copy_wait<kStages - 1>();
+    __syncwarp();
+  };
+  const auto done_stage = [&] { stage = stage == kStages - 1 ? 0 : stage + 1; };
+  const auto write_slot = [&](int which) {
+    float* slot = a.slots + (2 * b + which) * a.slot_dim + col0;
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int g = 0; g < COLS / 8; ++g) {
+        const int c = g * 8 * kWarp + lane * 8;
+        if (c < cols) {
+          float u[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) u[i] = acc[8 * g + i];
+          store8(slot + c, TRAIN_FP32, u);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < COLS; ++i)
+        if (lane + kWarp * i < cols) slot[lane + kWarp * i] = acc[i];
+    }
+  };
+
+  for (; x < stop; ++x) {
+    next_stage();
+    float v[COLS];
+    read_piece(stage, dy + int64_t(s.pos[x]) * a.dy_stride * size_of(IN), IN, v);
+    done_stage();
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) acc[i] += v[i];
+    if (!ends(x)) continue;
+    const uint32_t key = s.key[x];
+    if (is_head(key)) {
+      write_slot(0);
+    } else {
+      char* row = grad_at(a, key, 0);
+      if (a.accumulate) {
+        next_stage();
+        read_piece(stage, row, a.out_type, v);
+        done_stage();
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) acc[i] = fmaf(a.scale, acc[i], v[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) acc[i] *= a.scale;
+      }
+      if constexpr (ALIGNED) {
+#pragma unroll
+        for (int g = 0; g < COLS / 8; ++g) {
+          const int c = g * 8 * kWarp + lane * 8;
+          if (c < cols) {
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) u[i] = acc[8 * g + i];
+            store8(row + (col0 + c) * out_size, a.out_type, u);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i)
+          if (lane + kWarp * i < cols)
+            store1(row + (col0 + lane + kWarp * i) * out_size, a.out_type, acc[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < COLS; ++i) acc[i] = 0.0f;
+  }
+  // What is left in the registers is a piece of a run that goes on.
+  if (!ends(stop - 1)) write_slot(is_head(s.key[stop - 1]) ? 0 : 1);
+  if (tail_piece && col0 == 0) {
+    // The run covers the start of every block it has a piece in but its first.
+    uint32_t pieces = 1;
+    for (int64_t q = b + 1;; q += kWarp) {
+      const int64_t i = (q + lane) * C;
+      const int more = __popc(__ballot_sync(kAll, i < n && a.places[i < n ? i : 0].key == last));
+      pieces += more;
+      if (more < kWarp) break;
+    }
+    if (lane == 0) a.long_runs[atomicAdd(a.n_long, 1u)] = LongRun{uint32_t(b), last, pieces, 0u};
+  }
+}
+
+// Adds the pieces of every long run, in order.  A CTA takes a slab of 128
+// columns and every gridDim.y-th long run: its warps add neighbouring shares
+// of the pieces (8 at least), and the first warp adds the warps' sums.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 128;
+
+__global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(
+    const __grid_constant__ GradArgs a) {
+  __shared__ float4 part[kJoinWarps][kWarp];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t col = int64_t(blockIdx.x) * kJoinCols + 4 * lane;  // slots: whole groups of 8
+  pdl_wait();
+  const uint32_t runs = *a.n_long;
+  for (uint32_t k = blockIdx.y; k < runs; k += gridDim.y) {
+    const LongRun run = a.long_runs[k];
+    const int64_t from = run.block, pieces = run.pieces;
+    int64_t share = (pieces + kJoinWarps - 1) / kJoinWarps;
+    if (share < 8) share = 8;
+    const int64_t p0 = warp * share, p1 = min(p0 + share, pieces);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (col < a.slot_dim) {
+#pragma unroll 8
+      for (int64_t p = p0; p < p1; ++p) {
+        const float4 v = *reinterpret_cast<const float4*>(
+            a.slots + (2 * (from + p) + (p == 0 ? 1 : 0)) * a.slot_dim + col);
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+    }
+    part[warp][lane] = acc;
+    __syncthreads();
+    if (warp == 0 && col < a.dim) {
+      for (int w = 1; w < kJoinWarps && w * share < pieces; ++w) {
+        const float4 v = part[w][lane];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+      }
+      const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col + i < a.dim) {
+          char* g = grad_at(a, run.row, col + i);
+          const float old = a.accumulate ? load1(g, a.out_type) : 0.0f;
+          store1(g, a.out_type, a.accumulate ? fmaf(a.scale, x[i], old) : a.scale * x[i]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- sorting
+// Stable radix sort of the positions by row, lowest digit first, up to 8 bits
+// a pass.  Keys are rows; tokens that add nothing have the key n_rows.
+
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / kWarp;
+constexpr int kDigits = 256;
+
+struct SortArgs {
+  const void* ids;
+  int64_t n, first_row, n_rows, padding;
+  Place* places;        // the result
+  uint32_t* n_long;     // the first kernel clears it
+  int32_t bits, passes;  // of the keys; digits of (bits + passes - 1) / passes bits
+};
+
+template <class ID>
+__device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
+  const ID id = static_cast<const ID*>(a.ids)[i];
+  const int64_t row = row_of(id, a.first_row, a.n_rows);
+  return row < 0 || int64_t(id) == a.padding ? uint32_t(a.n_rows) : uint32_t(row);
+}
+
+struct RankSmem {
+  uint16_t warp_count[kSortWarps][kDigits];
+  uint16_t part[4][kDigits];
+  uint32_t total[kDigits];
+  uint32_t base[kDigits];
+  uint32_t scan[kDigits / kWarp];
+};
+
+// Ranks of a CTA's elements among those of equal digit.  Element j of a lane
+// stands at place warp * 32 * ITEMS + 32 * j + lane of the CTA.  On return
+// rank[j] counts the equal digits before it in its warp, warp_count[w][d] those
+// in the warps before w, and total[d] those in the CTA.
+template <int ITEMS>
+__device__ __forceinline__ void rank_digits(RankSmem& s, const uint32_t (&digit)[ITEMS],
+                                            uint32_t (&rank)[ITEMS]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t* z = reinterpret_cast<uint32_t*>(s.warp_count[warp]);
+#pragma unroll
+  for (int i = 0; i < kDigits / 2 / kWarp; ++i) z[lane + kWarp * i] = 0u;
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j) {
+    const unsigned peers = __match_any_sync(kAll, digit[j]);
+    const int leader = __ffs(peers) - 1;
+    uint32_t old = 0;
+    if (lane == leader) {
+      old = s.warp_count[warp][digit[j]];
+      s.warp_count[warp][digit[j]] = uint16_t(old + __popc(peers));
+    }
+    __syncwarp();
+    rank[j] = __shfl_sync(kAll, old, leader) + __popc(peers & ((1u << lane) - 1u));
+  }
+  __syncthreads();
+  // Per digit, the exclusive sum over the warps: a quarter of them a thread.
+  constexpr int kQuarter = kSortWarps / 4;
+  const int d = threadIdx.x & (kDigits - 1), quarter = threadIdx.x / kDigits;
+  uint32_t sum = 0, got[kQuarter];
+#pragma unroll
+  for (int w = 0; w < kQuarter; ++w) {
+    got[w] = s.warp_count[quarter * kQuarter + w][d];
+    sum += got[w];
+  }
+  s.part[quarter][d] = uint16_t(sum);
+  __syncthreads();
+  uint32_t before = 0;
+  for (int q = 0; q < quarter; ++q) before += s.part[q][d];
+  if (quarter == 3) s.total[d] = before + sum;
+#pragma unroll
+  for (int w = 0; w < kQuarter; ++w) {
+    s.warp_count[quarter * kQuarter + w][d] = uint16_t(before);
+    before += got[w];
+  }
+}
+
+// base[d] = mine + sum of all[d'] over d' < d, for the first 256 threads; every
+// thread of the CTA calls it.
+__device__ __forceinline__ void digit_bases(RankSmem& s, uint32_t all, uint32_t mine) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = all;
+#pragma unroll
+  for (int o = 1; o < kWarp; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kAll, x, o);
+    if (lane >= o) x += y;
+  }
+  if (warp < kDigits / kWarp && lane == kWarp - 1) s.scan[warp] = x;
+  __syncthreads();
+  if (warp < kDigits / kWarp) {
+    uint32_t before = 0;
+    for (int w = 0; w < warp; ++w) before += s.scan[w];
+    s.base[threadIdx.x] = before + x - all + mine;
+  }
+  __syncthreads();
+}
+
+// Up to 16 * 1024 * ITEMS positions in one cluster: every CTA holds a tile of
+// 1024 * ITEMS elements, and the CTAs exchange their digit counts.  A CTA
+// first orders its tile by digit in its own shared memory, so that a warp then
+// stores neighbours to neighbours: into the tiles of the other CTAs (distributed
+// shared memory), on the last pass into global memory.  (Scattered straight
+// from the registers, 8 bytes at a time, two passes over 50,021 tokens took
+// 28.6 us.)
+constexpr int kSortCtas = 16;
+
+template <int ITEMS, class ID>
+__global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
+    const __grid_constant__ SortArgs a) {
+  constexpr int kTile = kSortThreads * ITEMS;
+  extern __shared__ __align__(16) unsigned char raw[];
+  RankSmem& s = *reinterpret_cast<RankSmem*>(raw);
+  Place* tile = reinterpret_cast<Place*>(raw + sizeof(RankSmem));
+  Place* ordered = tile + kTile;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int me = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_trigger();
+  if (me == 0 && threadIdx.x == 0) *a.n_long = 0u;
+  const int width = (a.bits + a.passes - 1) / a.passes;
+  const uint32_t mask = (1u << width) - 1u;
+  const int local0 = warp * (kWarp * ITEMS) + lane;
+  Place x[ITEMS];
+#pragma unroll
+  for (int j = 0; j < ITEMS; ++j) {
+    const int64_t i = int64_t(me) * kTile + local0 + kWarp * j;
+    // Behind the last token: the largest digits, so these stay behind it.
+    x[j].key = i < a.n ? key_of<ID>(a, i) : 0xffffffffu;
+    x[j].pos = uint32_t(i);
+  }
+  for (int p = 0; p < a.passes; ++p) {
+    if (p > 0) {
+#pragma unroll
+      for (int j = 0; j < ITEMS; ++j) x[j] = tile[local0 + kWarp * j];
+    }
+    uint32_t digit[ITEMS], rank[ITEMS];
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) digit[j] = (x[j].key >> (p * width)) & mask;
+    rank_digits<ITEMS>(s, digit, rank);
+    cluster.sync();  // the counts are there, and the tiles have been read
+    // Thread d: where digit d starts in this CTA's ordered tile, and how far
+    // from there its elements go.
+    uint32_t all = 0, mine = 0, own = 0;
+    if (threadIdx.x < kDigits) {
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t c = cluster.map_shared_rank(s.total, r)[threadIdx.x];
+        if (r < me) mine += c;
+        all += c;
+      }
+      own = s.total[threadIdx.x];
+    }
+    digit_bases(s, own, 0u);
+    const uint32_t start = threadIdx.x < kDigits ? s.base[threadIdx.x] : 0u;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j)
+      ordered[s.base[digit[j]] + s.warp_count[warp][digit[j]] + rank[j]] = x[j];
+    __syncthreads();
+    digit_bases(s, all, mine - start);
+    const bool out = p == a.passes - 1;
+#pragma unroll
+    for (int j = 0; j < ITEMS; ++j) {
+      const int i = threadIdx.x + kSortThreads * j;
+      const Place y = ordered[i];
+      const uint32_t to = s.base[(y.key >> (p * width)) & mask] + uint32_t(i);
+      if (!out) cluster.map_shared_rank(tile, int(to / kTile))[to % kTile] = y;
+      else if (to < a.n) a.places[to] = y;
+    }
+    cluster.sync();  // the tiles are written, and the counts have been read
+  }
+}
+
+// More positions than a cluster holds: three kernels a pass.  Counts of every
+// tile's digits; their sums over the tiles, a CTA a digit; and the scatter.
+constexpr int kTileItems = 4;
+constexpr int kGlobalTile = kSortThreads * kTileItems;
+
+struct PassArgs {
+  SortArgs s;
+  const Place* in;  // NULL: from the ids
+  Place* out;
+  uint32_t* counts;  // [digit][tile]
+  uint32_t* totals;  // [digit]
+  int64_t tiles;
+  int32_t shift, width;
+};
+
+template <class ID>
+__device__ __forceinline__ void load_tile(const PassArgs& a, Place (&x)[kTileItems],
+                                          uint32_t (&digit)[kTileItems]) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < kTileItems; ++j) {
+    const int64_t i = int64_t(blockIdx.x) * kGlobalTile + warp * (kWarp * kTileItems) +
+                      kWarp * j + lane;
+    x[j] = Place{0xffffffffu, 0u};
+    if (i < a.s.n) x[j] = a.in ? a.in[i] : Place{key_of<ID>(a.s, i), uint32_t(i)};
+    digit[j] = (x[j].key >> a.shift) & ((1u << a.width) - 1u);
+  }
+}
+
+template <class ID>
+__global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_constant__ PassArgs a) {
+  __shared__ RankSmem s;
+  Place x[kTileItems];
+  uint32_t digit[kTileItems], rank[kTileItems];
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.s.n_long = 0u;
+  load_tile<ID>(a, x, digit);
+  rank_digits<kTileItems>(s, digit, rank);
+  __syncthreads();
+  if (threadIdx.x < kDigits) a.counts[threadIdx.x * a.tiles + blockIdx.x] = s.total[threadIdx.x];
+}
+
+__global__ void __launch_bounds__(kSortThreads) scan_kernel(const __grid_constant__ PassArgs a) {
+  __shared__ uint32_t sums[kSortWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t* c = a.counts + blockIdx.x * a.tiles;
+  uint32_t carry = 0;
+  for (int64_t t0 = 0; t0 < a.tiles; t0 += kSortThreads) {
+    const int64_t t = t0 + threadIdx.x;
+    const uint32_t v = t < a.tiles ? c[t] : 0u;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < kWarp; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(kAll, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == kWarp - 1) sums[warp] = x;
+    __syncthreads();
+    uint32_t before = carry, all = 0;
+    for (int w = 0; w < kSortWarps; ++w) {
+      if (w < warp) before += sums[w];
+      all += sums[w];
+    }
+    if (t < a.tiles) c[t] = before + x - v;
+    carry += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.totals[blockIdx.x] = carry;
+}
+
+template <class ID>
+__global__ void __launch_bounds__(kSortThreads) scatter_kernel(
+    const __grid_constant__ PassArgs a) {
+  __shared__ RankSmem s;
+  Place x[kTileItems];
+  uint32_t digit[kTileItems], rank[kTileItems];
+  load_tile<ID>(a, x, digit);
+  rank_digits<kTileItems>(s, digit, rank);
+  uint32_t all = 0, mine = 0;
+  if (threadIdx.x < kDigits) {
+    all = a.totals[threadIdx.x];
+    mine = a.counts[threadIdx.x * a.tiles + blockIdx.x];
+  }
+  digit_bases(s, all, mine);
+  const int warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int j = 0; j < kTileItems; ++j) {
+    const uint32_t to = s.base[digit[j]] + s.warp_count[warp][digit[j]] + rank[j];
+    if (to < a.s.n) a.out[to] = x[j];
+  }
+}
+
+// sum_kernel by the type of dy, the columns a lane holds and the alignment.
+using SumKernel = void (*)(GradArgs);
+const SumKernel sum_kernels[3][2][2] = {
+    {{sum_kernel<TRAIN_BF16, 8, false>, sum_kernel<TRAIN_BF16, 8, true>},
+     {sum_kernel<TRAIN_BF16, 16, false>, sum_kernel<TRAIN_BF16, 16, true>}},
+    {{sum_kernel<TRAIN_FP16, 8, false>, sum_kernel<TRAIN_FP16, 8, true>},
+     {sum_kernel<TRAIN_FP16, 16, false>, sum_kernel<TRAIN_FP16, 16, true>}},
+    {{sum_kernel<TRAIN_FP32, 8, false>, sum_kernel<TRAIN_FP32, 8, true>}, {nullptr, nullptr}}};
+
+// Every row starts at a multiple of 16 bytes.
+bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size_of(dtype) % 16 == 0;
+}
+
+// Zeros written while the tokens are being sorted.
+#ifndef KFB
+#define KFB 48e6
+#endif
+#ifndef KFE
+#define KFE 64e3
+#endif
+constexpr double kFillBytes = KFB;
+
+constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
+
+// How the gradient's work is cut; depends on the sizes alone.
+struct GradPlan {
+  int64_t block, n_blocks, slot_dim, tiles;
+  int64_t places, places2, counts, totals, n_long, long_runs, named, slots, bytes;  // in the workspace
+};
+
+GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
+  GradPlan p{};
+  // Blocks of 128 positions where they make work for 4096 warps, else fewer.
+  const int64_t slabs = (dim + 511) / 512;
+  p.block = kMaxBlock;
+  while (p.block > 16 && n / p.block * slabs < KU) p.block /= 2;
+  p.n_blocks = (n + p.block - 1) / p.block;
+  p.slot_dim = (dim + 7) / 8 * 8;
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += (bytes + 255) / 256 * 256;
+    return here;
+  };
+  p.places = take(int64_t(sizeof(Place)) * n);
+  if (n > kClusterCapacity) {
+    p.tiles = (n + kGlobalTile - 1) / kGlobalTile;
+    p.places2 = take(int64_t(sizeof(Place)) * n);
+    p.counts = take(4 * kDigits * p.tiles);
+    p.totals = take(4 * kDigits);
+  }
+  p.n_long = take(4);
+  p.long_runs = take(int64_t(sizeof(LongRun)) * (p.n_blocks / 2 + 1));
+  p.named = take(4 * ((n_rows + 31) / 32));
+  p.slots = at;
+  if (n > 2 * p.block) take(2 * p.n_blocks * p.slot_dim * 4);
+  p.bytes = at;
+  return p;
+}
+
+template <int ITEMS, class ID>
+cudaError_t launch_cluster_sort(const SortArgs& a, cudaStream_t s) {
+  constexpr int kTile = kSortThreads * ITEMS;
+  constexpr int kSmem = int(sizeof(RankSmem)) + 2 * int(sizeof(Place)) * kTile;
+  int ctas = 1;
+  while (int64_t(ctas) * kTile < a.n) ctas *= 2;
+  // What a kernel has to be told once per device; it costs less than a launch,
+  // so it is told every time.
+  cudaError_t ce = cudaSuccess;
+  if (kSmem > 48 * 1024)
+    ce = cudaFuncSetAttribute(cluster_sort_kernel<ITEMS, ID>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (ce == cudaSuccess && ctas > 8)
+    ce = cudaFuncSetAttribute(cluster_sort_kernel<ITEMS, ID>,
+                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (ce != cudaSuccess) return ce;
+  return launch(cluster_sort_kernel<ITEMS, ID>, dim3(unsigned(ctas)), kSortThreads, kSmem, s,
+                false, ctas, a);
+}
+
+template <class ID>
+cudaError_t launch_sort(const SortArgs& a, const GradPlan& p, char* ws, cudaStream_t s) {
+  // As many CTAs as the cluster takes, so that each has few elements to rank
+  // and to store.
+  if (a.n <= kSortCtas * kSortThreads) return launch_cluster_sort<1, ID>(a, s);
+  if (a.n <= kSortCtas * kSortThreads * 2) return launch_cluster_sort<2, ID>(a, s);
+  if (a.n <= kSortCtas * kSortThreads * 4) return launch_cluster_sort<4, ID>(a, s);
+  if (a.n <= kClusterCapacity) return launch_cluster_sort<8, ID>(a, s);
+  // The last pass writes to places.
+  Place* q[2] = {a.places, reinterpret_cast<Place*>(ws + p.places2)};
+  PassArgs b{};
+  b.s = a;
+  b.counts = reinterpret_cast<uint32_t*>(ws + p.counts);
+  b.totals = reinterpret_cast<uint32_t*>(ws + p.totals);
+  b.tiles = p.tiles;
+  b.width = (a.bits + a.passes - 1) / a.passes;
+  for (int i = 0; i < a.passes; ++i) {
+    const int to = (a.passes - 1 - i) & 1;
+    b.in = i == 0 ? nullptr : q[to ^ 1];
+    b.out = q[to];
+    b.shift = i * b.width;
+    const dim3 grid{unsigned(p.tiles)};
+    cudaError_t ce = launch(count_kernel<ID>, grid, kSortThreads, 0, s, false, 1, b);
+    if (ce == cudaSuccess) ce = launch(scan_kernel, dim3(kDigits), kSortThreads, 0, s, false, 1, b);
+    if (ce == cudaSuccess)
+      ce = launch(scatter_kernel<ID>, grid, kSortThreads, 0, s, false, 1, b);
+    if (ce != cudaSuccess) return ce;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+
+LAMB_API int train_embed_grad_workspace(int64_t n_ids, int64_t n_rows, int64_t dim,
+                                        int64_t* bytes) {
+  lambgb::set_last_error("");
+  if (!bytes) return fail(LAMB_ERR_INVALID, "bytes is NULL");
+  if (n_ids < 0 || n_rows < 0 || dim < 0 || n_ids > kMaxCount || n_rows > kMaxCount ||
+      dim > kMaxCount)
+    return fail(LAMB_ERR_INVALID, "sizes must be in [0, 2^31 - 1]");
+  *bytes = grad_plan(n_ids, n_rows, dim).bytes;
+  return LAMB_OK;
+}
+
+LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
+                              int64_t grad_out_stride, const void* ids, int32_t ids_dtype,
+                              int64_t n_ids, int64_t first_row, int64_t padding_id, float scale,
+                              int32_t accumulate, void* grad, int32_t grad_dtype,
+                              int64_t n_rows, int64_t dim, int64_t grad_stride, void* workspace,
+                              int64_t workspace_bytes, void* stream) {
+  lambgb::set_last_error("");
+  int rc = check_ids(ids, ids_dtype, n_ids, first_row);
+  if (rc == LAMB_OK)
+    rc = check_matrix("grad_out", grad_out, grad_out_dtype, n_ids, dim, grad_out_stride);
+  if (rc == LAMB_OK) rc = check_matrix("grad", grad, grad_dtype, n_rows, dim, grad_stride);
+  if (rc != LAMB_OK) return rc;
+  if (accumulate != 0 && accumulate != 1)
+    return fail(LAMB_ERR_INVALID, "accumulate must be 0 or 1");
+  int64_t need = 0;
+  rc = train_embed_grad_workspace(n_ids, n_rows, dim, &need);
+  if (rc != LAMB_OK) return rc;
+  if (workspace_bytes < need || (need > 0 && !workspace))
+    return fail(LAMB_ERR_INVALID, "workspace: " + std::to_string(need) + " bytes are needed");
+  if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16)
+    return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
+  if (n_rows == 0 || dim == 0 || (accumulate && n_ids == 0)) return LAMB_OK;
+  const GradPlan p = grad_plan(n_ids, n_rows, dim);
+  char* ws = static_cast<char*>(workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t ce = cudaSuccess;
+  GradArgs a{};
+  a.dy = grad_out;
+  a.grad = grad;
+  a.ids = ids;
+  a.first_row = first_row;
+  a.padding = padding_id;
+  a.places = reinterpret_cast<const Place*>(ws + p.places);
+  a.slots = reinterpret_cast<float*>(ws + p.slots);
+  a.n_long = reinterpret_cast<uint32_t*>(ws + p.n_long);
+  a.long_runs = reinterpret_cast<LongRun*>(ws + p.long_runs);
+  a.named = reinterpret_cast<uint32_t*>(ws + p.named);
+  a.dy_stride = grad_out_stride;
+  a.grad_stride = grad_stride;
+  a.n_rows = n_rows;
+  a.dim = dim;
+  a.slot_dim = p.slot_dim;
+  a.n = n_ids;
+  a.n_blocks = p.n_blocks;
+  a.block = int32_t(p.block);
+  a.scale = scale;
+  a.accumulate = accumulate;
+  a.out_type = grad_dtype;
+  if (n_ids > 0) {
+    SortArgs t{};
+    t.ids = ids;
+    t.n = n_ids;
+    t.first_row = first_row;
+    t.n_rows = n_rows;
+    t.padding = padding_id;
+    t.places = reinterpret_cast<Place*>(ws + p.places);
+    t.n_long = reinterpret_cast<uint32_t*>(ws + p.n_long);
+    while ((n_rows >> t.bits) != 0) ++t.bits;  // the largest key is n_rows
+    t.passes = (t.bits + 7) / 8;
+    ce = ids_dtype == TRAIN_INT64 ? launch_sort<int64_t>(t, p, ws, s)
+                                  : launch_sort<int32_t>(t, p, ws, s);
+    if (ce != cudaSuccess)
+      return fail(LAMB_ERR_CUDA, std::string("sorting the tokens: ") + cudaGetErrorString(ce));
+  }
+  if (!accumulate) {
+    // Ids are read by every CTA, which the sort hides, unless there are too
+    // many of them or of the CTAs.
+    int64_t ctas = 304;
+    while (n_rows > ctas * kFillRows) ctas *= 2;
+    a.rows_per_cta = ((n_rows + ctas - 1) / ctas + 31) / 32 * 32;
+    ctas = (n_rows + a.rows_per_cta - 1) / a.rows_per_cta;
+    const bool scan = n_ids <= kClusterCapacity && ctas <= 304;
+    a.fill_first = a.rows_per_cta;
+    if (scan && n_ids > 0) {
+      // What is written while the tokens are sorted; the rest among the sums.
+      const double row_bytes = double(dim) * size_of(grad_dtype);
+      const double part = kFillBytes / (double(n_rows) * row_bytes);
+      if (part < 1.0) a.fill_first = int64_t(part * double(a.rows_per_cta));
+      const int64_t most = int64_t(512e3 / row_bytes) + 1;  // of one CTA
+      if (a.fill_first > most) a.fill_first = most;
+      if (a.fill_first > a.rows_per_cta) a.fill_first = a.rows_per_cta;
+      a.fill_rest = ctas * (a.rows_per_cta - a.fill_first);
+      a.fill_each = int64_t(KFE / row_bytes) + 1;
+      a.fill_ctas = uint32_t((a.fill_rest + a.fill_each - 1) / a.fill_each);
+    }
+    const auto kernel = !scan ? fill_kernel<false, int32_t>
+                        : ids_dtype == TRAIN_INT64 ? fill_kernel<true, int64_t>
+                                                   : fill_kernel<true, int32_t>;
+    ce = launch(kernel, dim3(unsigned(ctas)), kFillThreads, 0, s, n_ids > 0, 1, a);
+  }
+  if (ce == cudaSuccess && n_ids > 0) {
+    const bool wide = grad_out_dtype == TRAIN_FP32 || (accumulate && grad_dtype == TRAIN_FP32);
+    const bool aligned = dim % 8 == 0 &&
+                         rows_aligned16(grad_out, grad_out_dtype, grad_out_stride) &&
+                         rows_aligned16(grad, grad_dtype, grad_stride);
+    const int64_t slab = wide ? 8 * kWarp : 16 * kWarp;
+    a.slabs = int32_t((dim + slab - 1) / slab);
+    a.units = p.n_blocks * a.slabs;
+    const int64_t ctas = (a.units + kSumWarps - 1) / kSumWarps + a.fill_ctas;
+    if (ctas > kMaxCount) return fail(LAMB_ERR_INVALID, "n_ids * dim is too large");
+    const SumKernel kernel = sum_kernels[grad_out_dtype][wide ? 0 : 1][aligned ? 1 : 0];
+    ce = launch(kernel, dim3(unsigned(ctas)), kSumWarps * kWarp, kSumWarps * sizeof(WarpSmem), s,
+                true, 1, a);
+  }
+  if (ce == cudaSuccess && n_ids > 2 * p.block) {
+    // A CTA for every 128 columns, and enough in all to fill the GPU.
+    const int64_t x = (dim + kJoinCols - 1) / kJoinCols;
+    int64_t y = x >= 1216 ? 1 : 1216 / x;
+    if (y > p.n_blocks / 2) y = p.n_blocks / 2 > 0 ? p.n_blocks / 2 : 1;
+    ce = launch(join_kernel, dim3(unsigned(x), unsigned(y)), kJoinWarps * kWarp, 0, s, true, 1, a);
+  }
+  return ce == cudaSuccess
+             ? LAMB_OK
+             : fail(LAMB_ERR_CUDA, std::string("embed_grad: ") + cudaGetErrorString(ce));
+}
+
+}  // extern "C"

@@ -7,7 +7,9 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <string>
 
+#include "lamb_internal.h"
 #include "train_ops.h"
 
 namespace traingb {
@@ -42,6 +44,89 @@ __device__ __forceinline__ typename TypeOf<DT>::T from_float(float x) {
   if constexpr (DT == TRAIN_BF16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
   if constexpr (DT == TRAIN_FP16) return __half_as_ushort(__float2half_rn(x));
   if constexpr (DT == TRAIN_FP32) return x;
+}
+
+// Lets the kernel behind this one start (its CTAs wait for this one to end
+// before they touch what it writes), and waits for the kernel in front.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+constexpr int kWarp = 32;
+constexpr unsigned kAll = 0xffffffffu;
+
+// Row of the table (or of its gradient) that a token names, or -1.
+template <class ID>
+__device__ __forceinline__ int64_t row_of(ID id, int64_t first_row, int64_t n_rows) {
+  const uint64_t r = uint64_t(int64_t(id)) - uint64_t(first_row);
+  return r < uint64_t(n_rows) ? int64_t(r) : -1;
+}
+
+// ------------------------------------------------------------------- host
+inline int fail(int code, const std::string& msg) {
+  lambgb::set_last_error(msg);
+  return code;
+}
+
+constexpr int64_t kMaxCount = 0x7fffffff;
+
+// Checks one matrix; LAMB_OK or the error.
+inline int check_matrix(const char* name, const void* p, int32_t dtype, int64_t rows, int64_t dim,
+                 int64_t stride) {
+  if (dtype != TRAIN_BF16 && dtype != TRAIN_FP16 && dtype != TRAIN_FP32)
+    return fail(LAMB_ERR_INVALID, std::string(name) + ": unknown element type");
+  if (rows < 0 || dim < 0 || rows > kMaxCount || dim > kMaxCount)
+    return fail(LAMB_ERR_INVALID, std::string(name) + ": sizes must be in [0, 2^31 - 1]");
+  if (stride < dim)
+    return fail(LAMB_ERR_INVALID, std::string(name) + ": stride is less than dim");
+  if (rows == 0 || dim == 0) return LAMB_OK;
+  if (!p) return fail(LAMB_ERR_INVALID, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % uintptr_t(size_of(dtype)))
+    return fail(LAMB_ERR_ALIGN, std::string(name) + " is not aligned to its element type");
+  return LAMB_OK;
+}
+
+inline int check_ids(const void* ids, int32_t ids_dtype, int64_t n_ids, int64_t first_row) {
+  if (ids_dtype != TRAIN_INT32 && ids_dtype != TRAIN_INT64)
+    return fail(LAMB_ERR_INVALID, "ids: unknown type");
+  if (n_ids < 0 || n_ids > kMaxCount)
+    return fail(LAMB_ERR_INVALID, "n_ids must be in [0, 2^31 - 1]");
+  if (first_row < 0) return fail(LAMB_ERR_INVALID, "first_row must be >= 0");
+  if (n_ids == 0) return LAMB_OK;
+  if (!ids) return fail(LAMB_ERR_INVALID, "ids is NULL");
+  if (reinterpret_cast<uintptr_t>(ids) % (ids_dtype == TRAIN_INT64 ? 8u : 4u))
+    return fail(LAMB_ERR_ALIGN, "ids is not aligned to its type");
+  return LAMB_OK;
+}
+
+// Launches a kernel, if asked as a programmatic dependent of the one before
+// it in the stream, in clusters of `cluster` CTAs.
+template <class... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                   bool dependent, int cluster, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  int k = 0;
+  if (dependent) {
+    attr[k].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[k++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    attr[k].id = cudaLaunchAttributeClusterDimension;
+    attr[k].val.clusterDim.x = unsigned(cluster);
+    attr[k].val.clusterDim.y = 1;
+    attr[k++].val.clusterDim.z = 1;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = unsigned(k);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 }  // namespace traingb

@@ -7,6 +7,7 @@ but their result and workspace through torch, and never wait for the GPU.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -18,29 +19,31 @@ _TYPES = {torch.bfloat16: _lib.TRAIN_BF16, torch.float16: _lib.TRAIN_FP16,
 _ID_TYPES = {torch.int32: _lib.TRAIN_INT32, torch.int64: _lib.TRAIN_INT64}
 
 
-def _matrix(name, t, device):
-    """(type, dim, row stride) of a tensor whose last dimension is dense and
-    whose leading ones step evenly from row to row."""
+def _code(name, t, codes, device):
+    """Code of a tensor's type, after the checks that every argument gets."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
-    code = _TYPES.get(t.dtype)
+    code = codes.get(t.dtype)
     if code is None:
-        raise TypeError(f"{name}: expected bfloat16, float16 or float32, got {t.dtype}")
+        raise TypeError(f"{name}: expected {', '.join(map(str, codes))}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
-    shape = t.shape
-    if not shape:
-        raise ValueError(f"{name}: needs at least one dimension")
-    dim = shape[-1]
+    return code
+
+
+def _row_stride(name, t):
+    """Elements from one row to the next of a tensor whose last dimension is
+    dense and whose leading ones step evenly from row to row."""
+    dim = t.shape[-1]
     if t.is_contiguous():
-        return code, dim, dim
+        return dim
     if dim > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: the last dimension must be dense")
-    stride = None  # of one row to the next
-    span = 1       # rows below the dimension looked at
-    for n, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+    stride = None
+    span = 1  # rows below the dimension looked at
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 0:
-            return code, dim, dim
+            return dim
         if n == 1:
             continue
         if stride is None:
@@ -49,32 +52,36 @@ def _matrix(name, t, device):
             raise ValueError(f"{name}: rows must step evenly through its leading dimensions")
         span *= n
     if stride is None:
-        stride = dim
+        return dim
     if stride < dim:
         raise ValueError(f"{name}: rows overlap")
-    return code, dim, stride
+    return stride
 
 
-def _token_ids(ids, device):
-    if not isinstance(ids, torch.Tensor):
-        raise TypeError("ids: expected a tensor")
-    code = _ID_TYPES.get(ids.dtype)
-    if code is None:
-        raise TypeError(f"ids: expected int32 or int64, got {ids.dtype}")
-    if ids.device != device:
-        raise ValueError(f"ids: on {ids.device}, expected {device}")
+def _ids_code(ids, device):
+    code = _code("ids", ids, _ID_TYPES, device)
     if not ids.is_contiguous():
         raise ValueError("ids: must be contiguous")
     return code
 
 
-def _on_device(device, call):
-    """Makes ``call(stream)`` with ``device`` current and its current stream."""
-    if device.index == torch.cuda.current_device():
-        check(call(torch.cuda.current_stream().cuda_stream))
+def _enqueue(device, call, *args):
+    """``call(*args, stream)`` with ``device`` current, on its current stream."""
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            check(call(torch.cuda.current_stream().cuda_stream))
+            rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc:
+        check(rc)
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(n_ids, n_rows, dim):
+    need = ctypes.c_int64()
+    check(_lib.load().train_embed_grad_workspace(n_ids, n_rows, dim, ctypes.byref(need)))
+    return need.value
 
 
 def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_row: int = 0,
@@ -90,19 +97,25 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise TypeError("table: expected a tensor of two dimensions")
     device = table.device
-    if device.type != "cuda":
+    if not table.is_cuda:
         raise ValueError("table: must live on a CUDA device")
-    t_code, dim, t_stride = _matrix("table", table, device)
-    i_code = _token_ids(ids, device)
+    t_code = _code("table", table, _TYPES, device)
+    i_code = _ids_code(ids, device)
+    rows, dim = table.shape
+    t_stride = _row_stride("table", table)
     shape = ids.shape + (dim,)
     if out is None:
         out = torch.empty(shape, dtype=out_dtype or table.dtype, device=device)
-    elif out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
-        raise ValueError(f"out: expected shape {tuple(shape)} and out_dtype's type")
-    o_code, _, o_stride = _matrix("out", out, device)
-    _on_device(device, lambda stream: _lib.load().train_embed(
-        table.data_ptr(), t_code, table.shape[0], dim, t_stride, ids.data_ptr(), i_code,
-        ids.numel(), first_row, scale, out.data_ptr(), o_code, o_stride, stream))
+        o_code = _code("out", out, _TYPES, device)
+        o_stride = dim
+    else:
+        o_code = _code("out", out, _TYPES, device)
+        if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out: expected shape {tuple(shape)} and out_dtype's type")
+        o_stride = _row_stride("out", out)
+    _enqueue(device, _lib.load().train_embed, table.data_ptr(), t_code, rows, dim, t_stride,
+             ids.data_ptr(), i_code, ids.numel(), first_row, scale, out.data_ptr(), o_code,
+             o_stride)
     return out
 
 
@@ -120,14 +133,16 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
     as they are.  Tokens outside the slice that starts at ``first_row``, and
     ``padding_id`` (negative: none), add nothing.
     """
-    if not isinstance(grad_out, torch.Tensor):
-        raise TypeError("grad_out: expected a tensor")
+    if not isinstance(grad_out, torch.Tensor) or grad_out.dim() == 0:
+        raise TypeError("grad_out: expected a tensor of one dimension or more")
     device = grad_out.device
-    if device.type != "cuda":
+    if not grad_out.is_cuda:
         raise ValueError("grad_out: must live on a CUDA device")
-    g_code, dim, g_stride = _matrix("grad_out", grad_out, device)
-    i_code = _token_ids(ids, device)
-    if grad_out.shape != ids.shape + (dim,):
+    g_code = _code("grad_out", grad_out, _TYPES, device)
+    i_code = _ids_code(ids, device)
+    dim = grad_out.shape[-1]
+    g_stride = _row_stride("grad_out", grad_out)
+    if grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out: expected ids.shape + (dim,)")
     if out is None:
         if n_rows is None:
@@ -135,23 +150,20 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((n_rows, dim), dtype=dtype or grad_out.dtype, device=device)
-    elif (out.dim() != 2 or out.shape[1] != dim or n_rows not in (None, out.shape[0])
-          or (dtype is not None and out.dtype != dtype)):
-        raise ValueError("out: expected [n_rows, dim] of dtype's type")
-    o_code, _, o_stride = _matrix("out", out, device)
-    lib = _lib.load()
+        o_code = _code("out", out, _TYPES, device)
+        o_stride = dim
+    else:
+        o_code = _code("out", out, _TYPES, device)
+        if (out.dim() != 2 or out.shape[1] != dim or n_rows not in (None, out.shape[0])
+                or (dtype is not None and out.dtype != dtype)):
+            raise ValueError("out: expected [n_rows, dim] of dtype's type")
+        o_stride = _row_stride("out", out)
     n_ids, rows = ids.numel(), out.shape[0]
-    need = ctypes.c_int64()
-    check(lib.train_embed_grad_workspace(n_ids, rows, dim, ctypes.byref(need)))
-
-    def call(stream):
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=device)
-        return lib.train_embed_grad(
-            grad_out.data_ptr(), g_code, g_stride, ids.data_ptr(), i_code, n_ids, first_row,
-            padding_id, scale, 1 if accumulate else 0, out.data_ptr(), o_code, rows, dim,
-            o_stride, workspace.data_ptr(), need.value, stream)
-
-    _on_device(device, call)
+    need = _workspace_bytes(n_ids, rows, dim)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    _enqueue(device, _lib.load().train_embed_grad, grad_out.data_ptr(), g_code, g_stride,
+             ids.data_ptr(), i_code, n_ids, first_row, padding_id, scale, 1 if accumulate else 0,
+             out.data_ptr(), o_code, rows, dim, o_stride, workspace.data_ptr(), need)
     return out
 
 
