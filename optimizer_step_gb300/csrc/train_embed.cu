@@ -19,64 +19,6 @@ struct EmbedArgs {
   int32_t ids64;
 };
 
-// VEC neighbouring elements, aligned to their size together or to 16 bytes.
-template <int DT, int VEC>
-struct Pack {
-  using T = typename TypeOf<DT>::T;
-  static constexpr int kBytes = VEC * int(sizeof(T));
-  uint32_t w[(kBytes + 3) / 4];
-
-  __device__ __forceinline__ void load(const T* p) {
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(p) + i);
-        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-      }
-    } else if constexpr (kBytes == 8) {
-      const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-      w[0] = q.x, w[1] = q.y;
-    } else if constexpr (kBytes == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    } else {
-      w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
-    }
-  }
-  __device__ __forceinline__ void store(T* p) const {
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i)
-        reinterpret_cast<uint4*>(p)[i] =
-            make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else if constexpr (kBytes == 8) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-    } else if constexpr (kBytes == 4) {
-      *reinterpret_cast<uint32_t*>(p) = w[0];
-    } else {
-      *reinterpret_cast<uint16_t*>(p) = uint16_t(w[0]);
-    }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < (kBytes + 3) / 4; ++i) w[i] = 0u;
-  }
-  __device__ __forceinline__ float get(int i) const {
-    if constexpr (DT == TRAIN_FP32) {
-      return __uint_as_float(w[i]);
-    } else {
-      return to_float<DT>(uint16_t((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu));
-    }
-  }
-  __device__ __forceinline__ void set(int i, float x) {
-    if constexpr (DT == TRAIN_FP32) {
-      w[i] = __float_as_uint(x);
-    } else {
-      const uint32_t h = from_float<DT>(x);
-      w[i / 2] = (i & 1) ? w[i / 2] | h << 16 : h;
-    }
-  }
-};
-
 // A warp takes R rows of the output and M times 32 units of VEC elements of
 // each: it reads the ids, then the units, all on their way together, and
 // writes them.  R is 1 where a row has more than 32 units.  A warp has one
