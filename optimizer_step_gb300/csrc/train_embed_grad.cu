@@ -225,7 +225,7 @@ __device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
 // of the grad that accumulation needs come through the same ring behind the
 // last row of their run: nothing waits for them when the run is finished.
 #ifndef KST
-#define KST 8
+#define KST 6
 #endif
 #ifndef KSW
 #define KSW 4
@@ -321,10 +321,10 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
   const auto ends = [&](int i) { return s.key[i] != s.key[i + 1]; };
   const auto is_head = [&](uint32_t key) { return head_piece && key == first; };
 
-  // Starts the copy of the piece [col0, col0 + cols) of a row at `row`.
-  const auto copy_piece = [&](unsigned char* dst, const char* row, int size, const char* begin,
+  // Starts the copy of this slab's piece of a row; src: its first byte.  [begin,
+  // limit) is all that belongs to the matrix.
+  const auto copy_piece = [&](unsigned char* dst, const char* src, int size, const char* begin,
                               const char* limit) {
-    const char* src = row + col0 * size;
     if constexpr (ALIGNED) {
 #pragma unroll
       for (int g = 0; g < COLS / 8; ++g) {
@@ -337,23 +337,33 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
     } else {
       const int shift = int(reinterpret_cast<uintptr_t>(src) & 15);
       const int granules = (shift + cols * size + 15) / 16;
-      for (int g = lane; g < granules; g += kWarp) {
-        const char* q = src - shift + 16 * g;
+      const char* q = src - shift + 16 * lane;
+      dst += 16 * lane;
+      if (src - shift >= begin && src - shift + 16 * granules <= limit) {
+        // At most 65 of them.
+        if (lane < granules) copy16(dst, q, 16);
+        if (lane + kWarp < granules) copy16(dst + 16 * kWarp, q + 16 * kWarp, 16);
+        if (lane + 2 * kWarp < granules) copy16(dst + 32 * kWarp, q + 32 * kWarp, 16);
+        return;
+      }
+      for (int g = lane; g < granules; g += kWarp, q += 16 * kWarp, dst += 16 * kWarp) {
         if (q >= begin) {
           const int64_t left = limit - q;
-          copy16(dst + 16 * g, q, left < 16 ? int(left) : 16);
+          copy16(dst, q, left < 16 ? int(left) : 16);
         } else {
           // In front of the matrix: only what belongs to it.
           for (int i = int(begin - q); i < 16; i += 2)
             if (q + i < limit)
-              *reinterpret_cast<uint16_t*>(dst + 16 * g + i) =
-                  *reinterpret_cast<const uint16_t*>(q + i);
+              *reinterpret_cast<uint16_t*>(dst + i) = *reinterpret_cast<const uint16_t*>(q + i);
         }
       }
     }
   };
-  const char* const dy_limit = dy + ((n - 1) * a.dy_stride + a.dim) * size_of(IN);
-  const char* const grad_limit = grad + ((a.n_rows - 1) * a.grad_stride + a.dim) * out_size;
+  const int64_t dy_step = a.dy_stride * size_of(IN), grad_step = a.grad_stride * out_size;
+  const char* const dy_slab = dy + col0 * size_of(IN);
+  char* const grad_slab = grad + col0 * out_size;
+  const char* const dy_limit = dy + (n - 1) * dy_step + a.dim * size_of(IN);
+  const char* const grad_limit = grad + (a.n_rows - 1) * grad_step + a.dim * out_size;
 
   // The next piece to fetch: position at, or the old row behind it.
   int at = x;
@@ -361,20 +371,20 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
   const auto fetch = [&](int stage) {
     if (at < stop) {
       if (!old_next) {
-        copy_piece(s.ring[stage], dy + int64_t(s.pos[at]) * a.dy_stride * size_of(IN),
-                   size_of(IN), dy, dy_limit);
+        copy_piece(s.ring[stage], dy_slab + s.pos[at] * dy_step, size_of(IN), dy, dy_limit);
         old_next = a.accumulate && ends(at) && !is_head(s.key[at]);
         if (!old_next) ++at;
       } else {
-        copy_piece(s.ring[stage], grad_at(a, s.key[at], 0), out_size, grad, grad_limit);
+        copy_piece(s.ring[stage], grad_slab + s.key[at] * grad_step, out_size, grad, grad_limit);
         old_next = false;
         ++at;
       }
     }
     copy_commit();
   };
-  // A lane's values of the piece in a stage; `row` gives its alignment.
-  const auto read_piece = [&](int stage, const char* row, auto t, float (&v)[COLS]) {
+  // A lane's values of the piece in a stage.  Unaligned: it starts `low` bytes
+  // (modulo 16) into its first granule.
+  const auto read_piece = [&](int stage, uint32_t low, auto t, float (&v)[COLS]) {
     constexpr int type = decltype(t)::value;
     if constexpr (ALIGNED) {
 #pragma unroll
@@ -385,12 +395,13 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
         for (int i = 0; i < 8; ++i) v[8 * g + i] = u[i];
       }
     } else {
-      const int shift = int(reinterpret_cast<uintptr_t>(row + col0 * size_of(type)) & 15);
+      const unsigned char* p = s.ring[stage] + (low & 15u) + lane * size_of(type);
 #pragma unroll
-      for (int i = 0; i < COLS; ++i)
-        v[i] = load1(s.ring[stage] + shift + (lane + kWarp * i) * size_of(type), type);
+      for (int i = 0; i < COLS; ++i) v[i] = load1(p + kWarp * i * size_of(type), type);
     }
   };
+  const uint32_t dy_low = uint32_t(reinterpret_cast<uintptr_t>(dy_slab));
+  const uint32_t grad_low = uint32_t(reinterpret_cast<uintptr_t>(grad_slab));
 
   for (int i = 0; i < kStages - 1; ++i) fetch(i);
   float acc[COLS];
@@ -428,7 +439,7 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
   for (; x < stop; ++x) {
     next_stage();
     float v[COLS];
-    read_piece(stage, dy + int64_t(s.pos[x]) * a.dy_stride * size_of(IN), Type<IN>{}, v);
+    read_piece(stage, dy_low + s.pos[x] * uint32_t(dy_step), Type<IN>{}, v);
     done_stage();
 #pragma unroll
     for (int i = 0; i < COLS; ++i) acc[i] += v[i];
@@ -437,10 +448,11 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
     if (is_head(key)) {
       write_slot(0);
     } else {
-      char* row = grad_at(a, key, 0);
       if (a.accumulate) {
         next_stage();
-        by_type(a.out_type, [&](auto t) { read_piece(stage, row, t, v); });
+        by_type(a.out_type, [&](auto t) {
+          read_piece(stage, grad_low + key * uint32_t(grad_step), t, v);
+        });
         done_stage();
 #pragma unroll
         for (int i = 0; i < COLS; ++i) acc[i] = fmaf(a.scale, acc[i], v[i]);
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
       }
       by_type(a.out_type, [&](auto t) {
         constexpr int type = decltype(t)::value;
-        char* p = row + col0 * size_of(type);
+        char* p = grad_slab + key * grad_step;
         if constexpr (ALIGNED) {
 #pragma unroll
           for (int g = 0; g < COLS / 8; ++g) {
@@ -463,10 +475,15 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
             }
           }
         } else {
+          p += lane * size_of(type);
+          if (cols == kSlab) {
 #pragma unroll
-          for (int i = 0; i < COLS; ++i)
-            if (lane + kWarp * i < cols)
-              store1(p + (lane + kWarp * i) * size_of(type), type, acc[i]);
+            for (int i = 0; i < COLS; ++i) store1(p + kWarp * i * size_of(type), type, acc[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < COLS; ++i)
+              if (lane + kWarp * i < cols) store1(p + kWarp * i * size_of(type), type, acc[i]);
+          }
         }
       });
     }
