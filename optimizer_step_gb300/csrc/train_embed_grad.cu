@@ -49,6 +49,9 @@ struct GradArgs {
   uint32_t* named;  // a bit a row
   int64_t rows_per_cta, fill_first, fill_rest, fill_each;
   uint32_t fill_ctas;    // of sum_kernel
+  uint32_t fill_last;    // of join_kernel
+  uint32_t join_ctas;    // of join_kernel: those that join, for join_slabs slabs each
+  uint32_t join_slabs;
   int32_t block, slabs;  // C, slabs of columns
   float scale;
   int32_t accumulate, out_type;
@@ -515,10 +518,16 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(
     const __grid_constant__ GradArgs a) {
   __shared__ float4 part[kJoinWarps][kWarp];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = int64_t(blockIdx.x) * kJoinCols + 4 * lane;  // slots: whole groups of 8
+  if (blockIdx.x >= a.join_ctas) {
+    pdl_wait();
+    fill_rest(a, a.fill_ctas + (blockIdx.x - a.join_ctas));
+    return;
+  }
+  // Slots are whole groups of 8 columns.
+  const int64_t col = int64_t(blockIdx.x % a.join_slabs) * kJoinCols + 4 * lane;
   pdl_wait();
   const uint32_t runs = *a.n_long;
-  for (uint32_t k = blockIdx.y; k < runs; k += gridDim.y) {
+  for (uint32_t k = blockIdx.x / a.join_slabs; k < runs; k += a.join_ctas / a.join_slabs) {
     const LongRun run = a.long_runs[k];
     const int64_t from = run.block, pieces = run.pieces;
     int64_t share = (pieces + kJoinWarps - 1) / kJoinWarps;
@@ -978,7 +987,7 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
 #define KFB 48e6
 #endif
 #ifndef KFE
-#define KFE 64e3
+#define KFE 32e3
 #endif
 constexpr double kFillBytes = KFB;
 
@@ -1207,7 +1216,12 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
       if (a.fill_first > a.rows_per_cta) a.fill_first = a.rows_per_cta;
       a.fill_rest = ctas * (a.rows_per_cta - a.fill_first);
       a.fill_each = int64_t(KFE / row_bytes) + 1;
-      a.fill_ctas = uint32_t((a.fill_rest + a.fill_each - 1) / a.fill_each);
+      const uint32_t fill = uint32_t((a.fill_rest + a.fill_each - 1) / a.fill_each);
+#ifndef KMID
+#define KMID 0.25
+#endif
+      a.fill_ctas = uint32_t(KMID * fill);
+      a.fill_last = fill - a.fill_ctas;
     }
     const auto kernel = !scan ? fill_kernel<false, int32_t>
                         : ids_dtype == TRAIN_INT64 ? fill_kernel<true, int64_t>
@@ -1225,12 +1239,15 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     ce = launch(kernel, dim3(unsigned(ctas)), kSumWarps * kWarp, kSumWarps * sizeof(WarpSmem), s,
                 true, 1, a);
   }
-  if (ce == cudaSuccess && n_ids > 2 * p.block) {
+  if (ce == cudaSuccess && (n_ids > 2 * p.block || a.fill_last > 0)) {
     // A CTA for every 128 columns, and enough in all to fill the GPU.
     const int64_t x = (dim + kJoinCols - 1) / kJoinCols;
     int64_t y = x >= 1216 ? 1 : 1216 / x;
     if (y > p.n_blocks / 2) y = p.n_blocks / 2 > 0 ? p.n_blocks / 2 : 1;
-    ce = launch(join_kernel, dim3(unsigned(x), unsigned(y)), kJoinWarps * kWarp, 0, s, true, 1, a);
+    if (n_ids <= 2 * p.block) y = 0;
+    a.join_slabs = uint32_t(x);
+    a.join_ctas = uint32_t(x * y);
+    ce = launch(join_kernel, dim3(a.join_ctas + a.fill_last), kJoinWarps * kWarp, 0, s, true, 1, a);
   }
   return ce == cudaSuccess
              ? LAMB_OK
