@@ -227,22 +227,10 @@ __device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
 // are asynchronous (16 bytes a lane), so they hold no registers, and the rows
 // of the grad that accumulation needs come through the same ring behind the
 // last row of their run: nothing waits for them when the run is finished.
-#ifndef KST
-#define KST 6
-#endif
-#ifndef KSW
-#define KSW 4
-#endif
-#ifndef KMB
-#define KMB 64
-#endif
-#ifndef KU
-#define KU 4096
-#endif
-constexpr int kStages = KST;
+constexpr int kStages = 6;
 constexpr int kStageBytes = 1024 + 32;  // a piece and its ends' alignment
-constexpr int kMaxBlock = KMB;
-constexpr int kSumWarps = KSW;
+constexpr int kMaxBlock = 64;
+constexpr int kSumWarps = 4;
 
 struct WarpSmem {
   alignas(16) unsigned char ring[kStages][kStageBytes];
@@ -983,13 +971,7 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
 }
 
 // Zeros written while the tokens are being sorted.
-#ifndef KFB
-#define KFB 48e6
-#endif
-#ifndef KFE
-#define KFE 32e3
-#endif
-constexpr double kFillBytes = KFB;
+constexpr double kFillBytes = 48e6;
 
 constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
 
@@ -1020,7 +1002,7 @@ GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
   // Blocks of 128 positions where they make work for 4096 warps, else fewer.
   const int64_t slabs = (dim + 511) / 512;
   p.block = kMaxBlock;
-  while (p.block > 16 && n / p.block * slabs < KU) p.block /= 2;
+  while (p.block > 16 && n / p.block * slabs < 4096) p.block /= 2;
   p.n_blocks = (n + p.block - 1) / p.block;
   p.slot_dim = (dim + 7) / 8 * 8;
   int64_t at = 0;
@@ -1215,12 +1197,9 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
       if (a.fill_first > most) a.fill_first = most;
       if (a.fill_first > a.rows_per_cta) a.fill_first = a.rows_per_cta;
       a.fill_rest = ctas * (a.rows_per_cta - a.fill_first);
-      a.fill_each = int64_t(KFE / row_bytes) + 1;
+      a.fill_each = int64_t(32e3 / row_bytes) + 1;
       const uint32_t fill = uint32_t((a.fill_rest + a.fill_each - 1) / a.fill_each);
-#ifndef KMID
-#define KMID 0.25
-#endif
-      a.fill_ctas = uint32_t(KMID * fill);
+      a.fill_ctas = fill / 4;
       a.fill_last = fill - a.fill_ctas;
     }
     const auto kernel = !scan ? fill_kernel<false, int32_t>
