@@ -1,4 +1,5 @@
 // Global gradient norm over many tensors and clipping (train_ops.h).
+#include <algorithm>
 #include <cmath>
 #include <new>
 #include <vector>
@@ -17,9 +18,15 @@ constexpr int64_t kItemBytes = kThreads * kLoads * 16;
 // Half as many where everything fits into L2, so that a few items a CTA come
 // out more even.
 constexpr int64_t kSmallTotal = 128 << 20;
+// Items of at most so many bytes are packed: one a warp of a CTA, or where that
+// gives more than kFewPacks packs, four.
+constexpr int64_t kPackedBytes = 4096;
+constexpr size_t kFewPacks = 760;
 constexpr int kNormCtas = 5;  // per SM
 
-// One piece of a tensor: count elements from src, written to dst.
+// One piece of work: count elements from src, written to dst; or, where `in`
+// is kPack, count items at src, a warp for each of them in turn.
+constexpr int8_t kPack = -1;
 struct __align__(32) Item {
   const void* src;
   void* dst;
@@ -93,14 +100,14 @@ __device__ __forceinline__ void add_square(Squares& s, float x) {
   else s.bad = 1u;
 }
 
-// The squares of a thread's vectors (v, v + kThreads, ... below end) in fp64,
+// The squares of a thread's vectors (v, v + threads, ... below end) in fp64,
 // and whether one is inf or NaN.  The rare path: not inlined, and the values
 // are read again, so that the fast path carries neither fp64 code nor words
 // kept for it.
 template <int DT>
-__device__ __noinline__ Squares squares_fp64(const char* base, int v, int end) {
+__device__ __noinline__ Squares squares_fp64(const char* base, int v, int end, int threads) {
   Squares s{0.0, 0u};
-  for (int u = 0; u < kLoads; ++u, v += kThreads) {
+  for (int u = 0; u < kLoads; ++u, v += threads) {
     if (v >= end) break;
     for (int i = 0; i < 16 / size_of(DT); ++i)
       add_square(s, to_float<DT>(reinterpret_cast<const typename TypeOf<DT>::T*>(
@@ -109,7 +116,8 @@ __device__ __noinline__ Squares squares_fp64(const char* base, int v, int end) {
   return s;
 }
 
-// A thread's share of the squares of one item.  They are summed in fp32, at
+// A thread's share of the squares of one item that `threads` threads take, this
+// one the `tid`-th.  They are summed in fp32, at
 // most 64 of them, and from there in fp64.  bf16 and fp32 grads span fp32's
 // exponents, so their squares may leave its range: a sum outside [2^-90,
 // 2^120] (some value not zero) is taken again in fp64.  Inside that range
@@ -117,23 +125,24 @@ __device__ __noinline__ Squares squares_fp64(const char* base, int v, int end) {
 // An inf or NaN makes its sum inf or NaN, which is never inside the range, so
 // the fast path does not test for them.  fp16 squares never leave it.
 template <int DT>
-__device__ __forceinline__ void item_squares(const Item& it, double& acc, uint32_t& bad) {
+__device__ __forceinline__ void item_squares(const Item& it, int tid, int threads, double& acc,
+                                             uint32_t& bad) {
   using T = typename TypeOf<DT>::T;
   constexpr int kPer = 16 / size_of(DT);
   const int head = it.head;
   const int vecs = (it.count - head) / kPer;
   const char* base = static_cast<const char*>(it.src) + head * size_of(DT);
-  const int v = threadIdx.x;
+  const int v = tid;
   uint4 q[kLoads];
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
     q[u] = make_uint4(0u, 0u, 0u, 0u);
-    if (v + u * kThreads < vecs) q[u] = load16(base + int64_t(v + u * kThreads) * 16);
+    if (v + u * threads < vecs) q[u] = load16(base + int64_t(v + u * threads) * 16);
   }
   // What the 16-byte loads leave: up to 7 elements in front and behind.
   const int rest = it.count - vecs * kPer;
-  if (threadIdx.x < rest) {
-    const int i = threadIdx.x < head ? int(threadIdx.x) : vecs * kPer + int(threadIdx.x);
+  if (tid < rest) {
+    const int i = tid < head ? tid : vecs * kPer + tid;
     Squares s{0.0, 0u};
     add_square(s, to_float<DT>(static_cast<const T*>(it.src)[i]));
     acc += s.sum;
@@ -167,11 +176,18 @@ __device__ __forceinline__ void item_squares(const Item& it, double& acc, uint32
     if (a <= 0x1p120f && (a >= 0x1p-90f || any == 0u)) {
       acc += double(a);
     } else {
-      const Squares s = squares_fp64<DT>(base, v, vecs);
+      const Squares s = squares_fp64<DT>(base, v, vecs, threads);
       acc += s.sum;
       bad |= s.bad;
     }
   }
+}
+
+__device__ __forceinline__ void any_squares(const Item& it, int tid, int threads, double& acc,
+                                            uint32_t& bad) {
+  if (it.in == TRAIN_BF16) item_squares<TRAIN_BF16>(it, tid, threads, acc, bad);
+  else if (it.in == TRAIN_FP32) item_squares<TRAIN_FP32>(it, tid, threads, acc, bad);
+  else item_squares<TRAIN_FP16>(it, tid, threads, acc, bad);
 }
 
 // Forms the norm, the factor and the flag from the sum of squares (infinite if
@@ -225,9 +241,14 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   for (int64_t k = blockIdx.x; k < T.n_items; k += gridDim.x) {
     const Item it = next;
     if (k + gridDim.x < T.n_items) next = T.items[k + gridDim.x];
-    if (it.in == TRAIN_BF16) item_squares<TRAIN_BF16>(it, acc, bad);
-    else if (it.in == TRAIN_FP32) item_squares<TRAIN_FP32>(it, acc, bad);
-    else item_squares<TRAIN_FP16>(it, acc, bad);
+    if (it.in != kPack) {
+      any_squares(it, threadIdx.x, kThreads, acc, bad);
+      continue;
+    }
+    const Item* packed = static_cast<const Item*>(it.src);
+#pragma unroll 1
+    for (int i = threadIdx.x >> 5; i < it.count; i += kWarps)
+      any_squares(packed[i], threadIdx.x & 31, kWarp, acc, bad);
   }
   // An inf or NaN grad makes the sum infinite; finite grads cannot.
   if (bad) acc = __longlong_as_double(0x7ff0000000000000ll);
@@ -276,12 +297,12 @@ __device__ __forceinline__ void store_value(const Item& it, int i, float x) {
 // factor * src into dst: 16 bytes of src a thread and load, coalesced on both
 // sides, or element by element where src and dst are aligned differently.
 template <int IN, int OUT>
-__device__ __forceinline__ void item_scale(const Item& it, float factor) {
+__device__ __forceinline__ void item_scale(const Item& it, int tid, int threads, float factor) {
   using TO = typename TypeOf<OUT>::T;
   constexpr int kPer = 16 / size_of(IN);
   if (!it.aligned) {
 #pragma unroll 8
-    for (int i = threadIdx.x; i < it.count; i += kThreads)
+    for (int i = tid; i < it.count; i += threads)
       store_value<OUT>(it, i, factor * load_value<IN>(it, i));
     return;
   }
@@ -292,16 +313,18 @@ __device__ __forceinline__ void item_scale(const Item& it, float factor) {
   TO* dst = static_cast<TO*>(it.dst) + head;
   uint4 q[kLoads];
 #pragma unroll
-  for (int u = 0; u < kLoads; ++u)
-    if (int(threadIdx.x) + u * kThreads < vecs) q[u] = load16(src + threadIdx.x + u * kThreads);
+  for (int u = 0; u < kLoads; ++u) {
+    q[u] = make_uint4(0u, 0u, 0u, 0u);  // or it would be live from one item to the next
+    if (tid + u * threads < vecs) q[u] = load16(src + tid + u * threads);
+  }
   const int rest = it.count - vecs * kPer;
-  if (threadIdx.x < rest) {
-    const int i = threadIdx.x < head ? int(threadIdx.x) : vecs * kPer + int(threadIdx.x);
+  if (tid < rest) {
+    const int i = tid < head ? tid : vecs * kPer + tid;
     store_value<OUT>(it, i, factor * load_value<IN>(it, i));
   }
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
-    const int v = threadIdx.x + u * kThreads;
+    const int v = tid + u * threads;
     if (v >= vecs) continue;
     const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
     float x[kPer];
@@ -334,10 +357,18 @@ __device__ __forceinline__ void item_scale(const Item& it, float factor) {
 }
 
 template <int IN>
-__device__ __forceinline__ void item_scale_to(const Item& it, float factor) {
-  if (it.out == TRAIN_BF16) item_scale<IN, TRAIN_BF16>(it, factor);
-  else if (it.out == TRAIN_FP32) item_scale<IN, TRAIN_FP32>(it, factor);
-  else item_scale<IN, TRAIN_FP16>(it, factor);
+__device__ __forceinline__ void item_scale_to(const Item& it, int tid, int threads,
+                                              float factor) {
+  if (it.out == TRAIN_BF16) item_scale<IN, TRAIN_BF16>(it, tid, threads, factor);
+  else if (it.out == TRAIN_FP32) item_scale<IN, TRAIN_FP32>(it, tid, threads, factor);
+  else item_scale<IN, TRAIN_FP16>(it, tid, threads, factor);
+}
+
+__device__ __forceinline__ void any_scale(const Item& it, int tid, int threads, float factor) {
+  if (it.src == it.dst && factor == 1.0f) return;
+  if (it.in == TRAIN_BF16) item_scale_to<TRAIN_BF16>(it, tid, threads, factor);
+  else if (it.in == TRAIN_FP32) item_scale_to<TRAIN_FP32>(it, tid, threads, factor);
+  else item_scale_to<TRAIN_FP16>(it, tid, threads, factor);
 }
 
 // One item a CTA, so that the CTAs go through memory in the order they are
@@ -349,10 +380,13 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(Tables T) {
   pdl_trigger();
   pdl_wait();
   const float factor = T.sc->factor;
-  if (T.sc->bad || (it.src == it.dst && factor == 1.0f)) return;
-  if (it.in == TRAIN_BF16) item_scale_to<TRAIN_BF16>(it, factor);
-  else if (it.in == TRAIN_FP32) item_scale_to<TRAIN_FP32>(it, factor);
-  else item_scale_to<TRAIN_FP16>(it, factor);
+  if (T.sc->bad) return;
+  const bool pack = it.in == kPack;
+  const Item* packed = static_cast<const Item*>(it.src);
+  const int count = pack ? it.count : 1, tid = pack ? threadIdx.x & 31 : threadIdx.x;
+#pragma unroll 1
+  for (int i = pack ? threadIdx.x >> 5 : 0; i < count; i += kWarps)
+    any_scale(pack ? packed[i] : it, tid, pack ? kWarp : kThreads, factor);
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
@@ -433,66 +467,109 @@ int launch_scale(train_clip_handle* h) {
   return launch(h, "scale kernel", scale_kernel, h->T.n_items, true, h->T);
 }
 
-// Cuts one tensor into items whose first 16-byte loads are aligned: only its
-// first item has elements in front of them.
-void add_items(std::vector<Item>* items, const char* src, char* dst, int64_t n, int32_t in,
-               int32_t out, int64_t item_bytes) {
-  const int si = size_of(in), so = size_of(out);
+// A run of neighbouring elements: a tensor, or several that lie one behind the
+// other on both sides.
+struct Span {
+  const char* src;
+  char* dst;
+  int64_t n;
+  int32_t in, out;
+};
+
+// Cuts a span into items whose first 16-byte loads are aligned: only its first
+// item has elements in front of them.  Small ones go to `small`.
+void add_items(std::vector<Item>* items, std::vector<Item>* small, const Span& span,
+               int64_t item_bytes) {
+  const int si = size_of(span.in), so = size_of(span.out);
   const int64_t per = item_bytes / si;
-  const int head = int((16 - reinterpret_cast<uintptr_t>(src) % 16) % 16) / si;
+  const int head = int((16 - reinterpret_cast<uintptr_t>(span.src) % 16) % 16) / si;
   const int wide = 16 / si * so < 16 ? 16 / si * so : 16;  // bytes of dst written at a time
-  const bool aligned = reinterpret_cast<uintptr_t>(dst + head * so) % unsigned(wide) == 0;
-  for (int64_t b = 0; b < n;) {
+  const bool aligned = reinterpret_cast<uintptr_t>(span.dst + head * so) % unsigned(wide) == 0;
+  for (int64_t b = 0; b < span.n;) {
+    const int64_t left = span.n - b;
     Item it{};
-    it.src = src + b * si;
-    it.dst = dst + b * so;
-    it.head = int8_t(b == 0 ? (head < n ? head : n) : 0);
-    it.count = int32_t(n - b < per + it.head ? n - b : per + it.head);
-    it.in = int8_t(in);
-    it.out = int8_t(out);
+    it.src = span.src + b * si;
+    it.dst = span.dst + b * so;
+    it.head = int8_t(b == 0 ? (head < left ? head : left) : 0);
+    it.count = int32_t(left < per + it.head ? left : per + it.head);
+    it.in = int8_t(span.in);
+    it.out = int8_t(span.out);
     it.aligned = aligned;
-    items->push_back(it);
+    (it.count * si <= kPackedBytes ? small : items)->push_back(it);
     b += it.count;
   }
 }
 
 int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32_t* dtypes,
            void* const* grads, void* const* outs, const int32_t* out_dtypes, void* stream) {
-  std::vector<Item> items;
-  int64_t total = 0;
-  for (int32_t i = 0; i < n && total < kSmallTotal; ++i)
-    if (sizes[i] > 0 && known(dtypes[i])) total += (sizes[i] < kSmallTotal ? sizes[i] : kSmallTotal) * size_of(dtypes[i]);
-  const int64_t item_bytes = total < kSmallTotal ? kItemBytes / 2 : kItemBytes;
+  std::vector<Span> spans;
+  spans.reserve(size_t(n));
+  int64_t total = 0;  // bytes, or kSmallTotal if there are more
   for (int32_t i = 0; i < n; ++i) {
-    const std::string at = "[" + std::to_string(i) + "]";
-    if (sizes[i] < 0) return fail(LAMB_ERR_INVALID, "sizes" + at + " < 0");
-    if (!known(dtypes[i])) return fail(LAMB_ERR_INVALID, "dtypes" + at + ": unknown type");
+    const auto at = [i](const char* what) { return what + ("[" + std::to_string(i) + "]"); };
+    if (sizes[i] < 0) return fail(LAMB_ERR_INVALID, at("sizes") + " < 0");
+    if (!known(dtypes[i])) return fail(LAMB_ERR_INVALID, at("dtypes") + ": unknown type");
     const int32_t to = outs ? out_dtypes[i] : dtypes[i];
-    if (!known(to)) return fail(LAMB_ERR_INVALID, "out_dtypes" + at + ": unknown type");
+    if (!known(to)) return fail(LAMB_ERR_INVALID, at("out_dtypes") + ": unknown type");
     if (sizes[i] == 0) continue;
     void* dst = outs ? outs[i] : grads[i];
-    int rc = check_device(grads[i], size_t(size_of(dtypes[i])), ("grads" + at).c_str());
-    if (rc == LAMB_OK) rc = check_device(dst, size_t(size_of(to)), ("outs" + at).c_str());
-    if (rc != LAMB_OK) return rc;
+    const int si = size_of(dtypes[i]), so = size_of(to);
+    if (!grads[i]) return fail(LAMB_ERR_INVALID, at("grads") + " is NULL");
+    if (!dst) return fail(LAMB_ERR_INVALID, at("outs") + " is NULL");
+    if (reinterpret_cast<uintptr_t>(grads[i]) % unsigned(si))
+      return fail(LAMB_ERR_ALIGN, at("grads") + " is not aligned to its element type");
+    if (reinterpret_cast<uintptr_t>(dst) % unsigned(so))
+      return fail(LAMB_ERR_ALIGN, at("outs") + " is not aligned to its element type");
     if (dst == grads[i] && to != dtypes[i])
-      return fail(LAMB_ERR_INVALID, "outs" + at + " is grads" + at + ", of another type");
-    add_items(&items, static_cast<const char*>(grads[i]), static_cast<char*>(dst), sizes[i],
-              dtypes[i], to, item_bytes);
+      return fail(LAMB_ERR_INVALID, at("outs") + " is " + at("grads") + ", of another type");
+    if (sizes[i] > INT64_MAX / 8) return fail(LAMB_ERR_INVALID, at("sizes") + " is too large");
+    spans.push_back(Span{static_cast<const char*>(grads[i]), static_cast<char*>(dst), sizes[i],
+                         dtypes[i], to});
+    total = sizes[i] * si < kSmallTotal - total ? total + sizes[i] * si : kSmallTotal;
+  }
+  // In the order of memory, neighbours joined.
+  std::stable_sort(spans.begin(), spans.end(),
+                   [](const Span& a, const Span& b) { return a.src < b.src; });
+  const int64_t item_bytes = total < kSmallTotal ? kItemBytes / 2 : kItemBytes;
+  std::vector<Item> items, small;
+  for (size_t i = 0; i < spans.size();) {
+    Span s = spans[i];
+    for (++i; i < spans.size(); ++i) {
+      const Span& next = spans[i];
+      if (next.in != s.in || next.out != s.out || next.src != s.src + s.n * size_of(s.in) ||
+          next.dst != s.dst + s.n * size_of(s.out))
+        break;
+      s.n += next.n;
+    }
+    add_items(&items, &small, s, item_bytes);
     if (items.size() > 0x7fffffff) return fail(LAMB_ERR_INVALID, "too many elements");
   }
+  const size_t per_pack = small.size() <= kWarps * kFewPacks ? kWarps : 4 * kWarps;
+  const size_t packs = (small.size() + per_pack - 1) / per_pack;
+  const size_t n_items = items.size() + packs;  // followed by the packed ones
+  for (size_t k = 0; k < packs; ++k) {
+    const size_t left = small.size() - k * per_pack;
+    Item it{};
+    it.count = int32_t(left < per_pack ? left : per_pack);
+    it.in = kPack;
+    items.push_back(it);
+  }
+  items.insert(items.end(), small.begin(), small.end());
   int dev = 0, sms = 0;
   cudaError_t ce = cudaGetDevice(&dev);
   if (ce == cudaSuccess)
     ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (ce != cudaSuccess) return cuda_fail(ce, "querying the device");
   int64_t grid = int64_t(sms) * kNormCtas;
-  if (grid > int64_t(items.size())) grid = items.empty() ? 1 : int64_t(items.size());
+  if (grid > int64_t(n_items)) grid = n_items ? int64_t(n_items) : 1;
   const size_t table_bytes = (items.size() * sizeof(Item) + 255) / 256 * 256;
   const size_t part_bytes = (size_t(grid) * sizeof(double) + 255) / 256 * 256;
   void* block = nullptr;
   ce = cudaMalloc(&block, table_bytes + part_bytes + sizeof(Scalars));
   if (ce != cudaSuccess) return cuda_fail(ce, "allocating the work table");
   char* p = static_cast<char*>(block);
+  for (size_t k = 0; k < packs; ++k)
+    items[n_items - packs + k].src = p + (n_items + k * per_pack) * sizeof(Item);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!items.empty())
     ce = cudaMemcpyAsync(p, items.data(), items.size() * sizeof(Item), cudaMemcpyHostToDevice, s);
@@ -512,7 +589,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   h->T.items = reinterpret_cast<const Item*>(p);
   h->T.partial = reinterpret_cast<double*>(p + table_bytes);
   h->T.sc = reinterpret_cast<Scalars*>(p + table_bytes + part_bytes);
-  h->T.n_items = int64_t(items.size());
+  h->T.n_items = int64_t(n_items);
   *out = h;
   return LAMB_OK;
 }

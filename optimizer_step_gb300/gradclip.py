@@ -13,21 +13,20 @@ from ._lib import check
 from .embedding import _TYPES
 
 
-def _checked(name, tensors, device):
+def _arrays(name, tensors, device):
+    """Sizes, type codes and addresses of tensors, after their checks."""
+    rows = []
     for i, t in enumerate(tensors):
-        if not isinstance(t, torch.Tensor) or t.dtype not in _TYPES:
+        code = _TYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+        if code is None:
             raise TypeError(f"{name}[{i}]: expected a bfloat16, float16 or float32 tensor")
         if t.device != device:
             raise ValueError(f"{name}[{i}]: on {t.device}, expected {device}")
         if not t.is_contiguous():
             raise ValueError(f"{name}[{i}]: must be contiguous")
-
-
-def _arrays(tensors):
-    n = len(tensors)
-    types = np.fromiter((_TYPES[t.dtype] for t in tensors), dtype=np.int32, count=n)
-    ptrs = np.fromiter((t.data_ptr() for t in tensors), dtype=np.uint64, count=n)
-    return types, ptrs
+        rows.append((t.numel(), code, t.data_ptr()))
+    table = np.array(rows, dtype=np.uint64).reshape(len(rows), 3).T
+    return table[0].astype(np.int64), table[1].astype(np.int32), table[2].copy()
 
 
 class GradClip:
@@ -55,20 +54,16 @@ class GradClip:
                 raise ValueError("grads must live on a CUDA device")
         self.device = grads[0].device if grads else torch.device("cuda",
                                                                  torch.cuda.current_device())
-        _checked("grads", grads, self.device)
         n = len(grads)
-        sizes = np.fromiter((t.numel() for t in grads), dtype=np.int64, count=n)
-        types, ptrs = _arrays(grads)
+        sizes, types, ptrs = _arrays("grads", grads, self.device)
         out_types = out_ptrs = None
         if out is not None:
             out = list(out)
             if len(out) != n:
                 raise ValueError(f"out: expected {n} tensors, got {len(out)}")
-            _checked("out", out, self.device)
-            for i, (a, b) in enumerate(zip(out, grads)):
-                if a.numel() != b.numel():
-                    raise ValueError(f"out[{i}]: expected {b.numel()} elements")
-            out_types, out_ptrs = _arrays(out)
+            out_sizes, out_types, out_ptrs = _arrays("out", out, self.device)
+            for i in np.flatnonzero(out_sizes != sizes):
+                raise ValueError(f"out[{i}]: expected {sizes[i]} elements")
         self._keep = (grads, out)
         address = lambda a: None if a is None else a.ctypes.data
         with torch.cuda.device(self.device):
