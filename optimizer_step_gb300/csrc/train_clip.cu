@@ -201,6 +201,7 @@ struct Request {
   double max_norm;
   float* stats;
   double* exchange;  // not NULL: only the sum and the flag, here
+  bool early;        // the next kernel may start at once
 };
 
 __device__ __forceinline__ void publish(Scalars* sc, const Request& r, double sum) {
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
                                                         const __grid_constant__ Request r) {
   __shared__ double red[kWarps];
   __shared__ uint32_t last;
-  pdl_trigger();
+  if (r.early) pdl_trigger();
   double acc = 0.0;
   uint32_t bad = 0;
   Item next{};
@@ -250,6 +251,7 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
     for (int i = threadIdx.x >> 5; i < it.count; i += kWarps)
       any_squares(packed[i], threadIdx.x & 31, kWarp, acc, bad);
   }
+  if (!r.early) pdl_trigger();
   // An inf or NaN grad makes the sum infinite; finite grads cannot.
   if (bad) acc = __longlong_as_double(0x7ff0000000000000ll);
   const double s = block_sum(acc, red);
@@ -417,6 +419,7 @@ struct train_clip_handle {
   void* block = nullptr;
   Tables T{};
   int grid = 1;
+  bool small = false;  // all grads fit into L2
 };
 
 namespace {
@@ -455,11 +458,15 @@ int launch(train_clip_handle* h, const char* what, void (*kernel)(A...), int64_t
   return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, what);
 }
 
-int launch_norm(train_clip_handle* h, const Request& r) {
-  // CTAs that start while another kernel holds part of the GPU are spread over
-  // the SMs unevenly.  Where each has one item that costs nothing and the early
-  // start saves 1.5 us; a walk over many items was up to 10% slower.
-  return launch(h, "norm kernel", norm_kernel, h->grid, h->T.n_items <= h->grid, h->T, r);
+// CTAs that start while another kernel holds part of the GPU are spread over the
+// SMs unevenly, which a walk over many items feels: 3% at 0.6 to 7 GB, and as
+// much where the norm of the next step starts beside the clipping of this one.
+// Where they all have one item, or nothing else is running, the early start
+// saves 1 to 1.5 us.
+int launch_norm(train_clip_handle* h, bool alone, Request r) {
+  const bool one_each = h->T.n_items <= h->grid;
+  r.early = !alone || one_each;
+  return launch(h, "norm kernel", norm_kernel, h->grid, one_each || (alone && h->small), h->T, r);
 }
 
 int launch_scale(train_clip_handle* h) {
@@ -586,6 +593,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   h->stream = s;
   h->block = block;
   h->grid = int(grid);
+  h->small = total < kSmallTotal;
   h->T.items = reinterpret_cast<const Item*>(p);
   h->T.partial = reinterpret_cast<double*>(p + table_bytes);
   h->T.sc = reinterpret_cast<Scalars*>(p + table_bytes + part_bytes);
@@ -624,7 +632,7 @@ LAMB_API int train_clip_norm(train_clip_handle* h, float loss_scale, float* stat
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  return launch_norm(h, Request{1.0 / double(loss_scale), 0.0, stats, nullptr});
+  return launch_norm(h, true, Request{1.0 / double(loss_scale), 0.0, stats, nullptr, false});
 }
 
 LAMB_API int train_clip_grads(train_clip_handle* h, float max_norm, float loss_scale,
@@ -636,7 +644,8 @@ LAMB_API int train_clip_grads(train_clip_handle* h, float max_norm, float loss_s
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  rc = launch_norm(h, Request{1.0 / double(loss_scale), double(max_norm), stats, nullptr});
+  rc = launch_norm(
+      h, false, Request{1.0 / double(loss_scale), double(max_norm), stats, nullptr, false});
   return rc == LAMB_OK ? launch_scale(h) : rc;
 }
 
@@ -647,7 +656,7 @@ LAMB_API int train_clip_partial(train_clip_handle* h, double* exchange) {
   if (rc != LAMB_OK) return rc;
   DeviceGuard dg(h->device);
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
-  return launch_norm(h, Request{1.0, 0.0, nullptr, exchange});
+  return launch_norm(h, true, Request{1.0, 0.0, nullptr, exchange, false});
 }
 
 LAMB_API int train_clip_finish(train_clip_handle* h, const double* exchange, float max_norm,
@@ -662,7 +671,7 @@ LAMB_API int train_clip_finish(train_clip_handle* h, const double* exchange, flo
   if (!dg.ok) return fail(LAMB_ERR_CUDA, "cannot make the handle's device current");
   finish_kernel<<<1, 1, 0, h->stream>>>(
       h->T, Request{1.0 / double(loss_scale), double(max_norm), stats,
-                    const_cast<double*>(exchange)});
+                    const_cast<double*>(exchange), false});
   const cudaError_t ce = cudaGetLastError();
   if (ce != cudaSuccess) return cuda_fail(ce, "finish kernel");
   return launch_scale(h);
