@@ -160,10 +160,11 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
         o_stride = _row_stride("out", out)
     n_ids, rows = ids.numel(), out.shape[0]
     need = _workspace_bytes(n_ids, rows, dim)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _enqueue(device, _lib.load().train_embed_grad, grad_out.data_ptr(), g_code, g_stride,
              ids.data_ptr(), i_code, n_ids, first_row, padding_id, scale, 1 if accumulate else 0,
-             out.data_ptr(), o_code, rows, dim, o_stride, workspace.data_ptr(), need)
+             out.data_ptr(), o_code, rows, dim, o_stride,
+             workspace.data_ptr() if need else None, need)
     return out
 
 

@@ -247,6 +247,34 @@ def test_grad_lengths(n, spread):
         check_grad(out, dy, ids, old=old)
 
 
+@pytest.mark.parametrize("n", [15, 16, 17, 255, 257, 2048, 2049, 16384, 16385, 32769, 65537])
+@pytest.mark.parametrize("dim", [8, 129, 520])
+def test_grad_where_the_ways_of_working_change(n, dim):
+    """Lengths beside each limit of the sort and of the cut into blocks, with
+    runs that end in, at and behind the ends of blocks."""
+    rows = 97
+    u = torch.arange(n, device="cuda")
+    for ids in ((u * u) % 89 % rows, torch.where(u % 3 == 0, 11, (u // 7) % rows), u * rows // n):
+        dy = randn((n, dim), BF16, n)
+        out = randn((rows, dim), FP32, 3)
+        old = out.clone()
+        og.embed_grad(dy, ids, out=out, accumulate=True, scale=0.5)
+        check_grad(out, dy, ids, 0.5, old=old)
+        check_grad(og.embed_grad(dy, ids, n_rows=rows), dy, ids)
+
+
+@pytest.mark.parametrize("n,dim", [(40_000, 3), (40_000, 21), (9000, 4100), (131_073, 12)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_of_one_token_throughout(n, dim, accumulate):
+    ids = torch.full((n,), 6, device="cuda", dtype=torch.int32)
+    ids[n // 2] = 3
+    dy = randn((n, dim), FP16, 1)
+    out = randn((9, dim), FP32, 2)
+    old = out.clone() if accumulate else None
+    og.embed_grad(dy, ids, out=out, accumulate=accumulate)
+    check_grad(out, dy, ids, old=old)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 255, 256, 257, 65535, 65537, 150_001])
 def test_grad_row_counts(rows):
     for n in (50, 5000, 30_000):
