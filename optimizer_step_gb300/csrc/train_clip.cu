@@ -228,7 +228,10 @@ __device__ __forceinline__ void publish(Scalars* sc, const Request& r, double su
 
 // Sum of squares: each CTA walks every gridDim.x-th item, all of them through
 // memory side by side; the last one to finish adds the CTAs' sums in order and
-// publishes.
+// publishes.  It is bound by reading: 1.2e9 fp16 grads take 331 us on GB300, 7.3
+// TB/s (5 CTAs an SM; 3 read 13% slower, 8 2%).  With a few MB it is a chain of
+// latencies: for 6 MB the last CTA has its data after 2.7 us, the last ticket
+// comes after 4.9, the norm is there after 7.2.
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Tables T,
                                                         const __grid_constant__ Request r) {
   __shared__ double red[kWarps];
@@ -376,7 +379,8 @@ __device__ __forceinline__ void any_scale(const Item& it, int tid, int threads, 
 // One item a CTA, so that the CTAs go through memory in the order they are
 // launched: on GB300 a copy runs at 7.1 TB/s this way and at 6.5 with a
 // persistent grid.  The last items come first: the norm kernel read them last,
-// and they may still be in L2.
+// and they may still be in L2.  1.8e9 fp32 grads clipped into bf16 take 2.48 ms in
+// all: 18.1 GB with the second reading, 7.3 TB/s.
 __global__ void __launch_bounds__(kThreads) scale_kernel(Tables T) {
   const Item it = T.items[T.n_items - 1 - blockIdx.x];
   pdl_trigger();

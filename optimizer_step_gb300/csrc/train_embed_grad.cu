@@ -9,16 +9,29 @@ namespace cg = cooperative_groups;
 namespace {
 
 // G[v, :] = scale * sum over the positions i with row(ids[i]) = v of dy[i, :].
+//
 // The positions are sorted by row (stably, so ascending within a row), and the
 // sorted list is cut into blocks of C positions.  A warp takes one block and
 // a slab of up to 512 columns, streams the rows of dy that its positions name
 // through a ring of shared memory and adds each run of equal rows in
-// registers.  A run that ends in the next block at the latest is finished by
-// the warp of the block it starts in.  A longer one (a frequent token) is cut
-// at the block boundaries: each piece's fp32 sum goes to a slot of the
-// workspace, and join_kernel adds the pieces in order.  So no warp adds more
-// than 2 C rows whatever the tokens are, only long runs pay for slots, and
+// registers, in fp32.  A run that ends in the next block at the latest is
+// finished by the warp of the block it starts in.  A longer one (a frequent
+// token) is cut at the block boundaries: each piece's fp32 sum goes to a slot
+// of the workspace, and join_kernel adds the pieces in order.  So no warp adds
+// more than 2 C rows whatever the tokens are, only long runs pay for slots, and
 // the order of every sum depends on the ids and the sizes alone.
+//
+// What bounds it is memory: every row of dy is read once, and a dense gradient
+// writes n_rows rows, most of them zeros.  Four launches, each started early
+// behind the one before it: the sort; beside it fill_kernel, which marks the
+// named rows and zeroes some of the others; sum_kernel, with CTAs behind it
+// that zero more; join_kernel, and the rest of the zeros beside its few long
+// chains.  On GB300 (copy rate 6.79 TB/s): 32768 bf16 tokens of width 12288 into
+// a dense gradient of 32000 rows 258 us, 6.2 TB/s over the 1.59 GB that have to
+// move; 8192 tokens of width 4096 60 us, 5.5 TB/s (the sort takes 9.5 of them,
+// the sums 22 if nothing else is written); 50,021 tokens of which a slice of
+// 15,013 rows holds half, fp16 of width 1023 added to fp32, 51 us, 4.0 TB/s (the
+// sort takes 15).
 
 // One sorted position: the row that its token names (n_rows for a token that
 // adds nothing) and the position.
@@ -45,7 +58,8 @@ struct GradArgs {
   int64_t units;         // blocks times slabs
   // Rows that no token names.  A CTA of fill_kernel marks the named ones among
   // rows_per_cta rows and zeroes the others of the first fill_first of them;
-  // CTAs of sum_kernel zero the rest, fill_each rows a CTA.
+  // CTAs of sum_kernel and join_kernel zero the rest (fill_rest rows in all,
+  // named ones among them), fill_each rows a CTA.
   uint32_t* named;  // a bit a row
   int64_t rows_per_cta, fill_first, fill_rest, fill_each;
   uint32_t fill_ctas;    // of sum_kernel
@@ -159,9 +173,10 @@ __device__ __forceinline__ void warp_zero(char* p, int64_t bytes, int lane) {
 // no sorted list and runs while the tokens are being sorted.  Else it looks
 // its rows up in that list.
 //
-// What is written alone goes out at 5.4 TB/s on GB300, and written while other
-// rows are read at 6.5 to 6.8; so this kernel zeroes what fits into the time of
-// the sort, and CTAs among those of sum_kernel zero the rest.
+// It zeroes what fits into the time of the sort (kFillBytes); the later kernels
+// zero the rest among their own work.  All of it here, before the sums, took 85 us
+// for 8192 tokens of width 4096 when the rest among the sums took 76: the sums
+// alone leave a third of the memory rate unused.
 constexpr int kFillThreads = 512;
 constexpr int kFillRows = 4096;  // at most, a CTA
 
@@ -203,8 +218,8 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
   if (SCAN) pdl_wait();
 }
 
-// The rows that fill_kernel has left, in a CTA of sum_kernel: fill_each of
-// them, `index` counting from the first.
+// The rows that fill_kernel has left, in a CTA of sum_kernel or join_kernel:
+// fill_each of them, `index` counting the CTAs.
 __device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x / kWarp;
   const int64_t left = a.rows_per_cta - a.fill_first;
@@ -227,6 +242,9 @@ __device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
 // are asynchronous (16 bytes a lane), so they hold no registers, and the rows
 // of the grad that accumulation needs come through the same ring behind the
 // last row of their run: nothing waits for them when the run is finished.
+// Measured on GB300 with 6 and 8 stages: 8192 tokens 60 and 61 us, 32768 wide ones
+// 259 and 254, the unaligned slice 51 and 53.  (Eight rows at a time in registers
+// took 276 us for that slice's sums alone, where the ring takes 31.)
 constexpr int kStages = 6;
 constexpr int kStageBytes = 1024 + 32;  // a piece and its ends' alignment
 constexpr int kMaxBlock = 64;
@@ -714,8 +732,8 @@ struct RankSmem {
 // stands at place warp * 32 * ITEMS + 32 * j + lane of the CTA.  On return
 // rank[j] counts the equal digits before it in its warp, warp_count[w][d] those
 // in the warps before w, and total[d] those in the CTA.
-// Lanes of equal digits are found bit by bit; __match_any_sync took up to 4 us
-// here where 32 lanes hold 32 digits, this 0.5.
+// Lanes of equal digits are found bit by bit: for 4 elements a lane 2.3 us, where
+// __match_any_sync took 0.5 to 4, more the more digits differ.
 template <int ITEMS>
 __device__ __forceinline__ void rank_digits(RankSmem& s, const uint32_t (&digit)[ITEMS],
                                             uint32_t (&rank)[ITEMS], int width) {
@@ -795,7 +813,7 @@ __device__ __forceinline__ void digit_bases(RankSmem& s, uint32_t all, uint32_t 
 // stores neighbours to neighbours: into the tiles of the other CTAs (distributed
 // shared memory), on the last pass into global memory.  (Scattered straight
 // from the registers, 8 bytes at a time, two passes over 50,021 tokens took
-// 28.6 us.)
+// 28.6 us in a cluster of 8; now they take 15.)
 constexpr int kSortCtas = 16;
 
 template <int ITEMS, class ID>
@@ -974,7 +992,8 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size_of(dtype) % 16 == 0;
 }
 
-// Zeros written while the tokens are being sorted.
+// Zeros written while the tokens are being sorted: 24, 48 and 80 MB measured 78.5,
+// 75.6 and 75.3 us for 8192 tokens of width 4096 at the time.
 constexpr double kFillBytes = 48e6;
 
 constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
@@ -997,13 +1016,16 @@ const DirectKernel direct_kernels[3][2] = {
 // How the gradient's work is cut; depends on the sizes alone.
 struct GradPlan {
   int64_t block, n_blocks, slot_dim, tiles;
-  int64_t places, places2, counts, totals, n_long, long_runs, named, slots, bytes;  // in the workspace
+  // Offsets in the workspace, and its size.
+  int64_t places, places2, counts, totals, n_long, long_runs, named, slots, bytes;
 };
 
 GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
   GradPlan p{};
   if (use_direct(n, dim)) return p;
-  // Blocks of 128 positions where they make work for 4096 warps, else fewer.
+  // Blocks of 64 positions where they make work for 4096 warps, else of 32 or 16:
+  // blocks of 128 were 5% slower for 32768 wide tokens, and 32 instead of 16 took 8%
+  // more for 8192 of width 4096.
   const int64_t slabs = (dim + 511) / 512;
   p.block = kMaxBlock;
   while (p.block > 16 && n / p.block * slabs < 4096) p.block /= 2;
@@ -1164,7 +1186,8 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
       fill = (n_rows + a.fill_each - 1) / a.fill_each;
     }
     d.g = a;
-    ce = launch(direct_kernels[grad_out_dtype][aligned ? 1 : 0], dim3(unsigned(d.sum_ctas + fill)), kDirectThreads, 0, s, true, 1, d);
+    ce = launch(direct_kernels[grad_out_dtype][aligned ? 1 : 0],
+                dim3(unsigned(d.sum_ctas + fill)), kDirectThreads, 0, s, true, 1, d);
     return ce == cudaSuccess
                ? LAMB_OK
                : fail(LAMB_ERR_CUDA, std::string("embed_grad: ") + cudaGetErrorString(ce));
