@@ -1001,10 +1001,12 @@ constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
 // One launch without a sort: few ids, and few enough CTAs that each of them
 // reading all ids does not matter.  On GB300, summed onto a bf16 grad, frequent
 // tokens as in text: 1024 ids of width 256 take 5 us this way and 20 us with a
-// sort, 256 of width 4096 (4096 CTAs) 11 and 20, 512 of them 28 and 22.
+// sort, 256 of width 4096 (4096 CTAs) 11 and 16, 512 of them 28 and 18.  Where rows
+// are not aligned a frequent token is slow this way (1024 times the same one, width
+// 1023: 65 us, with a sort 21), so only a quarter of the ids are taken.
 constexpr int64_t kDirectCtas = 4096;
 bool use_direct(int64_t n, int64_t dim) {
-  return n <= kDirectIds && n * ((dim + kDirectCols - 1) / kDirectCols) <= kDirectCtas;
+  return n <= (dim % 8 == 0 ? kDirectIds : kDirectIds / 4) && n * ((dim + kDirectCols - 1) / kDirectCols) <= kDirectCtas;
 }
 
 using DirectKernel = void (*)(DirectArgs);
@@ -1029,6 +1031,9 @@ GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
   const int64_t slabs = (dim + 511) / 512;
   p.block = kMaxBlock;
   while (p.block > 16 && n / p.block * slabs < 4096) p.block /= 2;
+  // Where even 16 make few: 1024 tokens of width 4096 added to bf16 take 17.5 us with
+  // blocks of 8, 21.5 with 16; 8192 of them (4096 warps with 16) 64 and 60.
+  if (n / 16 * slabs < 2048) p.block = 8;
   p.n_blocks = (n + p.block - 1) / p.block;
   p.slot_dim = (dim + 7) / 8 * 8;
   int64_t at = 0;

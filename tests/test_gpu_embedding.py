@@ -247,7 +247,7 @@ def test_grad_lengths(n, spread):
         check_grad(out, dy, ids, old=old)
 
 
-@pytest.mark.parametrize("n", [15, 16, 17, 255, 257, 2048, 2049, 16384, 16385, 32769, 65537])
+@pytest.mark.parametrize("n", [15, 16, 17, 255, 257, 512, 513, 2048, 2049, 16384, 16385, 32769, 65537])
 @pytest.mark.parametrize("dim", [8, 129, 520])
 def test_grad_where_the_ways_of_working_change(n, dim):
     """Lengths beside each limit of the sort and of the cut into blocks, with
