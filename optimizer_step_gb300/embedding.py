@@ -19,15 +19,16 @@ _TYPES = {torch.bfloat16: _lib.TRAIN_BF16, torch.float16: _lib.TRAIN_FP16,
 _ID_TYPES = {torch.int32: _lib.TRAIN_INT32, torch.int64: _lib.TRAIN_INT64}
 
 
-def _code(name, t, codes, device):
+def _code(name, t, codes, index):
     """Code of a tensor's type, after the checks that every argument gets."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a tensor")
     code = codes.get(t.dtype)
     if code is None:
         raise TypeError(f"{name}: expected {', '.join(map(str, codes))}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name}: on {t.device}, expected "
+                         + (f"cuda:{index}" if index >= 0 else "a CUDA device"))
     return code
 
 
@@ -58,20 +59,19 @@ def _row_stride(name, t):
     return stride
 
 
-def _ids_code(ids, device):
-    code = _code("ids", ids, _ID_TYPES, device)
+def _ids_code(ids, index):
+    code = _code("ids", ids, _ID_TYPES, index)
     if not ids.is_contiguous():
         raise ValueError("ids: must be contiguous")
     return code
 
 
-def _enqueue(device, call, *args):
-    """``call(*args, stream)`` with ``device`` current, on its current stream."""
-    index = device.index
+def _enqueue(index, call, *args):
+    """``call(*args, stream)`` with device ``index`` current, on its current stream."""
     if index == torch._C._cuda_getDevice():
         rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if rc:
         check(rc)
@@ -96,24 +96,23 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
     """
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise TypeError("table: expected a tensor of two dimensions")
-    device = table.device
-    if not table.is_cuda:
-        raise ValueError("table: must live on a CUDA device")
-    t_code = _code("table", table, _TYPES, device)
-    i_code = _ids_code(ids, device)
+    index = table.get_device()
+    t_code = _code("table", table, _TYPES, index)
+    i_code = _ids_code(ids, index)
     rows, dim = table.shape
-    t_stride = _row_stride("table", table)
-    shape = ids.shape + (dim,)
+    t_stride = dim if table.is_contiguous() else _row_stride("table", table)
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype or table.dtype, device=device)
-        o_code = _code("out", out, _TYPES, device)
+        o_code = t_code if out_dtype is None else _TYPES.get(out_dtype)
+        if o_code is None:
+            raise TypeError(f"out_dtype: expected {', '.join(map(str, _TYPES))}")
+        out = torch.empty((*ids.shape, dim), dtype=out_dtype or table.dtype, device=table.device)
         o_stride = dim
     else:
-        o_code = _code("out", out, _TYPES, device)
-        if out.shape != shape or (out_dtype is not None and out.dtype != out_dtype):
-            raise ValueError(f"out: expected shape {tuple(shape)} and out_dtype's type")
+        o_code = _code("out", out, _TYPES, index)
+        if out.shape != ids.shape + (dim,) or (out_dtype is not None and out.dtype != out_dtype):
+            raise ValueError(f"out: expected shape {(*ids.shape, dim)} and out_dtype's type")
         o_stride = _row_stride("out", out)
-    _enqueue(device, _lib.load().train_embed, table.data_ptr(), t_code, rows, dim, t_stride,
+    _enqueue(index, _lib.load().train_embed, table.data_ptr(), t_code, rows, dim, t_stride,
              ids.data_ptr(), i_code, ids.numel(), first_row, scale, out.data_ptr(), o_code,
              o_stride)
     return out
@@ -135,13 +134,11 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
     """
     if not isinstance(grad_out, torch.Tensor) or grad_out.dim() == 0:
         raise TypeError("grad_out: expected a tensor of one dimension or more")
-    device = grad_out.device
-    if not grad_out.is_cuda:
-        raise ValueError("grad_out: must live on a CUDA device")
-    g_code = _code("grad_out", grad_out, _TYPES, device)
-    i_code = _ids_code(ids, device)
+    index = grad_out.get_device()
+    g_code = _code("grad_out", grad_out, _TYPES, index)
+    i_code = _ids_code(ids, index)
     dim = grad_out.shape[-1]
-    g_stride = _row_stride("grad_out", grad_out)
+    g_stride = dim if grad_out.is_contiguous() else _row_stride("grad_out", grad_out)
     if grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out: expected ids.shape + (dim,)")
     if out is None:
@@ -149,19 +146,22 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
             raise ValueError("n_rows or out must be given")
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((n_rows, dim), dtype=dtype or grad_out.dtype, device=device)
-        o_code = _code("out", out, _TYPES, device)
+        o_code = g_code if dtype is None else _TYPES.get(dtype)
+        if o_code is None:
+            raise TypeError(f"dtype: expected {', '.join(map(str, _TYPES))}")
+        out = torch.empty((n_rows, dim), dtype=dtype or grad_out.dtype, device=grad_out.device)
         o_stride = dim
     else:
-        o_code = _code("out", out, _TYPES, device)
+        o_code = _code("out", out, _TYPES, index)
         if (out.dim() != 2 or out.shape[1] != dim or n_rows not in (None, out.shape[0])
                 or (dtype is not None and out.dtype != dtype)):
             raise ValueError("out: expected [n_rows, dim] of dtype's type")
         o_stride = _row_stride("out", out)
     n_ids, rows = ids.numel(), out.shape[0]
     need = _workspace_bytes(n_ids, rows, dim)
-    workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _enqueue(device, _lib.load().train_embed_grad, grad_out.data_ptr(), g_code, g_stride,
+    workspace = (torch.empty(need, dtype=torch.uint8, device=grad_out.device) if need
+                 else None)
+    _enqueue(index, _lib.load().train_embed_grad, grad_out.data_ptr(), g_code, g_stride,
              ids.data_ptr(), i_code, n_ids, first_row, padding_id, scale, 1 if accumulate else 0,
              out.data_ptr(), o_code, rows, dim, o_stride,
              workspace.data_ptr() if need else None, need)
