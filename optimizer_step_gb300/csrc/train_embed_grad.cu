@@ -50,8 +50,9 @@ struct GradArgs {
   const void* ids;
   const Place* places;  // sorted
   float* slots;         // [2 * block + (0: run from an earlier block, 1: starts here)][slot_dim]
-  uint32_t* n_long;     // long runs in the list
-  LongRun* long_runs;   // in any order
+  uint32_t* n_long;     // long runs in the list: of few pieces, of many
+  LongRun* long_runs;   // those of few pieces from the front, the others from the back
+  int64_t last_run;     // of the list
   int64_t dy_stride, grad_stride, n_rows, dim, slot_dim, first_row, padding;
   int64_t n;
   int64_t n_blocks;
@@ -64,8 +65,8 @@ struct GradArgs {
   int64_t rows_per_cta, fill_first, fill_rest, fill_each;
   uint32_t fill_ctas;    // of sum_kernel
   uint32_t fill_last;    // of join_kernel
-  uint32_t join_ctas;    // of join_kernel: those that join, for join_slabs slabs each
-  uint32_t join_slabs;
+  uint32_t join_ctas;    // of join_kernel: those that join
+  uint32_t join_slabs;   // of 128 columns
   int32_t block, slabs;  // C, slabs of columns
   float scale;
   int32_t accumulate, out_type;
@@ -168,6 +169,13 @@ __device__ __forceinline__ void warp_zero(char* p, int64_t bytes, int lane) {
     *reinterpret_cast<uint16_t*>(q + i) = 0;
 }
 
+// Sets bit r.  A token that has stood before finds it set: 54,000 times the same
+// one took 30 us of atomics.
+__device__ __forceinline__ void mark(uint32_t* named, uint32_t r) {
+  const uint32_t bit = 1u << (r & 31);
+  if (!(*const_cast<volatile uint32_t*>(&named[r / 32]) & bit)) atomicOr(&named[r / 32], bit);
+}
+
 // Marks the rows that tokens name and zeroes some of the others, a range of
 // rows a CTA.  SCAN: the CTA finds its rows by a walk over all ids, so it needs
 // no sorted list and runs while the tokens are being sorted.  Else it looks
@@ -195,16 +203,14 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
     for (int64_t i = threadIdx.x; i < a.n; i += kFillThreads) {
       const ID id = ids[i];
       const uint64_t r = uint64_t(int64_t(id)) - uint64_t(a.first_row) - uint64_t(r0);
-      if (r < uint64_t(count) && int64_t(id) != a.padding)
-        atomicOr(&named[r / 32], 1u << (r & 31));
+      if (r < uint64_t(count) && int64_t(id) != a.padding) mark(named, uint32_t(r));
     }
   } else {
     pdl_wait();
     const int64_t lo = lower_bound(a.places, a.n, uint32_t(r0));
     const int64_t hi = lower_bound(a.places, a.n, uint32_t(r0 + count));
     for (int64_t i = lo + threadIdx.x; i < hi; i += kFillThreads) {
-      const uint32_t r = a.places[i].key - uint32_t(r0);
-      atomicOr(&named[r / 32], 1u << (r & 31));
+      mark(named, a.places[i].key - uint32_t(r0));
     }
   }
   __syncthreads();
@@ -248,6 +254,7 @@ __device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
 constexpr int kStages = 6;
 constexpr int kStageBytes = 1024 + 32;  // a piece and its ends' alignment
 constexpr int kMaxBlock = 64;
+constexpr uint32_t kManyPieces = 64;
 constexpr int kSumWarps = 4;
 
 struct WarpSmem {
@@ -510,67 +517,87 @@ __global__ void __launch_bounds__(kSumWarps* kWarp) sum_kernel(
       pieces += more;
       if (more < kWarp) break;
     }
-    if (lane == 0) a.long_runs[atomicAdd(a.n_long, 1u)] = LongRun{uint32_t(b), last, pieces, 0u};
+    if (lane == 0) {
+      const int many = pieces >= kManyPieces;
+      const uint32_t k = atomicAdd(&a.n_long[many], 1u);
+      a.long_runs[many ? a.last_run - k : k] = LongRun{uint32_t(b), last, pieces, 0u};
+    }
   }
 }
 
-// Adds the pieces of every long run, in order.  A CTA takes a slab of up to 128
-// columns, four a lane, and every so many-th long run.  Where a slab needs no
-// more than half a warp, several groups of lanes share it.  The groups add
-// neighbouring shares of the pieces (8 at least), and the first group adds their
-// sums.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinCols = 128;
+// Adds the pieces of every long run, in order.  A lane takes four columns, a
+// group of lanes a slab of them; the groups of a CTA add neighbouring shares of
+// the pieces (8 at least), and the first group adds their sums.  A run of few
+// pieces has slabs of 128 columns (a warp a group), one of many pieces slabs of
+// 32, so that more CTAs and more groups share it: 847 pieces of width 4032 took 40
+// us with wide slabs.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = 128, kJoinNarrow = 32;
 
-__global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(
-    const __grid_constant__ GradArgs a) {
-  __shared__ float4 part[kJoinWarps * kWarp];
+template <int LANES>
+__device__ __forceinline__ void join_run(const GradArgs& a, const LongRun& run, int64_t col0,
+                                         float4* part) {
+  constexpr int kGroups = kJoinThreads / LANES;
+  constexpr int kAhead = 8;
+  const int group = threadIdx.x / LANES;
+  const int64_t col = col0 + 4 * (threadIdx.x & (LANES - 1));
+  const int pieces = int(run.pieces);
+  int share = (pieces + kGroups - 1) / kGroups;
+  if (share < 8) share = 8;
+  const int p1 = min((group + 1) * share, pieces);
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (col < a.slot_dim) {  // whole groups of 8 columns
+    // Piece 0 is in the second slot of its block, the others in the first.
+    const float* slot = a.slots + 2 * int64_t(run.block) * a.slot_dim + col;
+    for (int p = group * share; p < p1; p += kAhead) {
+      float4 v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (p + i < p1)
+          v[i] = *reinterpret_cast<const float4*>(
+              slot + (2 * int64_t(p + i) + (p + i == 0)) * a.slot_dim);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        acc.x += v[i].x, acc.y += v[i].y, acc.z += v[i].z, acc.w += v[i].w;
+    }
+  }
+  part[threadIdx.x] = acc;
+  __syncthreads();
+  if (group == 0) {
+    for (int g = 1; g < kGroups && g * share < pieces; ++g) {
+      const float4 v = part[g * LANES + threadIdx.x];
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    const float x[4] = {acc.x, acc.y, acc.z, acc.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (col + i < a.dim) {
+        char* g = grad_at(a, run.row, col + i);
+        const float old = a.accumulate ? load1(g, a.out_type) : 0.0f;
+        store1(g, a.out_type, a.accumulate ? fmaf(a.scale, x[i], old) : a.scale * x[i]);
+      }
+    }
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ GradArgs a) {
+  __shared__ float4 part[kJoinThreads];
+  pdl_wait();
   if (blockIdx.x >= a.join_ctas) {
-    pdl_wait();
     fill_rest(a, a.fill_ctas + (blockIdx.x - a.join_ctas));
     return;
   }
-  int lanes = kWarp;  // of a group; slots are whole groups of 8 columns
-  while (lanes > 1 && 2 * a.slot_dim <= 4 * lanes) lanes /= 2;
-  const int groups = kJoinWarps * kWarp / lanes, group = threadIdx.x / lanes;
-  const int64_t col =
-      int64_t(blockIdx.x % a.join_slabs) * kJoinCols + 4 * (threadIdx.x & (lanes - 1));
-  pdl_wait();
-  const uint32_t runs = *a.n_long;
-  for (uint32_t k = blockIdx.x / a.join_slabs; k < runs; k += a.join_ctas / a.join_slabs) {
-    const LongRun run = a.long_runs[k];
-    const int64_t from = run.block, pieces = run.pieces;
-    int64_t share = (pieces + groups - 1) / groups;
-    if (share < 8) share = 8;
-    const int64_t p0 = group * share, p1 = min(p0 + share, pieces);
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (col < a.slot_dim) {
-#pragma unroll 8
-      for (int64_t p = p0; p < p1; ++p) {
-        const float4 v = *reinterpret_cast<const float4*>(
-            a.slots + (2 * (from + p) + (p == 0 ? 1 : 0)) * a.slot_dim + col);
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-      }
-    }
-    part[threadIdx.x] = acc;
-    __syncthreads();
-    if (group == 0 && col < a.dim) {
-      for (int g = 1; g < groups && g * share < pieces; ++g) {
-        const float4 v = part[g * lanes + threadIdx.x];
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
-      }
-      const float x[4] = {acc.x, acc.y, acc.z, acc.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (col + i < a.dim) {
-          char* g = grad_at(a, run.row, col + i);
-          const float old = a.accumulate ? load1(g, a.out_type) : 0.0f;
-          store1(g, a.out_type, a.accumulate ? fmaf(a.scale, x[i], old) : a.scale * x[i]);
-        }
-      }
-    }
-    __syncthreads();
-  }
+  const uint32_t few = a.n_long[0], many = a.n_long[1];
+  const uint32_t narrow = uint32_t((a.dim + kJoinNarrow - 1) / kJoinNarrow);
+  for (uint64_t k = blockIdx.x; k < uint64_t(many) * narrow; k += a.join_ctas)
+    join_run<kJoinNarrow / 4>(a, a.long_runs[a.last_run - int64_t(k / narrow)],
+                              int64_t(k % narrow) * kJoinNarrow, part);
+  for (uint64_t k = blockIdx.x; k < uint64_t(few) * a.join_slabs; k += a.join_ctas)
+    join_run<kJoinCols / 4>(a, a.long_runs[k / a.join_slabs],
+                            int64_t(k % a.join_slabs) * kJoinCols, part);
 }
 
 // ------------------------------------------------------------- few tokens
@@ -618,7 +645,7 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(
     __syncthreads();
     for (int j = threadIdx.x; j < n; j += kDirectThreads) {
       const uint64_t r = uint64_t(keys[j]) - uint64_t(r0);
-      if (r < uint64_t(rows)) atomicOr(&named[r / 32], 1u << (r & 31));
+      if (r < uint64_t(rows)) mark(named, uint32_t(r));
     }
     __syncthreads();
     for (int64_t r = warp; r < rows; r += kDirectWarps)
@@ -709,7 +736,7 @@ struct SortArgs {
   const void* ids;
   int64_t n, first_row, n_rows, padding;
   Place* places;        // the result
-  uint32_t* n_long;     // the first kernel clears it
+  uint32_t* n_long;     // the first kernel clears both
   int32_t bits, passes;  // of the keys; digits of (bits + passes - 1) / passes bits
 };
 
@@ -829,7 +856,7 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
   const int me = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_trigger();
-  if (me == 0 && threadIdx.x == 0) *a.n_long = 0u;
+  if (me == 0 && threadIdx.x < 2) a.n_long[threadIdx.x] = 0u;
   const int width = (a.bits + a.passes - 1) / a.passes;
   const uint32_t mask = (1u << width) - 1u;
   const int local0 = warp * (kWarp * ITEMS) + lane;
@@ -921,7 +948,7 @@ __global__ void __launch_bounds__(kSortThreads) count_kernel(const __grid_consta
   __shared__ RankSmem s;
   Place x[kTileItems];
   uint32_t digit[kTileItems], rank[kTileItems];
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.s.n_long = 0u;
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.s.n_long[threadIdx.x] = 0u;
   load_tile<ID>(a, x, digit);
   rank_digits<kTileItems>(s, digit, rank, a.width);
   __syncthreads();
@@ -1049,7 +1076,7 @@ GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
     p.counts = take(4 * kDigits * p.tiles);
     p.totals = take(4 * kDigits);
   }
-  p.n_long = take(4);
+  p.n_long = take(8);
   p.long_runs = take(int64_t(sizeof(LongRun)) * (p.n_blocks / 2 + 1));
   p.named = take(4 * ((n_rows + 31) / 32));
   p.slots = at;
@@ -1169,6 +1196,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
   a.slot_dim = p.slot_dim;
   a.n = n_ids;
   a.n_blocks = p.n_blocks;
+  a.last_run = p.n_blocks / 2;
   a.block = int32_t(p.block);
   a.scale = scale;
   a.accumulate = accumulate;
@@ -1251,14 +1279,12 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
                 true, 1, a);
   }
   if (ce == cudaSuccess && (n_ids > 2 * p.block || a.fill_last > 0)) {
-    // A CTA for every 128 columns, and enough in all to fill the GPU.
-    const int64_t x = (dim + kJoinCols - 1) / kJoinCols;
-    int64_t y = x >= 1216 ? 1 : 1216 / x;
-    if (y > p.n_blocks / 2) y = p.n_blocks / 2 > 0 ? p.n_blocks / 2 : 1;
-    if (n_ids <= 2 * p.block) y = 0;
-    a.join_slabs = uint32_t(x);
-    a.join_ctas = uint32_t(x * y);
-    ce = launch(join_kernel, dim3(a.join_ctas + a.fill_last), kJoinWarps * kWarp, 0, s, true, 1, a);
+    // As many CTAs as run at once, or the slabs of the runs that there can be.
+    a.join_slabs = uint32_t((dim + kJoinCols - 1) / kJoinCols);
+    int64_t joins = n_ids > 2 * p.block ? (p.n_blocks / 2) * 4 * int64_t(a.join_slabs) : 0;
+    if (joins > 1216) joins = 1216;
+    a.join_ctas = uint32_t(joins);
+    ce = launch(join_kernel, dim3(a.join_ctas + a.fill_last), kJoinThreads, 0, s, true, 1, a);
   }
   return ce == cudaSuccess
              ? LAMB_OK
