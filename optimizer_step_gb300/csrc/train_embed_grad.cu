@@ -198,13 +198,39 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const __grid_constan
   for (int i = threadIdx.x; i < kFillRows / 32; i += kFillThreads) named[i] = 0u;
   __syncthreads();
   if (SCAN) {
+    // 16 bytes of ids at a time, from the first 16-byte boundary; kAhead loads on
+    // their way together.
+    constexpr int kPer = 16 / int(sizeof(ID)), kAhead = 8;
     const ID* ids = static_cast<const ID*>(a.ids);
-#pragma unroll 4
-    for (int64_t i = threadIdx.x; i < a.n; i += kFillThreads) {
-      const ID id = ids[i];
-      const uint64_t r = uint64_t(int64_t(id)) - uint64_t(a.first_row) - uint64_t(r0);
+    const uint64_t base = uint64_t(a.first_row) + uint64_t(r0);
+    const auto look = [&](ID id) {
+      const uint64_t r = uint64_t(int64_t(id)) - base;
       if (r < uint64_t(count) && int64_t(id) != a.padding) mark(named, uint32_t(r));
+    };
+    const int64_t head =
+        min(a.n, int64_t((16 - reinterpret_cast<uintptr_t>(ids) % 16) % 16 / sizeof(ID)));
+    const int64_t vecs = (a.n - head) / kPer;
+    const uint4* from = reinterpret_cast<const uint4*>(ids + head);
+    for (int64_t v0 = threadIdx.x; v0 < vecs; v0 += kAhead * kFillThreads) {
+      uint4 q[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (v0 + i * kFillThreads < vecs) q[i] = __ldg(from + v0 + i * kFillThreads);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (v0 + i * kFillThreads >= vecs) break;
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+        if constexpr (sizeof(ID) == 8) {
+          look(ID(int64_t(uint64_t(w[1]) << 32 | w[0])));
+          look(ID(int64_t(uint64_t(w[3]) << 32 | w[2])));
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) look(ID(int32_t(w[j])));
+        }
+      }
     }
+    if (threadIdx.x < head) look(ids[threadIdx.x]);
+    if (head + vecs * kPer + threadIdx.x < a.n) look(ids[head + vecs * kPer + threadIdx.x]);
   } else {
     pdl_wait();
     const int64_t lo = lower_bound(a.places, a.n, uint32_t(r0));

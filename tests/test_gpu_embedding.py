@@ -451,6 +451,17 @@ def test_grad_refusals():
         og.embed_grad(dy, ids, out=out, first_row=-5)
 
 
+@pytest.mark.parametrize("shift", [1, 2, 3])
+@pytest.mark.parametrize("id_type", [torch.int32, torch.int64])
+def test_ids_at_any_offset(id_type, shift):
+    for n in (5, 700, 5001):
+        ids = make_ids(n + shift, 60, "uniform", n, id_type)[shift:]
+        dy = randn((n, 520), BF16, 1)
+        table = randn((60, 520), BF16, 2)
+        check_embed(og.embed(table, ids), table, ids)
+        check_grad(og.embed_grad(dy, ids, n_rows=60, padding_id=3), dy, ids, padding=3)
+
+
 def test_embed_takes_ids_of_any_shape():
     table = randn((50, 40), BF16, 1)
     for shape in ((), (3,), (2, 3), (2, 0, 3), (2, 3, 4)):
