@@ -16,13 +16,15 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kLoads = 8;
 constexpr int64_t kItemBytes = kThreads * kLoads * 16;
 // Half as many where everything fits into L2, so that a few items a CTA come
-// out more even.
+// out more even: 18.0 us instead of 18.5 for 41 MB at the time.
 constexpr int64_t kSmallTotal = 128 << 20;
-// Items of at most so many bytes are packed: one a warp of a CTA, or where that
-// gives more than kFewPacks packs, four.
+constexpr int64_t kEarlyBytes = 5 << 20;
+// Items of at most so many bytes are packed, one a warp of a CTA: 1204 tensors of up
+// to 4 KB are clipped in 12 us, four a warp in 15.
 constexpr int64_t kPackedBytes = 4096;
-constexpr size_t kFewPacks = 760;
-constexpr int kNormCtas = 5;  // per SM
+// CTAs of the norm kernel an SM; with 3 the norm of 1.2e9 fp16 grads takes 13% longer
+// than with 5, that of 10 MB 7.4 us instead of 9.6 (fewer sums to wait for).
+constexpr int kNormCtas = 5, kNormCtasSmall = 3;
 
 // One piece of work: count elements from src, written to dst; or, where `in`
 // is kPack, count items at src, a warp for each of them in turn.
@@ -229,9 +231,8 @@ __device__ __forceinline__ void publish(Scalars* sc, const Request& r, double su
 // Sum of squares: each CTA walks every gridDim.x-th item, all of them through
 // memory side by side; the last one to finish adds the CTAs' sums in order and
 // publishes.  It is bound by reading: 1.2e9 fp16 grads take 331 us on GB300, 7.3
-// TB/s (5 CTAs an SM; 3 read 13% slower, 8 2%).  With a few MB it is a chain of
-// latencies: for 6 MB the last CTA has its data after 2.7 us, the last ticket
-// comes after 4.9, the norm is there after 7.2.
+// TB/s.  With a few MB it is a chain of latencies: for 6 MB the last CTA has its data
+// after 2.7 us, the last ticket comes after 4.9, the norm is there after 7.2.
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Tables T,
                                                         const __grid_constant__ Request r) {
   __shared__ double red[kWarps];
@@ -423,7 +424,7 @@ struct train_clip_handle {
   void* block = nullptr;
   Tables T{};
   int grid = 1;
-  bool small = false;  // all grads fit into L2
+  int64_t bytes = 0;  // of grads, or kSmallTotal if there are more
 };
 
 namespace {
@@ -462,15 +463,18 @@ int launch(train_clip_handle* h, const char* what, void (*kernel)(A...), int64_t
   return ce == cudaSuccess ? LAMB_OK : cuda_fail(ce, what);
 }
 
-// CTAs that start while another kernel holds part of the GPU are spread over the
-// SMs unevenly, which a walk over many items feels: 3% at 0.6 to 7 GB, and as
-// much where the norm of the next step starts beside the clipping of this one.
-// Where they all have one item, or nothing else is running, the early start
-// saves 1 to 1.5 us.
+// Which kernel starts beside which, measured on GB300:
+// - The clipping's CTAs may start at once, beside the norm (clip): 10.4 us instead of
+//   11.8 at 6 MB, 26.6 instead of 29 at 43 MB.  Below 5 MB they rather wait until the
+//   squares are added: 9.6 us instead of 12.0 at 0.7 MB.
+// - So does whatever follows the norm alone: 5.8 us instead of 9.7 at 4 MB.
+// - The norm itself starts before the kernel in front has ended, unless it walks over
+//   many items, which CTAs that are spread over the SMs unevenly feel: 3% at 0.6 to
+//   7 GB, and as much where the norm of the next step starts beside the clipping.
 int launch_norm(train_clip_handle* h, bool alone, Request r) {
-  const bool one_each = h->T.n_items <= h->grid;
-  r.early = !alone || one_each;
-  return launch(h, "norm kernel", norm_kernel, h->grid, one_each || (alone && h->small), h->T, r);
+  r.early = !alone && h->bytes >= kEarlyBytes;
+  const bool dependent = h->T.n_items <= h->grid || (alone && h->bytes < kSmallTotal);
+  return launch(h, "norm kernel", norm_kernel, h->grid, dependent, h->T, r);
 }
 
 int launch_scale(train_clip_handle* h) {
@@ -555,13 +559,12 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
     add_items(&items, &small, s, item_bytes);
     if (items.size() > 0x7fffffff) return fail(LAMB_ERR_INVALID, "too many elements");
   }
-  const size_t per_pack = small.size() <= kWarps * kFewPacks ? kWarps : 4 * kWarps;
-  const size_t packs = (small.size() + per_pack - 1) / per_pack;
+  const size_t packs = (small.size() + kWarps - 1) / kWarps;
   const size_t n_items = items.size() + packs;  // followed by the packed ones
   for (size_t k = 0; k < packs; ++k) {
-    const size_t left = small.size() - k * per_pack;
+    const size_t left = small.size() - k * kWarps;
     Item it{};
-    it.count = int32_t(left < per_pack ? left : per_pack);
+    it.count = int32_t(left < kWarps ? left : kWarps);
     it.in = kPack;
     items.push_back(it);
   }
@@ -571,7 +574,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   if (ce == cudaSuccess)
     ce = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (ce != cudaSuccess) return cuda_fail(ce, "querying the device");
-  int64_t grid = int64_t(sms) * kNormCtas;
+  int64_t grid = int64_t(sms) * (total < kSmallTotal ? kNormCtasSmall : kNormCtas);
   if (grid > int64_t(n_items)) grid = n_items ? int64_t(n_items) : 1;
   const size_t table_bytes = (items.size() * sizeof(Item) + 255) / 256 * 256;
   const size_t part_bytes = (size_t(grid) * sizeof(double) + 255) / 256 * 256;
@@ -580,7 +583,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   if (ce != cudaSuccess) return cuda_fail(ce, "allocating the work table");
   char* p = static_cast<char*>(block);
   for (size_t k = 0; k < packs; ++k)
-    items[n_items - packs + k].src = p + (n_items + k * per_pack) * sizeof(Item);
+    items[n_items - packs + k].src = p + (n_items + k * kWarps) * sizeof(Item);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!items.empty())
     ce = cudaMemcpyAsync(p, items.data(), items.size() * sizeof(Item), cudaMemcpyHostToDevice, s);
@@ -597,7 +600,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   h->stream = s;
   h->block = block;
   h->grid = int(grid);
-  h->small = total < kSmallTotal;
+  h->bytes = total;
   h->T.items = reinterpret_cast<const Item*>(p);
   h->T.partial = reinterpret_cast<double*>(p + table_bytes);
   h->T.sc = reinterpret_cast<Scalars*>(p + table_bytes + part_bytes);

@@ -27,7 +27,7 @@ namespace {
 // named rows and zeroes some of the others; sum_kernel, with CTAs behind it
 // that zero more; join_kernel, and the rest of the zeros beside its few long
 // chains.  On GB300 (copy rate 6.79 TB/s): 32768 bf16 tokens of width 12288 into
-// a dense gradient of 32000 rows 258 us, 6.2 TB/s over the 1.59 GB that have to
+// a dense gradient of 32000 rows 255 us, 6.2 TB/s over the 1.59 GB that have to
 // move; 8192 tokens of width 4096 60 us, 5.5 TB/s (the sort takes 9.5 of them,
 // the sums 22 if nothing else is written); 50,021 tokens of which a slice of
 // 15,013 rows holds half, fp16 of width 1023 added to fp32, 51 us, 4.0 TB/s (the
@@ -655,7 +655,6 @@ __global__ void __launch_bounds__(kDirectThreads, 4) direct_kernel(
   __shared__ uint32_t named[kDirectFill / 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n = int(a.n);
-  pdl_trigger();
   pdl_wait();
   for (int j = threadIdx.x; j < n; j += kDirectThreads) {
     const int64_t id = d.ids64 ? static_cast<const int64_t*>(a.ids)[j]
@@ -1059,7 +1058,8 @@ constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
 // 1023: 65 us, with a sort 21), so only a quarter of the ids are taken.
 constexpr int64_t kDirectCtas = 4096;
 bool use_direct(int64_t n, int64_t dim) {
-  return n <= (dim % 8 == 0 ? kDirectIds : kDirectIds / 4) && n * ((dim + kDirectCols - 1) / kDirectCols) <= kDirectCtas;
+  return n <= (dim % 8 == 0 ? kDirectIds : kDirectIds / 4) &&
+         n * ((dim + kDirectCols - 1) / kDirectCols) <= kDirectCtas;
 }
 
 using DirectKernel = void (*)(DirectArgs);
