@@ -119,7 +119,8 @@ typedef struct train_clip_handle train_clip_handle;
  *   outs         NULL: clipping works in place.  Else outs[i] receives tensor
  *                i's clipped grads in out_dtypes[i]; each is grads[i] itself
  *                (then of the same type) or overlaps none of the grads
- * The four arrays are host arrays, read before the call returns.  The call
+ * The tensors do not overlap one another.
+ * The arrays are host arrays, read before the call returns.  The call
  * waits for the upload of its work table.
  */
 LAMB_API int train_clip_create(train_clip_handle** out, int32_t n_tensors, const int64_t* sizes,

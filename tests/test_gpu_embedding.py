@@ -425,6 +425,59 @@ def test_calls_can_be_captured_into_a_graph():
     check_grad(grad, dy, ids, 2.0)
 
 
+def test_a_graph_with_copies_and_fills_between_the_calls():
+    """Copies and fills in front of and between the calls keep their order."""
+    table, ids = randn((600, 136), BF16, 1), make_ids(6000, 600, "zipf", 2)
+    dy, few = randn((6000, 136), BF16, 3), make_ids(40, 600, "uniform", 4)
+    table_in, ids_in, dy_in = torch.zeros_like(table), torch.zeros_like(ids), torch.zeros_like(dy)
+    out, grad = torch.empty_like(dy), torch.empty((600, 136), dtype=FP32, device="cuda")
+    small = torch.empty((600, 136), dtype=FP32, device="cuda")
+
+    def work():
+        table_in.copy_(table)
+        ids_in.copy_(ids)
+        og.embed(table_in, ids_in, out=out)
+        dy_in.copy_(out)
+        grad.fill_(1.0)
+        og.embed_grad(dy_in, ids_in, out=grad, accumulate=True)
+        dy_in.zero_()
+        small.copy_(grad)
+        og.embed_grad(out[:40], few, out=small, accumulate=True)
+        out.zero_()
+
+    work()
+    torch.cuda.synchronize()
+    want, want_small = grad.clone(), small.clone()
+    check_grad(want, table[ids], ids, old=torch.ones_like(grad))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        work()
+    for _ in range(3):
+        grad.fill_(-5.0)
+        small.fill_(-5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(grad, want) and torch.equal(small, want_small)
+
+
+def test_calls_on_several_streams_at_once():
+    cases = []
+    for k, n in enumerate((300, 9000, 40_000, 150_000)):
+        ids = make_ids(n, 5000, "zipf", k)
+        dy = randn((n, 200), BF16, k + 10)
+        cases.append((dy, ids, og.embed_grad(dy, ids, n_rows=5000), og.embed(dy[:5000], ids)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = []
+    for _ in range(10):
+        for (dy, ids, _, _), stream in zip(cases, streams):
+            with torch.cuda.stream(stream):
+                got.append((og.embed_grad(dy, ids, n_rows=5000), og.embed(dy[:5000], ids)))
+    torch.cuda.synchronize()
+    for i, (grad, out) in enumerate(got):
+        assert torch.equal(grad, cases[i % 4][2]) and torch.equal(out, cases[i % 4][3])
+
+
 def test_grad_refusals():
     dy = randn((4, 16), BF16, 1)
     ids = torch.zeros(4, dtype=torch.int64, device="cuda")
