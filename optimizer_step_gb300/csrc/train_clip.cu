@@ -15,8 +15,10 @@ constexpr int kWarps = kThreads / 32;
 // Bytes of grads in one piece of work: eight 16-byte loads a thread.
 constexpr int kLoads = 8;
 constexpr int64_t kItemBytes = kThreads * kLoads * 16;
-// Half as many where everything fits into L2, so that a few items a CTA come
-// out more even: 18.0 us instead of 18.5 for 41 MB at the time.
+// Half as many below 16 MB, where whole ones leave SMs idle: 10.4 us instead of 12.8
+// to clip 6 MB, while 43 MB take 22 us with whole ones and 26.5 with halves.
+constexpr int64_t kHalfBytes = 16 << 20;
+// What fits into L2.
 constexpr int64_t kSmallTotal = 128 << 20;
 constexpr int64_t kEarlyBytes = 5 << 20;
 // Items of at most so many bytes are packed, one a warp of a CTA: 1204 tensors of up
@@ -545,7 +547,7 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
   // In the order of memory, neighbours joined.
   std::stable_sort(spans.begin(), spans.end(),
                    [](const Span& a, const Span& b) { return a.src < b.src; });
-  const int64_t item_bytes = total < kSmallTotal ? kItemBytes / 2 : kItemBytes;
+  const int64_t item_bytes = total < kHalfBytes ? kItemBytes / 2 : kItemBytes;
   std::vector<Item> items, small;
   for (size_t i = 0; i < spans.size();) {
     Span s = spans[i];
