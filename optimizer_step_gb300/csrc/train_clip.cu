@@ -355,7 +355,7 @@ __device__ __forceinline__ void item_scale(const Item& it, int tid, int threads,
       uint32_t y[kPer / 2];
 #pragma unroll
       for (int i = 0; i < kPer / 2; ++i)
-        y[i] = uint32_t(from_float<OUT>(x[2 * i])) | uint32_t(from_float<OUT>(x[2 * i + 1])) << 16;
+        y[i] = pack2<OUT>(x[2 * i], x[2 * i + 1]);
       if constexpr (kPer == 8)
         *reinterpret_cast<uint4*>(dst + int64_t(v) * kPer) = make_uint4(y[0], y[1], y[2], y[3]);
       else

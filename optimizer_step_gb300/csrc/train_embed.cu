@@ -84,8 +84,10 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(const __grid_constant__
     }
 #pragma unroll
     for (int m = 0; m < M; ++m) {
+      float v[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) y.set(i, a.scale * x[r][m].get(i));
+      for (int i = 0; i < VEC; ++i) v[i] = a.scale * x[r][m].get(i);
+      y.set(v);
       if (unit0 + m * kWarp < a.units) y.store(out + m * (kWarp * VEC));
     }
   }

@@ -124,13 +124,9 @@ __device__ __forceinline__ void store8(void* p, int type, const float (&x)[8]) {
   }
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[2 * i])
-                                           : from_float<TRAIN_FP16>(x[2 * i]);
-    const uint32_t hi = type == TRAIN_BF16 ? from_float<TRAIN_BF16>(x[2 * i + 1])
-                                           : from_float<TRAIN_FP16>(x[2 * i + 1]);
-    w[i] = lo | hi << 16;
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = type == TRAIN_BF16 ? pack2<TRAIN_BF16>(x[2 * i], x[2 * i + 1])
+                              : pack2<TRAIN_FP16>(x[2 * i], x[2 * i + 1]);
   *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -46,6 +46,19 @@ __device__ __forceinline__ typename TypeOf<DT>::T from_float(float x) {
   if constexpr (DT == TRAIN_FP32) return x;
 }
 
+// Two values rounded to 16 bits, the first in the low half: one instruction.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  static_assert(DT != TRAIN_FP32, "16-bit types");
+  if constexpr (DT == TRAIN_BF16) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  } else {
+    const __half2 p = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&p);
+  }
+}
+
 template <int DT>
 struct Type {
   static constexpr int value = DT;
@@ -108,12 +121,15 @@ struct Pack {
       return to_float<DT>(uint16_t((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu));
     }
   }
-  __device__ __forceinline__ void set(int i, float x) {
+  __device__ __forceinline__ void set(const float (&x)[VEC]) {
     if constexpr (DT == TRAIN_FP32) {
-      w[i] = __float_as_uint(x);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) w[i] = __float_as_uint(x[i]);
+    } else if constexpr (VEC == 1) {
+      w[0] = from_float<DT>(x[0]);
     } else {
-      const uint32_t h = from_float<DT>(x);
-      w[i / 2] = (i & 1) ? w[i / 2] | h << 16 : h;
+#pragma unroll
+      for (int i = 0; i < VEC / 2; ++i) w[i] = pack2<DT>(x[2 * i], x[2 * i + 1]);
     }
   }
 };
