@@ -59,11 +59,15 @@ def _row_stride(name, t):
     return stride
 
 
-def _ids_code(ids, index):
-    code = _code("ids", ids, _ID_TYPES, index)
+def _refuse(name, t, ids):
+    """Says what is wrong with a call's matrix ``t`` or its ids."""
+    index = t.get_device() if isinstance(t, torch.Tensor) else -1
+    _code(name, t, _TYPES, index)
+    _code("ids", ids, _ID_TYPES, index)
     if not ids.is_contiguous():
         raise ValueError("ids: must be contiguous")
-    return code
+    raise TypeError(f"{name}: expected a tensor of two dimensions" if name == "table"
+                    else f"{name}: expected a tensor of one dimension or more")
 
 
 def _enqueue(index, call, *args):
@@ -94,12 +98,15 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
     may hold the slice of a vocabulary that starts at token ``first_row``: a
     token outside the slice gives a row of zeros.
     """
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise TypeError("table: expected a tensor of two dimensions")
-    index = table.get_device()
-    t_code = _code("table", table, _TYPES, index)
-    i_code = _ids_code(ids, index)
-    rows, dim = table.shape
+    try:
+        t_code, i_code = _TYPES[table.dtype], _ID_TYPES[ids.dtype]
+        rows, dim = table.shape
+        index = table.get_device()
+        fine = index >= 0 and ids.get_device() == index and ids.is_contiguous()
+    except (AttributeError, KeyError, ValueError):
+        fine = False
+    if not fine:
+        _refuse("table", table, ids)
     t_stride = dim if table.is_contiguous() else _row_stride("table", table)
     if out is None:
         o_code = t_code if out_dtype is None else _TYPES.get(out_dtype)
@@ -132,12 +139,15 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
     as they are.  Tokens outside the slice that starts at ``first_row``, and
     ``padding_id`` (negative: none), add nothing.
     """
-    if not isinstance(grad_out, torch.Tensor) or grad_out.dim() == 0:
-        raise TypeError("grad_out: expected a tensor of one dimension or more")
-    index = grad_out.get_device()
-    g_code = _code("grad_out", grad_out, _TYPES, index)
-    i_code = _ids_code(ids, index)
-    dim = grad_out.shape[-1]
+    try:
+        g_code, i_code = _TYPES[grad_out.dtype], _ID_TYPES[ids.dtype]
+        dim = grad_out.shape[-1]
+        index = grad_out.get_device()
+        fine = index >= 0 and ids.get_device() == index and ids.is_contiguous()
+    except (AttributeError, KeyError, IndexError):
+        fine = False
+    if not fine:
+        _refuse("grad_out", grad_out, ids)
     g_stride = dim if grad_out.is_contiguous() else _row_stride("grad_out", grad_out)
     if grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out: expected ids.shape + (dim,)")
