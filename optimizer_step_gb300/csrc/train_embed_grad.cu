@@ -27,7 +27,7 @@ namespace {
 // named rows and zeroes some of the others; sum_kernel, with CTAs behind it
 // that zero more; join_kernel, and the rest of the zeros beside its few long
 // chains.  On GB300 (copy rate 6.79 TB/s): 32768 bf16 tokens of width 12288 into
-// a dense gradient of 32000 rows 255 us, 6.2 TB/s over the 1.59 GB that have to
+// a dense gradient of 32000 rows 252 us, 6.3 TB/s over the 1.59 GB that have to
 // move; 8192 tokens of width 4096 60 us, 5.5 TB/s (the sort takes 9.5 of them,
 // the sums 22 if nothing else is written); 50,021 tokens of which a slice of
 // 15,013 rows holds half, fp16 of width 1023 added to fp32, 51 us, 4.0 TB/s (the
