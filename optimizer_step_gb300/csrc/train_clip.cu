@@ -558,8 +558,10 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
         break;
       s.n += next.n;
     }
+    // Refused before they are cut, which would fill the host's memory first.
+    if (int64_t(items.size() + small.size()) + s.n / (item_bytes / size_of(s.in)) > kMaxCount / 2)
+      return fail(LAMB_ERR_INVALID, "too many elements");
     add_items(&items, &small, s, item_bytes);
-    if (items.size() > 0x7fffffff) return fail(LAMB_ERR_INVALID, "too many elements");
   }
   const size_t packs = (small.size() + kWarps - 1) / kWarps;
   const size_t n_items = items.size() + packs;  // followed by the packed ones

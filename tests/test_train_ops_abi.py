@@ -152,6 +152,17 @@ def test_clip_create_refuses():
     assert not h.value
 
 
+@pytest.mark.parametrize("size", [1 << 50, (1 << 60) - 1, 1 << 62])
+def test_clip_create_refuses_sizes_beyond_any_memory_at_once(size):
+    # More than a table of 2^30 pieces can name; nothing is laid out for it.
+    lib, h = og.load(), ctypes.c_void_p()
+    sizes, types = np.array([64, size], np.int64), np.zeros(2, np.int32)
+    rc = lib.train_clip_create(ctypes.byref(h), 2, sizes.ctypes.data, types.ctypes.data,
+                               (ctypes.c_void_p * 2)(P, 4 * P), None, None, None)
+    assert rc == INVALID and not h.value
+    assert "too" in lib.lamb_last_error().decode()
+
+
 def test_clip_calls_refuse_a_missing_handle():
     lib = og.load()
     assert lib.train_clip_norm(None, 1.0, P) == INVALID
