@@ -16,7 +16,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kLoads = 8;
 constexpr int64_t kItemBytes = kThreads * kLoads * 16;
 // Half as many below 16 MB, where whole ones leave SMs idle: 10.4 us instead of 12.8
-// to clip 6 MB, while 43 MB take 22 us with whole ones and 26.5 with halves.
+// to clip 6 MB at the time, while 43 MB take 22 us with whole ones and 26.5 with halves.
 constexpr int64_t kHalfBytes = 16 << 20;
 // What fits into L2.
 constexpr int64_t kSmallTotal = 128 << 20;
@@ -67,21 +67,19 @@ __device__ __forceinline__ uint4 load16(const void* p) {
   return q;
 }
 
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-
-// Fixed-shape block sum; the result is valid in the first warp.
+// Fixed-shape block sum; the result is valid in the first warp.  An fp64 instruction
+// of a warp takes 16 cycles of its SM, so one warp adds the threads' values (13 such
+// instructions, where shuffles in every warp are 64): 8.5 us instead of 10.1 to clip
+// 6 MB, 8.7 instead of 9.4 for the norm of 43 MB.
 __device__ __forceinline__ double block_sum(double x, double* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  x = warp_sum(x);
-  if (lane == 0) red[warp] = x;
+  red[threadIdx.x] = x;
   __syncthreads();
-  double y = red[lane & (kWarps - 1)];
+  if (threadIdx.x >= kWarp) return 0.0;
+  double y = red[threadIdx.x];
 #pragma unroll
-  for (int o = kWarps / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+  for (int w = 1; w < kWarps; ++w) y += red[w * kWarp + threadIdx.x];
+#pragma unroll
+  for (int o = kWarp / 2; o > 0; o >>= 1) y += __shfl_xor_sync(kAll, y, o);
   return y;
 }
 
@@ -233,11 +231,11 @@ __device__ __forceinline__ void publish(Scalars* sc, const Request& r, double su
 // Sum of squares: each CTA walks every gridDim.x-th item, all of them through
 // memory side by side; the last one to finish adds the CTAs' sums in order and
 // publishes.  It is bound by reading: 1.2e9 fp16 grads take 331 us on GB300, 7.3
-// TB/s.  With a few MB it is a chain of latencies: for 6 MB the last CTA has its data
-// after 2.7 us, the last ticket comes after 4.9, the norm is there after 7.2.
+// TB/s.  With a few MB it is a chain of latencies: for 6 MB, 5.7 us a call, the last
+// CTA has its data after 2.7 us; the CTAs' sums, tickets and their sum are the rest.
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Tables T,
                                                         const __grid_constant__ Request r) {
-  __shared__ double red[kWarps];
+  __shared__ double red[kThreads];
   __shared__ uint32_t last;
   if (r.early) pdl_trigger();
   double acc = 0.0;
@@ -272,8 +270,9 @@ __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ 
   }
   __syncthreads();
   if (!last) return;
-  double sum = 0.0;
-  for (int i = threadIdx.x; i < int(gridDim.x); i += kThreads) sum += __ldcg(&T.partial[i]);
+  double sum = threadIdx.x < gridDim.x ? __ldcg(&T.partial[threadIdx.x]) : 0.0;
+  for (int i = threadIdx.x + kThreads; i < int(gridDim.x); i += kThreads)
+    sum += __ldcg(&T.partial[i]);
   sum = block_sum(sum, red);
   if (threadIdx.x != 0) return;
   T.sc->ticket = 0;
@@ -467,8 +466,8 @@ int launch(train_clip_handle* h, const char* what, void (*kernel)(A...), int64_t
 
 // Which kernel starts beside which, measured on GB300:
 // - The clipping's CTAs may start at once, beside the norm (clip): 10.4 us instead of
-//   11.8 at 6 MB, 26.6 instead of 29 at 43 MB.  Below 5 MB they rather wait until the
-//   squares are added: 9.6 us instead of 12.0 at 0.7 MB.
+//   11.8 at 6 MB at the time, 26.6 instead of 29 at 43 MB.  Below 5 MB they rather
+//   wait until the squares are added: 9.6 us instead of 12.0 at 0.7 MB.
 // - So does whatever follows the norm alone: 5.8 us instead of 9.7 at 4 MB.
 // - The norm itself starts before the kernel in front has ended, unless it walks over
 //   many items, which CTAs that are spread over the SMs unevenly feel: 3% at 0.6 to
