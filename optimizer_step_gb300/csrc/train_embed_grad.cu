@@ -855,6 +855,16 @@ __device__ __forceinline__ void digit_bases(RankSmem& s, uint32_t all, uint32_t 
   __syncthreads();
 }
 
+// A barrier of the cluster in two halves.  Shared memory of another CTA may be
+// used only once that CTA runs: each arrives as it starts, and waits for the
+// others in front of its first remote store, behind its own loads and ranks.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
 // Up to 16 * 1024 * ITEMS positions in one cluster: every CTA holds a tile of
 // 1024 * ITEMS elements, and the CTAs exchange their digit counts.  A CTA
 // first orders its tile by digit in its own shared memory, so that a warp then
@@ -876,6 +886,7 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
   cg::cluster_group cluster = cg::this_cluster();
   const int me = int(cluster.block_rank()), ctas = int(cluster.num_blocks());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  cluster_arrive();
   pdl_trigger();
   if (me == 0 && threadIdx.x < 2) a.n_long[threadIdx.x] = 0u;
   const int width = (a.bits + a.passes - 1) / a.passes;
@@ -899,6 +910,7 @@ __global__ void __launch_bounds__(kSortThreads) cluster_sort_kernel(
     for (int j = 0; j < ITEMS; ++j) digit[j] = (x[j].key >> (p * width)) & mask;
     rank_digits<ITEMS>(s, digit, rank, width);
     __syncthreads();
+    if (p == 0) cluster_wait();
     // Every CTA gets every CTA's counts.
     const int d = threadIdx.x & (kDigits - 1);
     for (int r = threadIdx.x / kDigits; r < ctas; r += kSortThreads / kDigits)
