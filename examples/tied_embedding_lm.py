@@ -6,7 +6,8 @@ step sums the grads of a few micro-batches in fp32, where the table gets two
 contributions: the head's product, and on top of it the lookup's gradient by
 sorted tokens.  GradClip takes the fp32 sums to the bf16 grads that the step
 reads, clipped by their global norm, and Lamb updates the weights.  Nothing
-waits for the GPU within a step.
+waits for the GPU within a step: when the sums overflow, the clip leaves NaN in
+the step's grads and the step skips.
 
     python examples/tied_embedding_lm.py [--steps 60]
 """
@@ -52,7 +53,7 @@ class TiedLM:
         _, self.grads = flat(sizes, torch.bfloat16, device)
         _, exp_avg = flat(sizes, torch.float32, device)
         _, exp_avg_sq = flat(sizes, torch.float32, device)
-        self.clipper = GradClip(self.sum_views, out=self.grads)
+        self.clipper = GradClip(self.sum_views, out=self.grads, poison=True)
         self.opt = Lamb(self.weights, exp_avg, exp_avg_sq, self.w16, [1, 1])
         self.opt.set_step(1)
 

@@ -10,12 +10,15 @@
  *                      ids[i] = first_row + v of grad_out[i, :])
  *   train_clip_*       G = ||g / S|| over all tensors;
  *                      c = max_norm / G if max_norm > 0 and G > max_norm, else 1;
- *                      out = round(c / S * g); inf/NaN anywhere: nothing written
+ *                      out = round(c / S * g); inf/NaN anywhere: nothing written,
+ *                      or NaN everywhere (train_clip_set_poison)
  *
  * With them a language model's training step runs around lamb_step: the
  * lookup starts the forward pass, the gradient by sorted tokens ends the
  * backward pass in the grad buffer that the step reads, and the clip takes
- * grads summed in fp32 (or in 16 bits) to the 16-bit grads of the step.
+ * grads summed in fp32 (or in 16 bits) to the 16-bit grads of the step.  A clip
+ * into other tensors that a step reads needs train_clip_set_poison, or the step
+ * does not learn of an overflow.
  *
  * Element types.  Every matrix and tensor is bf16, fp16 or fp32
  * (TRAIN_BF16, TRAIN_FP16, TRAIN_FP32), and input and output types need not
@@ -128,6 +131,23 @@ LAMB_API int train_clip_create(train_clip_handle** out, int32_t n_tensors, const
                                const int32_t* out_dtypes, void* stream);
 
 /*
+ * What clipping leaves in the outputs when a grad is inf or NaN.  poison 0, as a
+ * handle is made: nothing is written, they keep what they held.  1: every output
+ * becomes NaN, those in place too.
+ *
+ * A step that reads outputs in other tensors needs 1 (or must wait for stats[2]):
+ * lamb_step looks for inf and NaN in the grads that it is given, and would find
+ * the clipped grads of the step before, finite, and apply them again.  With NaN
+ * there it skips, and its loss scaler backs off.  The same holds in place for
+ * grads spread over ranks without the split step: what train_clip_finish knows
+ * of another rank's overflow, this rank's grads do not show.
+ *
+ * The call only sets the handle; calls made later use it (and so does a graph
+ * that they are captured into).
+ */
+LAMB_API int train_clip_set_poison(train_clip_handle* h, int32_t poison);
+
+/*
  * The norm alone.  stats (device, 3 floats) receives
  *   stats[0]  G = ||g / S||, +inf if a grad is inf or NaN
  *   stats[1]  the factor c / S that clipping multiplies the grads by (here
@@ -140,7 +160,8 @@ LAMB_API int train_clip_norm(train_clip_handle* h, float loss_scale, float* stat
 
 /* The norm, then out = round(c / S * g) for every tensor; max_norm <= 0 (or
  * a norm of at most max_norm) leaves c = 1.  If a grad is inf or NaN nothing
- * is written but stats.  In place with c / S = 1 nothing needs writing. */
+ * is written but stats, or NaN to every output (train_clip_set_poison).  In
+ * place with c / S = 1 nothing needs writing. */
 LAMB_API int train_clip_grads(train_clip_handle* h, float max_norm, float loss_scale,
                               float* stats);
 

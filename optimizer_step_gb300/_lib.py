@@ -32,8 +32,9 @@ EXPORTS = ("lamb_create", "lamb_step", "lamb_destroy", "lamb_last_error", "lamb_
 
 # Every symbol include/train_ops.h declares.
 TRAIN_EXPORTS = ("train_embed", "train_embed_grad_workspace", "train_embed_grad",
-                 "train_clip_create", "train_clip_norm", "train_clip_grads",
-                 "train_clip_partial", "train_clip_finish", "train_clip_destroy")
+                 "train_clip_create", "train_clip_set_poison", "train_clip_norm",
+                 "train_clip_grads", "train_clip_partial", "train_clip_finish",
+                 "train_clip_destroy")
 TRAIN_BF16 = 0
 TRAIN_FP16 = 1
 TRAIN_FP32 = 2
@@ -159,6 +160,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                          i64, i64, i64, P, i64, P]
         lib.train_clip_create.restype = ctypes.c_int
         lib.train_clip_create.argtypes = [ctypes.POINTER(P), i32, P, P, P, P, P, P]
+        lib.train_clip_set_poison.restype = ctypes.c_int
+        lib.train_clip_set_poison.argtypes = [P, i32]
         lib.train_clip_norm.restype = ctypes.c_int
         lib.train_clip_norm.argtypes = [P, f32, P]
         lib.train_clip_grads.restype = ctypes.c_int

@@ -55,6 +55,7 @@ struct Tables {
   double* partial;  // per CTA of the norm kernel
   Scalars* sc;
   int64_t n_items;
+  int32_t poison;  // outputs become NaN when a grad is inf or NaN
 };
 
 // 16 bytes, in order with the other loads of its kind: a thread's loads are all
@@ -387,8 +388,11 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(Tables T) {
   const Item it = T.items[T.n_items - 1 - blockIdx.x];
   pdl_trigger();
   pdl_wait();
-  const float factor = T.sc->factor;
-  if (T.sc->bad) return;
+  float factor = T.sc->factor;
+  if (T.sc->bad) {
+    if (!T.poison) return;
+    factor = __int_as_float(0x7fffffff);  // NaN times anything
+  }
   const bool pack = it.in == kPack;
   const Item* packed = static_cast<const Item*>(it.src);
   const int count = pack ? it.count : 1, tid = pack ? threadIdx.x & 31 : threadIdx.x;
@@ -632,6 +636,14 @@ LAMB_API int train_clip_create(train_clip_handle** out, int32_t n_tensors, const
   } catch (const std::bad_alloc&) {
     return fail(LAMB_ERR_NOMEM, "out of host memory");
   }
+}
+
+LAMB_API int train_clip_set_poison(train_clip_handle* h, int32_t poison) {
+  lambgb::set_last_error("");
+  if (!h) return fail(LAMB_ERR_INVALID, "handle is NULL");
+  if (poison != 0 && poison != 1) return fail(LAMB_ERR_INVALID, "poison must be 0 or 1");
+  h->T.poison = poison;
+  return LAMB_OK;
 }
 
 LAMB_API int train_clip_norm(train_clip_handle* h, float loss_scale, float* stats) {

@@ -38,6 +38,13 @@ class GradClip:
     each of any of the three types.  ``stream`` defaults to the current torch
     stream at construction; every call runs on it and returns without waiting.
 
+    ``poison``: what ``clip`` and ``finish`` leave in the outputs when a grad is
+    inf or NaN.  False: what they held.  True: NaN in every output.  A step that
+    reads outputs in other tensors needs True, unless the program looks at
+    ``stats`` first: ``Lamb`` skips when it finds inf or NaN in its grads, and
+    would else apply the clipped grads of the step before again.  So do steps on
+    grads clipped in place over several ranks without the split step.
+
     The calls return ``stats``, a float32 CUDA tensor that the next call
     overwrites: the norm of ``g / loss_scale`` (inf if a grad is inf or NaN),
     the factor that the grads are multiplied by (0 then), and 1.0 if a grad is
@@ -45,7 +52,8 @@ class GradClip:
     """
 
     def __init__(self, grads: Sequence[torch.Tensor],
-                 out: Sequence[torch.Tensor] | None = None, stream=None):
+                 out: Sequence[torch.Tensor] | None = None, stream=None, *,
+                 poison: bool = False):
         self._lib = _lib.load()
         self._h = None
         grads = list(grads)
@@ -76,6 +84,7 @@ class GradClip:
                 address(out_ptrs), address(out_types),
                 ctypes.c_void_p(self.stream.cuda_stream)))
         self._h = h
+        check(self._lib.train_clip_set_poison(h, 1 if poison else 0))
         self._stats_ptr = self.stats.data_ptr()
 
     def _handle(self):
@@ -91,7 +100,7 @@ class GradClip:
     def clip(self, max_norm: float, loss_scale: float = 1.0) -> torch.Tensor:
         """Divides the grads by ``loss_scale`` and clips their global norm to
         ``max_norm`` (<= 0: no clipping), rounding once.  If a grad is inf or
-        NaN the outputs stay as they are."""
+        NaN the outputs stay as they are, or all become NaN (``poison``)."""
         check(self._lib.train_clip_grads(self._handle(), max_norm, loss_scale, self._stats_ptr))
         return self.stats
 
