@@ -81,6 +81,29 @@ def _enqueue(index, call, *args):
         check(rc)
 
 
+class _Embed(torch.autograd.Function):
+    """The lookup of a table that requires grad."""
+
+    @staticmethod
+    def forward(ctx, table, ids, scale, first_row, out_dtype):
+        ctx.save_for_backward(ids)
+        ctx.scale, ctx.first_row = scale, first_row
+        ctx.n_rows, ctx.dtype = table.shape[0], table.dtype
+        return embed(table, ids, scale=scale, first_row=first_row, out_dtype=out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_out):
+        ids, = ctx.saved_tensors
+        try:
+            _row_stride("grad_out", grad_out)
+        except ValueError:  # one row for many, or rows that step unevenly
+            grad_out = grad_out.contiguous()
+        grad = embed_grad(grad_out, ids, n_rows=ctx.n_rows, scale=ctx.scale,
+                          first_row=ctx.first_row, dtype=ctx.dtype)
+        return grad, None, None, None, None
+
+
 @functools.lru_cache(maxsize=256)
 def _workspace_bytes(n_ids, n_rows, dim):
     need = ctypes.c_int64()
@@ -97,6 +120,10 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
     ``out_dtype`` (default: the table's), or is written to ``out``.  The table
     may hold the slice of a vocabulary that starts at token ``first_row``: a
     token outside the slice gives a row of zeros.
+
+    If the table requires grad, so does the result: its gradient is
+    ``embed_grad`` into a new table of the same type.  It can be
+    differentiated once, and ``out`` is refused then.
     """
     try:
         t_code, i_code = _TYPES[table.dtype], _ID_TYPES[ids.dtype]
@@ -107,6 +134,10 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
         fine = False
     if not fine:
         _refuse("table", table, ids)
+    if table.requires_grad and torch.is_grad_enabled():
+        if out is not None:
+            raise RuntimeError("embed: out= cannot be given for a table that requires grad")
+        return _Embed.apply(table, ids, scale, first_row, out_dtype)
     t_stride = dim if table.is_contiguous() else _row_stride("table", table)
     if out is None:
         o_code = t_code if out_dtype is None else _TYPES.get(out_dtype)
@@ -137,7 +168,7 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
     the ids fix, rounded once.  Rows without a token become zero, or with
     ``accumulate`` the sums are added to what ``out`` holds and those rows stay
     as they are.  Tokens outside the slice that starts at ``first_row``, and
-    ``padding_id`` (negative: none), add nothing.
+    ``padding_id`` (negative: none), add nothing.  The result has no history.
     """
     try:
         g_code, i_code = _TYPES[grad_out.dtype], _ID_TYPES[ids.dtype]
