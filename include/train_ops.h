@@ -62,8 +62,9 @@ extern "C" {
  *
  *   table        n_rows x dim, rows table_stride elements apart, read only
  *   ids          n_ids token ids (TRAIN_INT32 or TRAIN_INT64), consecutive
- *   first_row    the token id of the table's first row (>= 0): a table may
- *                hold a slice of the vocabulary.  A token outside
+ *   first_row    the token id of the table's first row (>= 0; the last row's
+ *                is at most 2^63 - 1): a table may hold a slice of the
+ *                vocabulary.  A token outside
  *                [first_row, first_row + n_rows), negative ones among them,
  *                gives a row of zeros, so that the slices' results add up
  *   out          n_ids x dim, rows out_stride elements apart

@@ -152,7 +152,7 @@ LAMB_API int train_embed(const void* table, int32_t table_dtype, int64_t n_rows,
                          int32_t out_dtype, int64_t out_stride, void* stream) {
   lambgb::set_last_error("");
   int rc = check_matrix("table", table, table_dtype, n_rows, dim, table_stride);
-  if (rc == LAMB_OK) rc = check_ids(ids, ids_dtype, n_ids, first_row);
+  if (rc == LAMB_OK) rc = check_ids(ids, ids_dtype, n_ids, first_row, n_rows);
   if (rc == LAMB_OK) rc = check_matrix("out", out, out_dtype, n_ids, dim, out_stride);
   if (rc != LAMB_OK) return rc;
   if (n_ids == 0 || dim == 0) return LAMB_OK;

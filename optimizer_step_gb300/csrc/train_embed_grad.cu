@@ -1193,7 +1193,7 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
                               int64_t n_rows, int64_t dim, int64_t grad_stride, void* workspace,
                               int64_t workspace_bytes, void* stream) {
   lambgb::set_last_error("");
-  int rc = check_ids(ids, ids_dtype, n_ids, first_row);
+  int rc = check_ids(ids, ids_dtype, n_ids, first_row, n_rows);
   if (rc == LAMB_OK)
     rc = check_matrix("grad_out", grad_out, grad_out_dtype, n_ids, dim, grad_out_stride);
   if (rc == LAMB_OK) rc = check_matrix("grad", grad, grad_dtype, n_rows, dim, grad_stride);

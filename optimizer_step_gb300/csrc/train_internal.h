@@ -177,12 +177,16 @@ inline int check_matrix(const char* name, const void* p, int32_t dtype, int64_t 
   return LAMB_OK;
 }
 
-inline int check_ids(const void* ids, int32_t ids_dtype, int64_t n_ids, int64_t first_row) {
+inline int check_ids(const void* ids, int32_t ids_dtype, int64_t n_ids, int64_t first_row,
+                     int64_t n_rows) {
   if (ids_dtype != TRAIN_INT32 && ids_dtype != TRAIN_INT64)
     return fail(LAMB_ERR_INVALID, "ids: unknown type");
   if (n_ids < 0 || n_ids > kMaxCount)
     return fail(LAMB_ERR_INVALID, "n_ids must be in [0, 2^31 - 1]");
   if (first_row < 0) return fail(LAMB_ERR_INVALID, "first_row must be >= 0");
+  // Rows behind the last number would be named by negative ids.
+  if (n_rows > 0 && first_row > INT64_MAX - (n_rows - 1))
+    return fail(LAMB_ERR_INVALID, "first_row + n_rows - 1 must be at most 2^63 - 1");
   if (n_ids == 0) return LAMB_OK;
   if (!ids) return fail(LAMB_ERR_INVALID, "ids is NULL");
   if (reinterpret_cast<uintptr_t>(ids) % (ids_dtype == TRAIN_INT64 ? 8u : 4u))
