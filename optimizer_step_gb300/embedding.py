@@ -59,6 +59,12 @@ def _row_stride(name, t):
     return stride
 
 
+def _fits(name, number):
+    """Refuses a token number that the C ABI would take modulo 2^64."""
+    if not -2 ** 63 <= number < 2 ** 63:
+        raise ValueError(f"{name}: expected a number of 64 bits, got {number}")
+
+
 def _refuse(name, t, ids):
     """Says what is wrong with a call's matrix ``t`` or its ids."""
     index = t.get_device() if isinstance(t, torch.Tensor) else -1
@@ -134,6 +140,7 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
         fine = False
     if not fine:
         _refuse("table", table, ids)
+    _fits("first_row", first_row)
     if table.requires_grad and torch.is_grad_enabled():
         if out is not None:
             raise RuntimeError("embed: out= cannot be given for a table that requires grad")
@@ -179,6 +186,8 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
         fine = False
     if not fine:
         _refuse("grad_out", grad_out, ids)
+    _fits("first_row", first_row)
+    _fits("padding_id", padding_id)
     g_stride = dim if grad_out.is_contiguous() else _row_stride("grad_out", grad_out)
     if grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out: expected ids.shape + (dim,)")
