@@ -99,6 +99,7 @@ LAMB_API int train_embed_grad_workspace(int64_t n_ids, int64_t n_rows, int64_t d
  *                train_embed_grad_workspace bytes; its contents before the
  *                call do not matter, and it is free again when the stream has
  *                passed the call
+ * n_ids * dim and n_rows * dim are at most 2^40.
  */
 LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
                               int64_t grad_out_stride, const void* ids, int32_t ids_dtype,

@@ -1056,6 +1056,9 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
 // 75.6 and 75.3 us for 8192 tokens of width 4096 at the time.
 constexpr double kFillBytes = 48e6;
 
+// Elements of one matrix, at most.
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
 constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
 
 // One launch without a sort: few ids, and few enough CTAs that each of them
@@ -1208,6 +1211,9 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
   if (need > 0 && reinterpret_cast<uintptr_t>(workspace) % 16)
     return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
   if (n_rows == 0 || dim == 0 || (accumulate && n_ids == 0)) return LAMB_OK;
+  // Beyond any memory; below it every count of CTAs and rows fits its type.
+  if (n_ids > kMaxElements / dim || n_rows > kMaxElements / dim)
+    return fail(LAMB_ERR_INVALID, "n_ids * dim or n_rows * dim is too large");
   const GradPlan p = grad_plan(n_ids, n_rows, dim);
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1307,7 +1313,6 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
     a.slabs = int32_t((dim + slab - 1) / slab);
     a.units = p.n_blocks * a.slabs;
     const int64_t ctas = (a.units + kSumWarps - 1) / kSumWarps + a.fill_ctas;
-    if (ctas > kMaxCount) return fail(LAMB_ERR_INVALID, "n_ids * dim is too large");
     const SumKernel kernel = sum_kernels[grad_out_dtype][wide ? 0 : 1][aligned ? 1 : 0];
     ce = launch(kernel, dim3(unsigned(ctas)), kSumWarps * kWarp, kSumWarps * sizeof(WarpSmem), s,
                 true, 1, a);
