@@ -156,7 +156,8 @@ LAMB_API int train_clip_set_poison(train_clip_handle* h, int32_t poison);
  *             1 / S), 0 if a grad is inf or NaN
  *   stats[2]  1 if a grad is inf or NaN, else 0
  * Squares are summed in fp32 a few at a time and in fp64 beyond; G and the
- * factor are formed in fp64 and rounded once.  loss_scale S is finite, > 0.
+ * factor are formed in fp64 and rounded once.  loss_scale S is finite, > 0, and
+ * 1 / S is finite in fp32.
  */
 LAMB_API int train_clip_norm(train_clip_handle* h, float loss_scale, float* stats);
 

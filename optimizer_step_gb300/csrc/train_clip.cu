@@ -437,6 +437,9 @@ namespace {
 int check_scale(float loss_scale, float max_norm) {
   if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale))
     return fail(LAMB_ERR_INVALID, "loss_scale must be finite and > 0");
+  // The factor 1 / S would be inf, and zeros times it NaN.
+  if (!std::isfinite(float(1.0 / double(loss_scale))))
+    return fail(LAMB_ERR_INVALID, "loss_scale is so small that 1 / loss_scale is not finite");
   if (std::isnan(max_norm)) return fail(LAMB_ERR_INVALID, "max_norm is NaN");
   return LAMB_OK;
 }
