@@ -43,9 +43,18 @@ struct __align__(32) Item {
   int64_t unused;
 };
 
+// What clipping multiplies by, first by one and then by the other.  A factor below
+// 2^-100, of grads that have exploded but are finite, is lifted by a power of two
+// that `after` takes off the products, or it would be a number of few bits (below
+// 2^-126) or zero.  Lifted it is at least 2^-126 wherever a product can be, and
+// below 1, so no product overflows.
+struct Factor {
+  float lifted, after;
+};
+
 // What the kernels of one call leave for one another.
 struct Scalars {
-  float factor;     // c / S, 0 when a grad is not finite
+  Factor factor;    // c / S
   uint32_t bad;     // a grad is inf or NaN
   uint32_t ticket;  // CTAs of the norm kernel that have finished
 };
@@ -222,7 +231,12 @@ __device__ __forceinline__ void publish(Scalars* sc, const Request& r, double su
   }
   const double norm = root * r.inv_scale;
   const double factor = r.max_norm > 0.0 && norm > r.max_norm ? r.max_norm * inverse : r.inv_scale;
-  sc->factor = bad ? 0.0f : float(factor);
+  // By its exponent alone; the factor is a normal number.
+  const int64_t word = __double_as_longlong(factor);
+  const int exponent = int(word >> 52) - 1023;
+  const int lift = exponent >= -100 ? 0 : exponent >= -226 ? 100 : 149;
+  sc->factor.lifted = float(__longlong_as_double(word + (int64_t(lift) << 52)));
+  sc->factor.after = lift == 0 ? 1.0f : lift == 100 ? 0x1p-100f : 0x1p-149f;
   sc->bad = bad;
   r.stats[0] = bad ? __int_as_float(0x7f800000) : float(norm);
   r.stats[1] = bad ? 0.0f : float(factor);
@@ -302,16 +316,16 @@ __device__ __forceinline__ void store_value(const Item& it, int i, float x) {
   static_cast<typename TypeOf<OUT>::T*>(it.dst)[i] = from_float<OUT>(x);
 }
 
-// factor * src into dst: 16 bytes of src a thread and load, coalesced on both
+// src times the factor into dst: 16 bytes of src a thread and load, coalesced on both
 // sides, or element by element where src and dst are aligned differently.
 template <int IN, int OUT>
-__device__ __forceinline__ void item_scale(const Item& it, int tid, int threads, float factor) {
+__device__ __forceinline__ void item_scale(const Item& it, int tid, int threads, Factor f) {
   using TO = typename TypeOf<OUT>::T;
   constexpr int kPer = 16 / size_of(IN);
   if (!it.aligned) {
 #pragma unroll 8
     for (int i = tid; i < it.count; i += threads)
-      store_value<OUT>(it, i, factor * load_value<IN>(it, i));
+      store_value<OUT>(it, i, f.lifted * load_value<IN>(it, i) * f.after);
     return;
   }
   const int head = it.head;
@@ -328,7 +342,7 @@ __device__ __forceinline__ void item_scale(const Item& it, int tid, int threads,
   const int rest = it.count - vecs * kPer;
   if (tid < rest) {
     const int i = tid < head ? tid : vecs * kPer + tid;
-    store_value<OUT>(it, i, factor * load_value<IN>(it, i));
+    store_value<OUT>(it, i, f.lifted * load_value<IN>(it, i) * f.after);
   }
 #pragma unroll
   for (int u = 0; u < kLoads; ++u) {
@@ -339,11 +353,11 @@ __device__ __forceinline__ void item_scale(const Item& it, int tid, int threads,
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if constexpr (IN == TRAIN_FP32) {
-        x[i] = factor * __uint_as_float(w[i]);
+        x[i] = f.lifted * __uint_as_float(w[i]) * f.after;
       } else {
         const float2 d = decode2<IN>(w[i]);
-        x[2 * i] = factor * d.x;
-        x[2 * i + 1] = factor * d.y;
+        x[2 * i] = f.lifted * d.x * f.after;
+        x[2 * i + 1] = f.lifted * d.y * f.after;
       }
     }
     if constexpr (OUT == TRAIN_FP32) {
@@ -366,17 +380,17 @@ __device__ __forceinline__ void item_scale(const Item& it, int tid, int threads,
 
 template <int IN>
 __device__ __forceinline__ void item_scale_to(const Item& it, int tid, int threads,
-                                              float factor) {
-  if (it.out == TRAIN_BF16) item_scale<IN, TRAIN_BF16>(it, tid, threads, factor);
-  else if (it.out == TRAIN_FP32) item_scale<IN, TRAIN_FP32>(it, tid, threads, factor);
-  else item_scale<IN, TRAIN_FP16>(it, tid, threads, factor);
+                                              Factor f) {
+  if (it.out == TRAIN_BF16) item_scale<IN, TRAIN_BF16>(it, tid, threads, f);
+  else if (it.out == TRAIN_FP32) item_scale<IN, TRAIN_FP32>(it, tid, threads, f);
+  else item_scale<IN, TRAIN_FP16>(it, tid, threads, f);
 }
 
-__device__ __forceinline__ void any_scale(const Item& it, int tid, int threads, float factor) {
-  if (it.src == it.dst && factor == 1.0f) return;
-  if (it.in == TRAIN_BF16) item_scale_to<TRAIN_BF16>(it, tid, threads, factor);
-  else if (it.in == TRAIN_FP32) item_scale_to<TRAIN_FP32>(it, tid, threads, factor);
-  else item_scale_to<TRAIN_FP16>(it, tid, threads, factor);
+__device__ __forceinline__ void any_scale(const Item& it, int tid, int threads, Factor f) {
+  if (it.src == it.dst && f.lifted == 1.0f) return;
+  if (it.in == TRAIN_BF16) item_scale_to<TRAIN_BF16>(it, tid, threads, f);
+  else if (it.in == TRAIN_FP32) item_scale_to<TRAIN_FP32>(it, tid, threads, f);
+  else item_scale_to<TRAIN_FP16>(it, tid, threads, f);
 }
 
 // One item a CTA, so that the CTAs go through memory in the order they are
@@ -388,17 +402,17 @@ __global__ void __launch_bounds__(kThreads) scale_kernel(Tables T) {
   const Item it = T.items[T.n_items - 1 - blockIdx.x];
   pdl_trigger();
   pdl_wait();
-  float factor = T.sc->factor;
+  Factor f = T.sc->factor;
   if (T.sc->bad) {
     if (!T.poison) return;
-    factor = __int_as_float(0x7fffffff);  // NaN times anything
+    f.lifted = __int_as_float(0x7fffffff);  // NaN times anything
   }
   const bool pack = it.in == kPack;
   const Item* packed = static_cast<const Item*>(it.src);
   const int count = pack ? it.count : 1, tid = pack ? threadIdx.x & 31 : threadIdx.x;
 #pragma unroll 1
   for (int i = pack ? threadIdx.x >> 5 : 0; i < count; i += kWarps)
-    any_scale(pack ? packed[i] : it, tid, pack ? kWarp : kThreads, factor);
+    any_scale(pack ? packed[i] : it, tid, pack ? kWarp : kThreads, f);
 }
 
 int cuda_fail(cudaError_t e, const char* what) {
