@@ -124,7 +124,7 @@ typedef struct train_clip_handle train_clip_handle;
  *   outs         NULL: clipping works in place.  Else outs[i] receives tensor
  *                i's clipped grads in out_dtypes[i]; each is grads[i] itself
  *                (then of the same type) or overlaps none of the grads
- * The tensors do not overlap one another.
+ * Tensors that overlap, one that is listed twice among them, are refused.
  * The arrays are host arrays, read before the call returns.  The call
  * waits for the upload of its work table.
  */

@@ -513,6 +513,26 @@ struct Span {
   int32_t in, out;
 };
 
+// The memory of one tensor.
+struct Range {
+  uintptr_t begin, end;
+  int32_t index;
+  bool out;
+};
+
+// Every tensor but an output that is its own grad has memory of its own.
+int check_disjoint(std::vector<Range>& ranges) {
+  std::sort(ranges.begin(), ranges.end(),
+            [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  const auto name = [](const Range& r) {
+    return (r.out ? "outs[" : "grads[") + std::to_string(r.index) + "]";
+  };
+  for (size_t i = 1; i < ranges.size(); ++i)
+    if (ranges[i].begin < ranges[i - 1].end)
+      return fail(LAMB_ERR_INVALID, name(ranges[i - 1]) + " and " + name(ranges[i]) + " overlap");
+  return LAMB_OK;
+}
+
 // Cuts a span into items whose first 16-byte loads are aligned: only its first
 // item has elements in front of them.  Small ones go to `small`.
 void add_items(std::vector<Item>* items, std::vector<Item>* small, const Span& span,
@@ -540,7 +560,9 @@ void add_items(std::vector<Item>* items, std::vector<Item>* small, const Span& s
 int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32_t* dtypes,
            void* const* grads, void* const* outs, const int32_t* out_dtypes, void* stream) {
   std::vector<Span> spans;
+  std::vector<Range> ranges;
   spans.reserve(size_t(n));
+  ranges.reserve(outs ? 2 * size_t(n) : size_t(n));
   int64_t total = 0;  // bytes, or kSmallTotal if there are more
   for (int32_t i = 0; i < n; ++i) {
     const auto at = [i](const char* what) { return what + ("[" + std::to_string(i) + "]"); };
@@ -562,8 +584,16 @@ int create(train_clip_handle** out, int32_t n, const int64_t* sizes, const int32
     if (sizes[i] > INT64_MAX / 8) return fail(LAMB_ERR_INVALID, at("sizes") + " is too large");
     spans.push_back(Span{static_cast<const char*>(grads[i]), static_cast<char*>(dst), sizes[i],
                          dtypes[i], to});
+    const auto range = [&](const void* p, int size, bool out) {
+      const uintptr_t begin = reinterpret_cast<uintptr_t>(p);
+      ranges.push_back(Range{begin, begin + uintptr_t(sizes[i]) * unsigned(size), i, out});
+    };
+    range(grads[i], si, false);
+    if (dst != grads[i]) range(dst, so, true);
     total = sizes[i] * si < kSmallTotal - total ? total + sizes[i] * si : kSmallTotal;
   }
+  const int rc = check_disjoint(ranges);
+  if (rc != LAMB_OK) return rc;
   // In the order of memory, neighbours joined.
   std::stable_sort(spans.begin(), spans.end(),
                    [](const Span& a, const Span& b) { return a.src < b.src; });

@@ -35,7 +35,8 @@ class GradClip:
     ``grads``: contiguous CUDA tensors on one device, bfloat16, float16 and
     float32 in any mix and of any size.  ``out`` (default: the grads
     themselves): tensors of the same sizes that receive the clipped grads,
-    each of any of the three types.  ``stream`` defaults to the current torch
+    each of any of the three types.  No two tensors may overlap, but an output
+    may be its own grad: a grad that is shared is listed once.  ``stream`` defaults to the current torch
     stream at construction; every call runs on it and returns without waiting.
 
     ``poison``: what ``clip`` and ``finish`` leave in the outputs when a grad is
