@@ -59,3 +59,17 @@ def test_factors_below_the_normal_range_of_fp32(value, max_norm, loss_scale, to)
         want = b * (c / loss_scale)
         tol = (19 * 2.0 ** -24 + u) * 1.01 * want.abs() + sub
         assert bool(((x.double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("n", [7, 4096, 100_003, 5_000_000])
+def test_the_norm_within_what_its_additions_allow(dtype, n):
+    """A thread adds 64 squares of 16 bits (32 of fp32) in two chains and then the
+    chains, fp64 from there: 33 roundings of positive sums, halved by the root,
+    and the norm's own.  33 / 2 + 1 times 2^-24 is 1.05e-6."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n)
+    grads = [torch.randn(n, generator=gen, device="cuda").to(dtype).abs_()]
+    want = float(grads[0].double().square().sum()) ** 0.5
+    with og.GradClip(grads) as clipper:
+        assert abs(float(clipper.norm()[0]) - want) <= 1.05e-6 * want
