@@ -18,6 +18,12 @@ _TYPES = {torch.bfloat16: _lib.TRAIN_BF16, torch.float16: _lib.TRAIN_FP16,
           torch.float32: _lib.TRAIN_FP32}
 _ID_TYPES = {torch.int32: _lib.TRAIN_INT32, torch.int64: _lib.TRAIN_INT64}
 
+# The current device and stream, from torch's quick private calls (0.1 us each, where
+# the public ones take 0.2 and 2.9) as long as it has them.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _code(name, t, codes, index):
     """Code of a tensor's type, after the checks that every argument gets."""
@@ -78,11 +84,11 @@ def _refuse(name, t, ids):
 
 def _enqueue(index, call, *args):
     """``call(*args, stream)`` with device ``index`` current, on its current stream."""
-    if index == torch._C._cuda_getDevice():
-        rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _current_device():
+        rc = call(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = call(*args, torch._C._cuda_getCurrentRawStream(index))
+            rc = call(*args, _raw_stream(index))
     if rc:
         check(rc)
 
