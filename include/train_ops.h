@@ -164,7 +164,13 @@ LAMB_API int train_clip_norm(train_clip_handle* h, float loss_scale, float* stat
 /* The norm, then out = round(c / S * g) for every tensor; max_norm <= 0 (or
  * a norm of at most max_norm) leaves c = 1.  If a grad is inf or NaN nothing
  * is written but stats, or NaN to every output (train_clip_set_poison).  In
- * place with c / S = 1 nothing needs writing. */
+ * place with c / S = 1 nothing needs writing.
+ *
+ * The outputs are divided by S, so a step that reads them takes loss_scale 1.
+ * While lamb_step's dynamic loss scaler is on it divides by its own scale
+ * whatever it is told: then clip with loss_scale 1 and max_norm times that scale
+ * (lamb_result's next_loss_scale before the backward pass), which leaves the
+ * scale in the outputs for the step to take off; stats[0] carries it too. */
 LAMB_API int train_clip_grads(train_clip_handle* h, float max_norm, float loss_scale,
                               float* stats);
 

@@ -101,7 +101,13 @@ class GradClip:
     def clip(self, max_norm: float, loss_scale: float = 1.0) -> torch.Tensor:
         """Divides the grads by ``loss_scale`` and clips their global norm to
         ``max_norm`` (<= 0: no clipping), rounding once.  If a grad is inf or
-        NaN the outputs stay as they are, or all become NaN (``poison``)."""
+        NaN the outputs stay as they are, or all become NaN (``poison``).
+
+        A step that reads the outputs takes ``loss_scale=1``.  While ``Lamb``'s
+        dynamic loss scaler is on, its steps divide by their own scale S in any
+        case: then call ``clip(max_norm * S)`` with ``S = opt.next_loss_scale``
+        as of the backward pass, which leaves S in the outputs (and in the norm)
+        for the step to take off."""
         check(self._lib.train_clip_grads(self._handle(), max_norm, loss_scale, self._stats_ptr))
         return self.stats
 
