@@ -15,9 +15,10 @@ constexpr int kWarps = kThreads / 32;
 // Bytes of grads in one piece of work: eight 16-byte loads a thread.
 constexpr int kLoads = 8;
 constexpr int64_t kItemBytes = kThreads * kLoads * 16;
-// Half as many below 16 MB, where whole ones leave SMs idle: 10.4 us instead of 12.8
-// to clip 6 MB at the time, while 43 MB take 22 us with whole ones and 26.5 with halves.
-constexpr int64_t kHalfBytes = 16 << 20;
+// Half as many as long as the norm's CTAs (3 an SM) take all of those in one round:
+// fp32 clipped into bf16, halves against whole ones, 6 MB 9.7 us and 10.4, 6.5 MB 9.5
+// and 9.7, 7.6 MB 12.2 and 10.1, 13 MB 16.3 and 11.3, 43 MB 26.5 and 22.8.
+constexpr int64_t kHalfBytes = 7 << 20;
 // What fits into L2.
 constexpr int64_t kSmallTotal = 128 << 20;
 constexpr int64_t kEarlyBytes = 5 << 20;
