@@ -22,11 +22,13 @@ constexpr int64_t kHalfBytes = 7 << 20;
 // What fits into L2.
 constexpr int64_t kSmallTotal = 128 << 20;
 constexpr int64_t kEarlyBytes = 5 << 20;
-// Items of at most so many bytes are packed, one a warp of a CTA: 1204 tensors of up
-// to 4 KB are clipped in 12 us, four a warp in 15.
+// Items of at most so many bytes are packed, one a warp of a CTA: 1204 tensors of 4 KB
+// are clipped in 8.8 us, with a CTA each in 14.4; 4000 of 2 KB in 12.4 and 24.6.
 constexpr int64_t kPackedBytes = 4096;
-// CTAs of the norm kernel an SM; with 3 the norm of 1.2e9 fp16 grads takes 13% longer
-// than with 5, that of 10 MB 7.4 us instead of 9.6 (fewer sums to wait for).
+// CTAs of the norm kernel an SM, from 128 MB on and below.  With 3 the norm of 2.4 GB
+// takes 360 us, with 5 330; 600 MB 96 and 90.  Below, 5 are as good or a little better
+// (20 MB 8.8 and 8.8 us, 43 MB 12.5 and 12.4, 130 MB 25.6 and 24.6; clipped, 20 MB 16.5
+// and 13.7): 3 were chosen when the sums of the CTAs cost more.
 constexpr int kNormCtas = 5, kNormCtasSmall = 3;
 
 // One piece of work: count elements from src, written to dst; or, where `in`
@@ -68,8 +70,9 @@ struct Tables {
   int32_t poison;  // outputs become NaN when a grad is inf or NaN
 };
 
-// 16 bytes, in order with the other loads of its kind: a thread's loads are all
-// on their way before the first value is used.
+// 16 bytes, in order with the other loads of its kind: as many of a thread's are on
+// their way together as it has registers for, all eight in the clipping (62
+// registers), fewer in the norm (32 registers, so that more warps run).
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 q;
   asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -80,8 +83,7 @@ __device__ __forceinline__ uint4 load16(const void* p) {
 
 // Fixed-shape block sum; the result is valid in the first warp.  An fp64 instruction
 // of a warp takes 16 cycles of its SM, so one warp adds the threads' values (13 such
-// instructions, where shuffles in every warp are 64): 8.5 us instead of 10.1 to clip
-// 6 MB, 8.7 instead of 9.4 for the norm of 43 MB.
+// instructions, where shuffles in every warp are 64).
 __device__ __forceinline__ double block_sum(double x, double* red) {
   red[threadIdx.x] = x;
   __syncthreads();
@@ -116,7 +118,8 @@ __device__ __forceinline__ void add_square(Squares& s, float x) {
 // The squares of a thread's vectors (v, v + threads, ... below end) in fp64,
 // and whether one is inf or NaN.  The rare path: not inlined, and the values
 // are read again, so that the fast path carries neither fp64 code nor words
-// kept for it.
+// kept for it.  Where every vector comes here, it is slow: the norm of 2.4 GB takes
+// 4.6 ms if they are bf16 of 1e-16, 2.4 ms if they are fp32, instead of 0.33.
 template <int DT>
 __device__ __noinline__ Squares squares_fp64(const char* base, int v, int end, int threads) {
   Squares s{0.0, 0u};
@@ -247,8 +250,9 @@ __device__ __forceinline__ void publish(Scalars* sc, const Request& r, double su
 // Sum of squares: each CTA walks every gridDim.x-th item, all of them through
 // memory side by side; the last one to finish adds the CTAs' sums in order and
 // publishes.  It is bound by reading: 1.2e9 fp16 grads take 331 us on GB300, 7.3
-// TB/s.  With a few MB it is a chain of latencies: for 6 MB, 5.7 us a call, the last
-// CTA has its data after 2.7 us; the CTAs' sums, tickets and their sum are the rest.
+// TB/s.  With a few MB it is a chain of latencies: 6 MB take 6.3 us, 43 MB (three
+// items for most CTAs, two for the others) 12.5; behind the last data come the CTAs'
+// sums, their tickets and the sum of those.
 __global__ void __launch_bounds__(kThreads) norm_kernel(const __grid_constant__ Tables T,
                                                         const __grid_constant__ Request r) {
   __shared__ double red[kThreads];
@@ -487,13 +491,16 @@ int launch(train_clip_handle* h, const char* what, void (*kernel)(A...), int64_t
 }
 
 // Which kernel starts beside which, measured on GB300:
-// - The clipping's CTAs may start at once, beside the norm (clip): 10.4 us instead of
-//   11.8 at 6 MB at the time, 26.6 instead of 29 at 43 MB.  Below 5 MB they rather
-//   wait until the squares are added: 9.6 us instead of 12.0 at 0.7 MB.
-// - So does whatever follows the norm alone: 5.8 us instead of 9.7 at 4 MB.
-// - The norm itself starts before the kernel in front has ended, unless it walks over
-//   many items, which CTAs that are spread over the SMs unevenly feel: 3% at 0.6 to
-//   7 GB, and as much where the norm of the next step starts beside the clipping.
+// - The clipping's CTAs may start at once, beside the norm: 6 MB 9.7 us instead of
+//   10.0, 6.5 MB 9.5 instead of 10.3; 8 to 17 MB cost up to 8% so, and 20 MB and more
+//   are the same either way.  Below 5 MB they wait until the squares are added: 9.3 us instead
+//   of 9.9 at 4.5 MB, 6.4 instead of 6.9 at 0.7.
+// - So does whatever follows the norm alone.
+// - The norm itself starts before the kernel in front has ended (4.6 us instead of 6.2
+//   at 0.7 MB, 12.5 instead of 14.4 at 43 MB), unless it walks over many items in front
+//   of a clipping: CTAs that are spread over the SMs unevenly cost 4% at 600 MB (234 us
+//   instead of 224), though 20 and 43 MB would gain (14.3 instead of 16.5, 20.7 instead
+//   of 22.8).  Alone from 128 MB on it would gain 3% (600 MB: 87 us instead of 90).
 int launch_norm(train_clip_handle* h, bool alone, Request r) {
   r.early = !alone && h->bytes >= kEarlyBytes;
   const bool dependent = h->T.n_items <= h->grid || (alone && h->bytes < kSmallTotal);

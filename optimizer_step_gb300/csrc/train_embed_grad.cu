@@ -31,7 +31,8 @@ namespace {
 // move; 8192 tokens of width 4096 60 us, 5.5 TB/s (the sort takes 9.5 of them,
 // the sums 22 if nothing else is written); 50,021 tokens of which a slice of
 // 15,013 rows holds half, fp16 of width 1023 added to fp32, 51 us, 4.0 TB/s (the
-// sort takes 15).
+// sort takes 15).  Rows of 32 bits hold half as many columns a lane: 8192 fp32 tokens of
+// width 4096 take 109 us dense, 6.1 TB/s, 66 added to what is there.
 
 // One sorted position: the row that its token names (n_rows for a token that
 // adds nothing) and the position.
@@ -178,9 +179,9 @@ __device__ __forceinline__ void mark(uint32_t* named, uint32_t r) {
 // its rows up in that list.
 //
 // It zeroes what fits into the time of the sort (kFillBytes); the later kernels
-// zero the rest among their own work.  All of it here, before the sums, took 85 us
-// for 8192 tokens of width 4096 when the rest among the sums took 76: the sums
-// alone leave a third of the memory rate unused.
+// zero the rest among their own work.  All of it here, before the sums, takes 71.5 us
+// for 8192 tokens of width 4096 instead of 59.6, 291 for 32768 of width 12288 instead
+// of 262: the sums alone leave a third of the memory rate unused.
 constexpr int kFillThreads = 512;
 constexpr int kFillRows = 4096;  // at most, a CTA
 
@@ -270,8 +271,9 @@ __device__ __forceinline__ void fill_rest(const GradArgs& a, int64_t index) {
 // are asynchronous (16 bytes a lane), so they hold no registers, and the rows
 // of the grad that accumulation needs come through the same ring behind the
 // last row of their run: nothing waits for them when the run is finished.
-// Measured on GB300 with 6 and 8 stages: 8192 tokens 60 and 61 us, 32768 wide ones
-// 259 and 254, the unaligned slice 51 and 53.  (Eight rows at a time in registers
+// Measured on GB300 with 6 and 8 stages: 8192 tokens 59.6 and 59.5 us (added to what
+// is there, 42.0 and 43.0), 32768 wide ones 262 and 256, 50,021 of width 1023 in rows
+// that are not aligned 62.9 and 67.1.  (Eight rows at a time in registers
 // took 276 us for that slice's sums alone, where the ring takes 31.)
 constexpr int kStages = 6;
 constexpr int kStageBytes = 1024 + 32;  // a piece and its ends' alignment
@@ -1052,8 +1054,8 @@ bool rows_aligned16(const void* p, int32_t dtype, int64_t stride) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * size_of(dtype) % 16 == 0;
 }
 
-// Zeros written while the tokens are being sorted: 24, 48 and 80 MB measured 78.5,
-// 75.6 and 75.3 us for 8192 tokens of width 4096 at the time.
+// Zeros written while the tokens are being sorted: with 24, 48 and 80 MB 8192 tokens
+// of width 4096 take 61.7, 59.6 and 60.6 us.
 constexpr double kFillBytes = 48e6;
 
 // Elements of one matrix, at most.
@@ -1063,10 +1065,14 @@ constexpr int64_t kClusterCapacity = kSortCtas * kSortThreads * 8;
 
 // One launch without a sort: few ids, and few enough CTAs that each of them
 // reading all ids does not matter.  On GB300, summed onto a bf16 grad, frequent
-// tokens as in text: 1024 ids of width 256 take 5 us this way and 20 us with a
-// sort, 256 of width 4096 (4096 CTAs) 11 and 16, 512 of them 28 and 18.  Where rows
-// are not aligned a frequent token is slow this way (1024 times the same one, width
-// 1023: 65 us, with a sort 21), so only a quarter of the ids are taken.
+// tokens as in text: 1024 ids of width 256 take 5.4 us this way and 18.5 with a
+// sort, 256 of width 4096 (4096 CTAs) 11.1 and 18.1, 512 of them 23.0 and 18.5.
+// A frequent token is slow this way where rows are not aligned (1024 times the same
+// one, width 1023: 64 us, with a sort 18.5), so only a quarter of the ids are taken
+// where the width is no multiple of 8.  The rule sees the width alone, so that the
+// workspace depends on sizes only: of rows of 1024 that their address or stride puts
+// off the alignment all 2048 are taken, in 18.0 us instead of 20.5 if they are 1024 as
+// in text, in 64 instead of 20.4 if they are the same token throughout.
 constexpr int64_t kDirectCtas = 4096;
 bool use_direct(int64_t n, int64_t dim) {
   return n <= (dim % 8 == 0 ? kDirectIds : kDirectIds / 4) &&
@@ -1090,13 +1096,13 @@ GradPlan grad_plan(int64_t n, int64_t n_rows, int64_t dim) {
   GradPlan p{};
   if (use_direct(n, dim)) return p;
   // Blocks of 64 positions where they make work for 4096 warps, else of 32 or 16:
-  // blocks of 128 were 5% slower for 32768 wide tokens, and 32 instead of 16 took 8%
-  // more for 8192 of width 4096.
+  // 32768 wide tokens take 262 us with 64 and 268 with 128, 8192 of width 4096 59.6
+  // with 16 and 66.5 with 32.
   const int64_t slabs = (dim + 511) / 512;
   p.block = kMaxBlock;
   while (p.block > 16 && n / p.block * slabs < 4096) p.block /= 2;
-  // Where even 16 make few: 1024 tokens of width 4096 added to bf16 take 17.5 us with
-  // blocks of 8, 21.5 with 16; 8192 of them (4096 warps with 16) 64 and 60.
+  // Where even 16 make few: 1024 tokens of width 4096 added to bf16 take 20.4 us with
+  // blocks of 8, 22.7 with 16; 8192 of them (4096 warps with 16) 66.9 and 59.6.
   if (n / 16 * slabs < 2048) p.block = 8;
   p.n_blocks = (n + p.block - 1) / p.block;
   p.slot_dim = (dim + 7) / 8 * 8;
