@@ -1,21 +1,28 @@
 /*
  * train_ops.h -- C ABI of the operators in front of the optimizer step, on
  * one GB300 (sm_103a): the embedding lookup with scaling, its gradient by
- * sorted tokens, and the global gradient norm over many tensors with
- * clipping.  They are part of the library of lamb.h and share its return
- * codes and lamb_last_error().
+ * sorted tokens, layer norm forwards and backwards, the loss against a
+ * teacher's top logits and true labels with its gradient, and the global
+ * gradient norm over many tensors with clipping.  They are part of the library
+ * of lamb.h and share its return codes and lamb_last_error().
  *
  *   train_embed        out[i, :] = round(scale * table[ids[i] - first_row, :])
  *   train_embed_grad   grad[v, :] = round(old + scale * sum over the i with
  *                      ids[i] = first_row + v of grad_out[i, :])
+ *   train_layer_norm   y = round((x - mean) * rstd * weight + bias), a row at a time
+ *   train_layer_norm_grad   its gradients for x, the weight and the bias
+ *   train_distill      loss against a teacher's top logits and true labels, and
+ *                      the gradient for the logits, in one pass over them
  *   train_clip_*       G = ||g / S|| over all tensors;
  *                      c = max_norm / G if max_norm > 0 and G > max_norm, else 1;
  *                      out = round(c / S * g); inf/NaN anywhere: nothing written,
  *                      or NaN everywhere (train_clip_set_poison)
  *
  * With them a language model's training step runs around lamb_step: the
- * lookup starts the forward pass, the gradient by sorted tokens ends the
- * backward pass in the grad buffer that the step reads, and the clip takes
+ * lookup starts the forward pass, layer norm stands in front of its matrix
+ * products, the loss ends it and starts the backward pass at the logits, the
+ * gradient by sorted tokens ends that
+ * in the grad buffer that the step reads, and the clip takes
  * grads summed in fp32 (or in 16 bits) to the 16-bit grads of the step.  A clip
  * into other tensors that a step reads needs train_clip_set_poison, or the step
  * does not learn of an overflow.
@@ -107,6 +114,114 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
                               int32_t accumulate, void* grad, int32_t grad_dtype,
                               int64_t n_rows, int64_t dim, int64_t grad_stride, void* workspace,
                               int64_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm of each row of x:
+ *
+ *   mean = sum(x) / dim     var = sum((x - mean)^2) / dim
+ *   rstd = 1 / sqrt(var + eps)
+ *   y    = round((x - mean) * rstd * weight + bias)
+ *
+ *   x            n_rows x dim, rows x_stride elements apart
+ *   weight, bias dim consecutive elements of type param_dtype; NULL: 1 and 0
+ *   eps          finite, >= 0.  With 0, a row of equal elements has no rstd and
+ *                becomes NaN
+ *   y            n_rows x dim, rows y_stride elements apart.  May be x itself
+ *                (the same address, type and stride)
+ *   stats        NULL, or 2 * n_rows floats that receive the rows' means and
+ *                behind them their rstd, for train_layer_norm_grad
+ *
+ * The variance is summed from the differences to the mean, so rows far from
+ * zero keep their digits; rows whose squares leave fp32's range are scaled by a
+ * power of two first (magnitudes up to 2^126).  An inf or NaN makes its row NaN.
+ * Strides are at least dim; dim is at least 1, n_rows may be 0, both are at most
+ * 2^31 - 1.
+ */
+LAMB_API int train_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n_rows,
+                              int64_t dim, const void* weight, const void* bias,
+                              int32_t param_dtype, float eps, void* y, int32_t y_dtype,
+                              int64_t y_stride, float* stats, void* stream);
+
+/* Bytes of workspace that train_layer_norm_grad needs for these sizes. */
+LAMB_API int train_layer_norm_grad_workspace(int64_t n_rows, int64_t dim, int64_t* bytes);
+
+/*
+ * Gradients of layer norm.  With xhat = (x - mean) * rstd and g = grad_out * weight:
+ *
+ *   x_grad       round(rstd * (g - mean of g - xhat * mean of g * xhat)), the
+ *                means over a row
+ *   weight_grad  round(old + sum over the rows of grad_out * xhat)
+ *   bias_grad    round(old + sum over the rows of grad_out)
+ *
+ *   grad_out, x  n_rows x dim, rows grad_out_stride and x_stride elements apart
+ *   weight       as in the forward pass, of type weight_dtype; NULL: 1
+ *   stats        the 2 * n_rows floats of the forward pass
+ *   x_grad       NULL, or n_rows x dim of x's type, rows x_grad_stride elements
+ *                apart.  May be grad_out or x itself (the same address, type
+ *                and stride)
+ *   weight_grad, bias_grad   each NULL, or dim consecutive elements of type
+ *                param_grad_dtype
+ *   accumulate   0: what weight_grad and bias_grad held is not read (without
+ *                rows they become zero); 1: `old` above, added to
+ *   workspace    device memory, 16-byte aligned, of at least
+ *                train_layer_norm_grad_workspace bytes; only needed for
+ *                weight_grad or bias_grad.  Its contents before the call do not
+ *                matter, and it is free again when the stream has passed the call
+ *
+ * The sums over the rows are fp32, in an order that only the sizes, types and
+ * alignment fix; no atomic sum is used.  n_rows * dim is at most 2^40.
+ */
+LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
+                                   int64_t grad_out_stride, const void* x, int32_t x_dtype,
+                                   int64_t x_stride, int64_t n_rows, int64_t dim,
+                                   const void* weight, int32_t weight_dtype, const float* stats,
+                                   void* x_grad, int64_t x_grad_stride, void* weight_grad,
+                                   void* bias_grad, int32_t param_grad_dtype, int32_t accumulate,
+                                   void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * The loss of each row of logits z against a teacher's top logits and a true
+ * label, and its gradient.  With T the temperature, p = softmax(t / T) over the
+ * row's entries (j_k, t_k) of the teacher, q = softmax(z / T) and s = softmax(z)
+ * over the vocabulary, and y the label:
+ *
+ *   loss    = soft_weight * T^2 * sum_k p_k (log p_k - log q[j_k])
+ *             - hard_weight * log s[y]
+ *   grad[j] = round(scale * row_grad * (
+ *               soft_weight * T * (q[j] - sum of the p_k with j_k = j)
+ *               + hard_weight * (s[j] - 1 if j = y)))
+ *
+ *   logits       n_rows x vocab, rows logits_stride elements apart
+ *   top_ids, top_logits   n_rows x top_k, rows top_ids_stride and
+ *                top_logits_stride elements apart; top_k is at most 1024.  An
+ *                entry whose id lies outside [0, vocab) or whose logit is -inf
+ *                is left out, and a row without entries has no first term.  A
+ *                token may be named twice.  Not read when top_k or soft_weight
+ *                is 0
+ *   labels       NULL (then hard_weight is 0), or n_rows consecutive ids.  A row
+ *                whose label is ignore_id or lies outside [0, vocab) is left
+ *                out: its loss and gradient are 0 whatever its logits hold
+ *   temperature  finite and > 0, as its reciprocal; the weights are finite
+ *   loss         NULL, or n_rows floats
+ *   row_grad     NULL (1 for every row), or n_rows floats: the gradient of what
+ *                is minimised for each row's loss.  A row where it is 0 gets a
+ *                gradient of 0 whatever its logits hold
+ *   grad         NULL, or n_rows x vocab, rows grad_stride elements apart.  May
+ *                be the logits themselves (the same address, type and stride)
+ *
+ * Sums are fp32 or wider.  A logit of -inf (a masked token) has q = s = 0; if
+ * the teacher or the label names it the loss is +inf.  A row with a NaN or +inf,
+ * or with nothing but -inf, has a NaN loss and gradient.  vocab is at least 1,
+ * n_rows may be 0, both are at most 2^31 - 1.
+ */
+LAMB_API int train_distill(const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                           int64_t n_rows, int64_t vocab, const void* top_ids,
+                           int32_t top_ids_dtype, int64_t top_ids_stride, const void* top_logits,
+                           int32_t top_logits_dtype, int64_t top_logits_stride, int64_t top_k,
+                           const void* labels, int32_t labels_dtype, int64_t ignore_id,
+                           float temperature, float soft_weight, float hard_weight, float* loss,
+                           const float* row_grad, float scale, void* grad, int32_t grad_dtype,
+                           int64_t grad_stride, void* stream);
 
 /*
  * Global gradient norm and clipping over a fixed list of tensors.

@@ -32,7 +32,8 @@ EXPORTS = ("lamb_create", "lamb_step", "lamb_destroy", "lamb_last_error", "lamb_
 
 # Every symbol include/train_ops.h declares.
 TRAIN_EXPORTS = ("train_embed", "train_embed_grad_workspace", "train_embed_grad",
-                 "train_clip_create", "train_clip_set_poison", "train_clip_norm",
+                 "train_layer_norm", "train_layer_norm_grad_workspace", "train_layer_norm_grad",
+                 "train_distill", "train_clip_create", "train_clip_set_poison", "train_clip_norm",
                  "train_clip_grads", "train_clip_partial", "train_clip_finish",
                  "train_clip_destroy")
 TRAIN_BF16 = 0
@@ -158,6 +159,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.train_embed_grad.restype = ctypes.c_int
         lib.train_embed_grad.argtypes = [P, i32, i64, P, i32, i64, i64, i64, f32, i32, P, i32,
                                          i64, i64, i64, P, i64, P]
+        lib.train_layer_norm.restype = ctypes.c_int
+        lib.train_layer_norm.argtypes = [P, i32, i64, i64, i64, P, P, i32, f32, P, i32, i64, P, P]
+        lib.train_layer_norm_grad_workspace.restype = ctypes.c_int
+        lib.train_layer_norm_grad_workspace.argtypes = [i64, i64, ctypes.POINTER(i64)]
+        lib.train_layer_norm_grad.restype = ctypes.c_int
+        lib.train_layer_norm_grad.argtypes = [P, i32, i64, P, i32, i64, i64, i64, P, i32, P, P,
+                                              i64, P, P, i32, i32, P, i64, P]
+        lib.train_distill.restype = ctypes.c_int
+        lib.train_distill.argtypes = [P, i32, i64, i64, i64, P, i32, i64, P, i32, i64, i64, P, i32,
+                                      i64, f32, f32, f32, P, P, f32, P, i32, i64, P]
         lib.train_clip_create.restype = ctypes.c_int
         lib.train_clip_create.argtypes = [ctypes.POINTER(P), i32, P, P, P, P, P, P]
         lib.train_clip_set_poison.restype = ctypes.c_int

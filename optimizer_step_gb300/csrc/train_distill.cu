@@ -1,0 +1,223 @@
+// The loss against a teacher's top logits and the true labels, and its gradient
+// (train_ops.h).
+#include "train_norm.h"
+
+using namespace traingb;
+
+namespace {
+
+constexpr int kMaxTop = 1024;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct DistillArgs {
+  const void* logits;
+  const void* top_ids;
+  const void* top_logits;
+  const void* labels;
+  const float* row_grad;
+  float* loss;
+  void* grad;
+  int64_t stride, ids_stride, top_stride, grad_stride, ignore_id;
+  int32_t vocab, top_k;
+  float inv_temperature, soft_weight, hard_weight, temperature, scale;
+  int32_t type, grad_type, ids64, top_type, labels64;
+};
+
+__device__ __forceinline__ int64_t read_id(const void* p, int64_t i, int32_t is64) {
+  return is64 ? static_cast<const int64_t*>(p)[i] : int64_t(static_cast<const int32_t*>(p)[i]);
+}
+
+constexpr int kThreads = 512;
+
+// One CTA a row, which it reads three times (from L1 or L2 after the first).
+__global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
+  // The row's entries: the teacher's tokens and behind them the label.
+  __shared__ int32_t id[kMaxTop + 1];
+  __shared__ float coef[kMaxTop + 1];  // what the entry takes off its gradient
+  __shared__ float zed[kMaxTop + 1];   // the student's logit there
+  __shared__ float part[4][kThreads / kWarp];
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const int tid = threadIdx.x;
+  const bool soft = a.top_k > 0 && a.soft_weight != 0.f;
+  int64_t label = -1;
+  bool live = true;
+  if (a.labels) {
+    label = read_id(a.labels, row, a.labels64);
+    live = label != a.ignore_id && label >= 0 && label < a.vocab;
+  }
+  const bool hard = a.labels && a.hard_weight != 0.f;
+  float up = a.scale;
+  if (a.grad && a.row_grad) up *= a.row_grad[row];
+  by_type(a.type, [&](auto Z) {
+    constexpr int ZT = decltype(Z)::value;
+    using TZ = typename TypeOf<ZT>::T;
+    const TZ* z = static_cast<const TZ*>(a.logits) + row * a.stride;
+    // The teacher's distribution.
+    const int top_k = soft && live ? a.top_k : 0;
+    float best = -INFINITY;
+    for (int k = tid; k < top_k; k += kThreads) {
+      const int64_t i = read_id(a.top_ids, row * a.ids_stride + k, a.ids64);
+      float t = 0.f;
+      by_type(a.top_type, [&](auto T) {
+        constexpr int TT = decltype(T)::value;
+        t = to_float<TT>(static_cast<const typename TypeOf<TT>::T*>(
+            a.top_logits)[row * a.top_stride + k]);
+      });
+      const bool valid = i >= 0 && i < a.vocab && t != -INFINITY;
+      id[k] = valid ? int32_t(i) : -1;
+      coef[k] = t;
+      if (valid) {
+        zed[k] = to_float<ZT>(z[i]);
+        best = t != t ? t : fmaxf(best, t);
+      }
+    }
+    best = cta_max<kThreads>(best, part[0]);
+    float size = 0.f;
+    for (int k = tid; k < top_k; k += kThreads)
+      if (id[k] >= 0) size += exp2f((coef[k] - best) * (a.inv_temperature * kLog2e));
+    size = cta_sum<kThreads>(size, part[1]);
+    const bool any = size != 0.f;  // NaN too
+    // The student's.
+    const bool work = live && (any || hard) && (a.loss || up != 0.f);
+    float top = -INFINITY, soft_sum = 0.f, hard_sum = 0.f;
+    if (work) {
+      for (int j = tid; j < a.vocab; j += kThreads) top = fmaxf(top, to_float<ZT>(z[j]));
+    }
+    top = cta_max<kThreads>(top, part[2]);
+    const float c = a.inv_temperature * kLog2e;
+    if (work) {
+      for (int j = tid; j < a.vocab; j += kThreads) {
+        const float d = to_float<ZT>(z[j]) - top;
+        if (any) soft_sum += exp2f(d * c);
+        if (hard) hard_sum += exp2f(d * kLog2e);
+      }
+    }
+    soft_sum = cta_sum<kThreads>(soft_sum, part[0]);
+    hard_sum = cta_sum<kThreads>(hard_sum, part[3]);
+    // The loss, and what each entry takes off the gradient.
+    float terms = 0.f;
+    const float log_size = logf(size), log_soft = logf(soft_sum);
+    for (int k = tid; k < top_k; k += kThreads) {
+      if (id[k] < 0) {
+        coef[k] = 0.f;
+        continue;
+      }
+      const float t = (coef[k] - best) * a.inv_temperature;
+      const float p = exp2f((coef[k] - best) * c) / size;
+      const float q = (zed[k] - top) * a.inv_temperature - log_soft;
+      terms += zed[k] == -INFINITY ? INFINITY : p * (t - log_size - q);
+      coef[k] = a.soft_weight * a.temperature * p;
+    }
+    const bool hits = work && hard;
+    if (tid == 0) {
+      id[top_k] = hits ? int32_t(label) : -1;
+      coef[top_k] = a.hard_weight;
+      zed[top_k] = hits ? to_float<ZT>(z[label]) : 0.f;
+    }
+    terms = cta_sum<kThreads>(terms, part[1]);
+    if (a.loss && tid == 0) {
+      float loss = 0.f;
+      // Without a distribution (soft_sum is NaN) a masked token's term means nothing.
+      if (soft_sum != soft_sum) terms = soft_sum;
+      if (work && any) loss = a.soft_weight * a.temperature * a.temperature * terms;
+      if (hits) loss += a.hard_weight * (logf(hard_sum) - (zed[top_k] - top));
+      a.loss[row] = loss;
+    }
+    if (!a.grad) return;
+    by_type(a.grad_type, [&](auto G) {
+      constexpr int GT = decltype(G)::value;
+      using TG = typename TypeOf<GT>::T;
+      TG* grad = static_cast<TG*>(a.grad) + row * a.grad_stride;
+      const bool zero = !work || up == 0.f;
+      const float qs = any ? a.soft_weight * a.temperature / soft_sum : 0.f;
+      const float ss = hard ? a.hard_weight / hard_sum : 0.f;
+      const auto smooth = [&](float v) {
+        const float d = v - top;
+        float g = 0.f;
+        if (any) g += qs * exp2f(d * c);
+        if (hard) g += ss * exp2f(d * kLog2e);
+        return g;
+      };
+      for (int j = tid; j < a.vocab; j += kThreads)
+        grad[j] = zero ? TG(0) : from_float<GT>(up * smooth(to_float<ZT>(z[j])));
+      if (zero) return;
+      __syncthreads();
+      // Again where the entries are: all of a token's are taken off together.
+      for (int k = tid; k <= top_k; k += kThreads) {
+        if (id[k] < 0) continue;
+        float off = 0.f;
+        for (int o = 0; o <= top_k; ++o)
+          if (id[o] == id[k]) off += coef[o];
+        grad[id[k]] = from_float<GT>(up * (smooth(zed[k]) - off));
+      }
+    });
+  });
+}
+
+int check_ids(const char* name, const void* p, int32_t dtype, int64_t n) {
+  if (dtype != TRAIN_INT32 && dtype != TRAIN_INT64)
+    return fail(LAMB_ERR_INVALID, std::string(name) + ": unknown type");
+  if (n == 0) return LAMB_OK;
+  if (!p) return fail(LAMB_ERR_INVALID, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % (dtype == TRAIN_INT64 ? 8u : 4u))
+    return fail(LAMB_ERR_ALIGN, std::string(name) + " is not aligned to its type");
+  return LAMB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+LAMB_API int train_distill(const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                           int64_t n_rows, int64_t vocab, const void* top_ids,
+                           int32_t top_ids_dtype, int64_t top_ids_stride, const void* top_logits,
+                           int32_t top_logits_dtype, int64_t top_logits_stride, int64_t top_k,
+                           const void* labels, int32_t labels_dtype, int64_t ignore_id,
+                           float temperature, float soft_weight, float hard_weight, float* loss,
+                           const float* row_grad, float scale, void* grad, int32_t grad_dtype,
+                           int64_t grad_stride, void* stream) {
+  lambgb::set_last_error("");
+  int rc = check_matrix("logits", logits, logits_dtype, n_rows, vocab, logits_stride);
+  if (rc == LAMB_OK && grad)
+    rc = check_matrix("grad", grad, grad_dtype, n_rows, vocab, grad_stride);
+  if (rc != LAMB_OK) return rc;
+  if (vocab == 0) return fail(LAMB_ERR_INVALID, "vocab must be at least 1");
+  if (top_k < 0 || top_k > kMaxTop)
+    return fail(LAMB_ERR_INVALID, "top_k must be in [0, " + std::to_string(kMaxTop) + "]");
+  if (top_k > 0) {
+    rc = check_matrix("top_logits", top_logits, top_logits_dtype, n_rows, top_k,
+                      top_logits_stride);
+    if (rc == LAMB_OK)
+      rc = check_ids("top_ids", top_ids, top_ids_dtype, n_rows);
+    if (rc == LAMB_OK && top_ids_stride < top_k)
+      rc = fail(LAMB_ERR_INVALID, "top_ids: stride is less than top_k");
+  }
+  if (rc == LAMB_OK && labels) rc = check_ids("labels", labels, labels_dtype, n_rows);
+  if (rc == LAMB_OK) rc = check_vector("loss", loss, TRAIN_FP32);
+  if (rc == LAMB_OK) rc = check_vector("row_grad", row_grad, TRAIN_FP32);
+  if (rc != LAMB_OK) return rc;
+  const float inv = 1.f / temperature;
+  if (!(temperature > 0.f && temperature <= FLT_MAX && inv > 0.f && inv <= FLT_MAX))
+    return fail(LAMB_ERR_INVALID, "temperature and its reciprocal must be finite and > 0");
+  if (!(fabsf(soft_weight) <= FLT_MAX && fabsf(hard_weight) <= FLT_MAX))
+    return fail(LAMB_ERR_INVALID, "soft_weight and hard_weight must be finite");
+  if (hard_weight != 0.f && !labels && n_rows > 0)
+    return fail(LAMB_ERR_INVALID, "hard_weight needs labels");
+  if (n_rows == 0 || (!loss && !grad)) return LAMB_OK;
+  DistillArgs a{};
+  a.logits = logits, a.top_ids = top_ids, a.top_logits = top_logits, a.labels = labels;
+  a.row_grad = row_grad, a.loss = loss, a.grad = grad;
+  a.stride = logits_stride, a.ids_stride = top_ids_stride, a.top_stride = top_logits_stride;
+  a.grad_stride = grad_stride, a.ignore_id = ignore_id;
+  a.vocab = int32_t(vocab), a.top_k = int32_t(top_k);
+  a.inv_temperature = inv, a.temperature = temperature;
+  a.soft_weight = soft_weight, a.hard_weight = hard_weight, a.scale = scale;
+  a.type = logits_dtype, a.grad_type = grad_dtype;
+  a.ids64 = top_ids_dtype == TRAIN_INT64, a.labels64 = labels_dtype == TRAIN_INT64;
+  a.top_type = top_logits_dtype;
+  return launched("distill", launch(row_kernel, dim3(unsigned(n_rows)), kThreads, 0,
+                                    static_cast<cudaStream_t>(stream), true, 1, a));
+}
+
+}  // extern "C"

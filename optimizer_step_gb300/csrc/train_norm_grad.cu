@@ -1,0 +1,223 @@
+// Layer norm's backward pass (train_ops.h).
+#include "train_norm.h"
+
+using namespace traingb;
+
+namespace {
+
+struct GradArgs {
+  const void* dy;
+  const void* x;
+  const void* weight;
+  const float* stats;
+  void* dx;
+  float* partial;  // [pieces][2][dim]: of the weight's and the bias's gradient
+  int64_t n_rows, dim, dy_stride, x_stride, dx_stride;
+  int64_t rows_per_piece;
+  int32_t dy_type, x_type, param_type;
+};
+
+// ------------------------------------------------------------ rows of any width
+constexpr int kWideThreads = 512;
+
+// dx, one CTA a row.
+__global__ void __launch_bounds__(kWideThreads) wide_dx_kernel(const GradArgs a) {
+  __shared__ float part[2][kWideThreads / kWarp];
+  pdl_wait();
+  const int64_t row = blockIdx.x;
+  const float mean = a.stats[row], rstd = a.stats[a.n_rows + row];
+  by_type(a.x_type, [&](auto X) {
+    by_type(a.dy_type, [&](auto Y) {
+      by_type(a.param_type, [&](auto P) {
+        constexpr int XT = decltype(X)::value, YT = decltype(Y)::value, PT = decltype(P)::value;
+        using TX = typename TypeOf<XT>::T;
+        using TY = typename TypeOf<YT>::T;
+        using TP = typename TypeOf<PT>::T;
+        const TX* x = static_cast<const TX*>(a.x) + row * a.x_stride;
+        const TY* dy = static_cast<const TY*>(a.dy) + row * a.dy_stride;
+        const TP* weight = static_cast<const TP*>(a.weight);
+        float s = 0.f, t = 0.f;
+        for (int64_t i = threadIdx.x; i < a.dim; i += kWideThreads) {
+          float g = to_float<YT>(dy[i]);
+          if (weight) g *= to_float<PT>(weight[i]);
+          s += g;
+          t += g * ((to_float<XT>(x[i]) - mean) * rstd);
+        }
+        const float along1 = cta_sum<kWideThreads>(s, part[0]) / float(a.dim);
+        const float alongx = cta_sum<kWideThreads>(t, part[1]) / float(a.dim);
+        TX* dx = static_cast<TX*>(a.dx) + row * a.dx_stride;
+        for (int64_t i = threadIdx.x; i < a.dim; i += kWideThreads) {
+          float g = to_float<YT>(dy[i]);
+          if (weight) g *= to_float<PT>(weight[i]);
+          const float xhat = (to_float<XT>(x[i]) - mean) * rstd;
+          dx[i] = from_float<XT>(rstd * (g - along1 - xhat * alongx));
+        }
+      });
+    });
+  });
+}
+
+// Partial sums over rows_per_piece rows, a CTA for 32 columns.
+constexpr int kSlabWarps = 8;
+__global__ void __launch_bounds__(kSlabWarps* kWarp) wide_partial_kernel(const GradArgs a) {
+  __shared__ float part[2][kSlabWarps][kWarp];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t column = int64_t(blockIdx.x) * kWarp + lane;
+  const int64_t first = int64_t(blockIdx.y) * a.rows_per_piece;
+  const int64_t end = min(a.n_rows, first + a.rows_per_piece);
+  float s = 0.f, t = 0.f;
+  if (column < a.dim) {
+    by_type(a.x_type, [&](auto X) {
+      by_type(a.dy_type, [&](auto Y) {
+        constexpr int XT = decltype(X)::value, YT = decltype(Y)::value;
+        const auto* x = static_cast<const typename TypeOf<XT>::T*>(a.x) + column;
+        const auto* dy = static_cast<const typename TypeOf<YT>::T*>(a.dy) + column;
+        for (int64_t r = first + warp; r < end; r += kSlabWarps) {
+          const float g = to_float<YT>(dy[r * a.dy_stride]);
+          s += g * ((to_float<XT>(x[r * a.x_stride]) - a.stats[r]) * a.stats[a.n_rows + r]);
+          t += g;
+        }
+      });
+    });
+  }
+  part[0][warp][lane] = s, part[1][warp][lane] = t;
+  __syncthreads();
+  if (warp < 2 && column < a.dim) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kSlabWarps; ++w) s += part[warp][w][lane];
+    a.partial[(2 * int64_t(blockIdx.y) + warp) * a.dim + column] = s;
+  }
+}
+
+// --------------------------------------------------------------------- the join
+struct JoinArgs {
+  const float* partial;
+  void* weight_grad;
+  void* bias_grad;
+  int64_t dim, pieces;
+  int32_t type, accumulate;
+};
+
+// Adds the pieces of 32 columns in a fixed order.
+constexpr int kJoinWarps = 16;
+__global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const JoinArgs a) {
+  __shared__ float part[2][kJoinWarps][kWarp];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t column = int64_t(blockIdx.x) * kWarp + lane;
+  float s = 0.f, t = 0.f;
+  if (column < a.dim)
+    for (int64_t k = warp; k < a.pieces; k += kJoinWarps) {
+      s += a.partial[2 * k * a.dim + column];
+      t += a.partial[(2 * k + 1) * a.dim + column];
+    }
+  part[0][warp][lane] = s, part[1][warp][lane] = t;
+  __syncthreads();
+  void* out = warp == 0 ? a.weight_grad : a.bias_grad;
+  if (warp < 2 && column < a.dim && out) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) s += part[warp][w][lane];
+    by_type(a.type, [&](auto P) {
+      constexpr int PT = decltype(P)::value;
+      auto* p = static_cast<typename TypeOf<PT>::T*>(out) + column;
+      if (a.accumulate) s += to_float<PT>(*p);
+      *p = from_float<PT>(s);
+    });
+  }
+}
+
+// ------------------------------------------------------------------------- plan
+struct Plan {
+  int64_t pieces, rows_per_piece;
+};
+
+Plan plan(int64_t n_rows, int64_t dim) {
+  Plan p{};
+  if (n_rows == 0) return p;
+  p.rows_per_piece = std::max<int64_t>(64, (n_rows + 255) / 256);
+  p.pieces = (n_rows + p.rows_per_piece - 1) / p.rows_per_piece;
+  return p;
+}
+
+constexpr int64_t kMaxElements = int64_t(1) << 40;
+
+int check_sizes(int64_t n_rows, int64_t dim) {
+  if (n_rows < 0 || dim < 1 || n_rows > kMaxCount || dim > kMaxCount)
+    return fail(LAMB_ERR_INVALID, "n_rows must be in [0, 2^31 - 1], dim in [1, 2^31 - 1]");
+  if (n_rows > kMaxElements / dim) return fail(LAMB_ERR_INVALID, "n_rows * dim is too large");
+  return LAMB_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+LAMB_API int train_layer_norm_grad_workspace(int64_t n_rows, int64_t dim, int64_t* bytes) {
+  lambgb::set_last_error("");
+  if (!bytes) return fail(LAMB_ERR_INVALID, "bytes is NULL");
+  const int rc = check_sizes(n_rows, dim);
+  if (rc != LAMB_OK) return rc;
+  *bytes = plan(n_rows, dim).pieces * 2 * dim * 4;
+  return LAMB_OK;
+}
+
+LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
+                                   int64_t grad_out_stride, const void* x, int32_t x_dtype,
+                                   int64_t x_stride, int64_t n_rows, int64_t dim,
+                                   const void* weight, int32_t weight_dtype, const float* stats,
+                                   void* x_grad, int64_t x_grad_stride, void* weight_grad,
+                                   void* bias_grad, int32_t param_grad_dtype, int32_t accumulate,
+                                   void* workspace, int64_t workspace_bytes, void* stream) {
+  lambgb::set_last_error("");
+  int rc = check_matrix("grad_out", grad_out, grad_out_dtype, n_rows, dim, grad_out_stride);
+  if (rc == LAMB_OK) rc = check_matrix("x", x, x_dtype, n_rows, dim, x_stride);
+  if (rc == LAMB_OK && x_grad)
+    rc = check_matrix("x_grad", x_grad, x_dtype, n_rows, dim, x_grad_stride);
+  if (rc == LAMB_OK) rc = check_sizes(n_rows, dim);
+  if (rc == LAMB_OK) rc = check_vector("weight", weight, weight_dtype);
+  if (rc == LAMB_OK) rc = check_vector("stats", stats, TRAIN_FP32);
+  if (rc == LAMB_OK) rc = check_vector("weight_grad", weight_grad, param_grad_dtype);
+  if (rc == LAMB_OK) rc = check_vector("bias_grad", bias_grad, param_grad_dtype);
+  if (rc != LAMB_OK) return rc;
+  if (accumulate != 0 && accumulate != 1)
+    return fail(LAMB_ERR_INVALID, "accumulate must be 0 or 1");
+  if (n_rows > 0 && !stats) return fail(LAMB_ERR_INVALID, "stats is NULL");
+  const bool params = weight_grad || bias_grad;
+  const Plan p = plan(n_rows, dim);
+  if (params && p.pieces > 0) {
+    if (!workspace || workspace_bytes < p.pieces * 2 * dim * 4)
+      return fail(LAMB_ERR_INVALID, "workspace is missing or too small");
+    if (reinterpret_cast<uintptr_t>(workspace) % 16)
+      return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
+  }
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  GradArgs a{};
+  a.dy = grad_out, a.x = x, a.weight = weight, a.stats = stats, a.dx = x_grad;
+  a.partial = static_cast<float*>(workspace);
+  a.n_rows = n_rows, a.dim = dim;
+  a.dy_stride = grad_out_stride, a.x_stride = x_stride, a.dx_stride = x_grad_stride;
+  a.rows_per_piece = p.rows_per_piece;
+  a.dy_type = grad_out_dtype, a.x_type = x_dtype, a.param_type = weight_dtype;
+  cudaError_t ce = cudaSuccess;
+  // The sums first: dx may take the place of grad_out.
+  if (params && n_rows > 0)
+    ce = launch(wide_partial_kernel,
+                dim3(unsigned((dim + kWarp - 1) / kWarp), unsigned(p.pieces)),
+                kSlabWarps * kWarp, 0, st, true, 1, a);
+  if (ce == cudaSuccess && x_grad && n_rows > 0)
+    ce = launch(wide_dx_kernel, dim3(unsigned(n_rows)), kWideThreads, 0, st, true, 1, a);
+  if (ce == cudaSuccess && params && !(n_rows == 0 && accumulate)) {
+    JoinArgs j{};
+    j.partial = a.partial, j.weight_grad = weight_grad, j.bias_grad = bias_grad;
+    j.dim = dim, j.pieces = p.pieces;
+    j.type = param_grad_dtype, j.accumulate = accumulate;
+    ce = launch(join_kernel, dim3(unsigned((dim + kWarp - 1) / kWarp)), kJoinWarps * kWarp, 0,
+                st, true, 1, j);
+  }
+  return launched("layer_norm_grad", ce);
+}
+
+}  // extern "C"
