@@ -96,6 +96,40 @@ struct Pack {
       w[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
     }
   }
+  // The same of what is read once, by a plain load: what a kernel also writes.
+  __device__ __forceinline__ void load_once(const T* p) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+      }
+    } else if constexpr (kBytes == 8) {
+      const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
+      w[0] = q.x, w[1] = q.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
+    } else {
+      w[0] = __ldcs(reinterpret_cast<const uint16_t*>(p));
+    }
+  }
+  // By a plain load that keeps its place among the stores around it.
+  __device__ __forceinline__ void load_kept(const T* p) {
+    if constexpr (kBytes >= 16) {
+#pragma unroll
+      for (int i = 0; i < kBytes / 16; ++i) {
+        const uint4 q = reinterpret_cast<const uint4*>(p)[i];
+        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
+      }
+    } else if constexpr (kBytes == 8) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      w[0] = q.x, w[1] = q.y;
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+  }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (kBytes >= 16) {
 #pragma unroll
@@ -133,6 +167,62 @@ struct Pack {
     }
   }
 };
+
+// Two fp32 values in one register pair, for the instructions that work on both.
+using F2 = unsigned long long;
+__device__ __forceinline__ F2 pair(float lo, float hi) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ F2 pair(float x) { return pair(x, x); }
+__device__ __forceinline__ void split(F2 p, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 p) {
+  float lo, hi;
+  split(p, lo, hi);
+  return lo + hi;
+}
+
+// Elements 2 i and 2 i + 1 of a pack.
+template <int DT, int VEC>
+__device__ __forceinline__ F2 get2(const Pack<DT, VEC>& p, int i) {
+  static_assert(VEC % 2 == 0, "pairs");
+  if constexpr (DT == TRAIN_FP32) {
+    return pair(__uint_as_float(p.w[2 * i]), __uint_as_float(p.w[2 * i + 1]));
+  } else if constexpr (DT == TRAIN_BF16) {
+    return pair(__uint_as_float(p.w[i] << 16), __uint_as_float(p.w[i] & 0xffff0000u));
+  } else {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p.w[i]));
+    return pair(f.x, f.y);
+  }
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void set2(Pack<DT, VEC>& p, int i, F2 x) {
+  float lo, hi;
+  split(x, lo, hi);
+  if constexpr (DT == TRAIN_FP32) {
+    p.w[2 * i] = __float_as_uint(lo), p.w[2 * i + 1] = __float_as_uint(hi);
+  } else {
+    p.w[i] = pack2<DT>(lo, hi);
+  }
+}
 
 // Lets the kernel behind this one start (its CTAs wait for this one to end
 // before they touch what it writes), and waits for the kernel in front.

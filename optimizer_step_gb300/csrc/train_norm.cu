@@ -1,5 +1,5 @@
 // Layer norm and its backward pass (train_ops.h).
-#include "train_norm.h"
+#include "train_norm_rows.h"
 
 using namespace traingb;
 
@@ -83,6 +83,78 @@ __global__ void __launch_bounds__(kWideThreads) wide_norm_kernel(const WideArgs 
   });
 }
 
+
+constexpr int kSms = 152;
+constexpr int64_t kMostShared = 224 * 1024;  // a CTA's dynamic shared memory
+
+// Launches the kernel for rows that stay on chip, if there is one; sets `done`.
+cudaError_t launch_rows(NormArgs& a, int32_t x_dtype, int32_t y_dtype, cudaStream_t stream,
+                        bool* done) {
+  *done = false;
+  const int64_t dim = a.dim;
+  const NormKernels& k = x_dtype == TRAIN_BF16   ? norm_kernels_bf16(y_dtype)
+                         : x_dtype == TRAIN_FP16 ? norm_kernels_fp16(y_dtype)
+                                                 : norm_kernels_fp32(y_dtype);
+  const auto phase = [](const void* p, int32_t type, int64_t e) {
+    return int64_t(reinterpret_cast<uintptr_t>(p) / uintptr_t(size_of(type))) % e;
+  };
+  const auto go = [&](NormKernel kernel, int64_t ctas, int threads, int64_t smem) {
+    *done = true;
+    if (smem > 48 * 1024) {
+      const cudaError_t ce =
+          cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+      if (ce != cudaSuccess) return ce;
+    }
+    return launch(kernel, dim3(unsigned(ctas)), threads, size_t(smem), stream, true, 1, a);
+  };
+  // Short rows of whole units.
+  int64_t e = x_dtype == TRAIN_FP32 || y_dtype == TRAIN_FP32 ? 4 : 8;
+  if (dim <= kWarp * e && dim % e == 0 && a.x_stride % e == 0 && a.y_stride % e == 0 &&
+      phase(a.x, x_dtype, e) == 0 && phase(a.y, y_dtype, e) == 0) {
+    a.lanes = 1;
+    while (a.lanes * e < dim) a.lanes *= 2;
+    const int64_t rows = kNormThreads / a.lanes * 4;  // a CTA
+    return go(k.whole, (a.n_rows + rows - 1) / rows, kNormThreads, 0);
+  }
+  const int64_t params = 2 * int64_t(staged_width(a.dim)) * 4;
+  e = x_dtype == TRAIN_FP32 ? 4 : 8;
+  const int64_t px = phase(a.x, x_dtype, e), row = a.x_stride % e;
+  if (dim >= 256 && px == phase(a.y, y_dtype, e) && row == a.y_stride % e) {
+    a.phase = int32_t(px), a.row_phase = int32_t(row);
+    a.period = 1;
+    while (a.period * row % e != 0) a.period *= 2;
+    const int64_t units = dim / e;
+    const int m = (units <= 16 / e * kWarp ? 16 : 32) / int(e);  // units a thread
+    a.lanes = int32_t((units + m * kWarp - 1) / (m * kWarp)) * kWarp;
+    const int64_t stage = int64_t(m) * a.lanes * 16;  // of a group
+    if (params + 2 * stage <= kMostShared && a.lanes <= 768) {
+      // As many rows at once as a CTA holds and there are for each SM.
+      int64_t groups = std::min<int64_t>(768 / a.lanes, a.lanes == kWarp ? 24 : 15);
+      groups = std::min(groups, (a.n_rows + kSms - 1) / kSms);
+      groups = std::max<int64_t>(1, std::min(groups, (kMostShared - params) / (2 * stage)));
+      a.stages = params + 3 * groups * stage <= kMostShared ? 3 : 2;
+      int64_t ctas = std::min<int64_t>(kSms, (a.n_rows + groups - 1) / groups);
+      ctas = (ctas + a.period - 1) / a.period * a.period;
+      return go(k.ring[a.lanes > kWarp ? 2 : m * e / 32], ctas, int(groups * a.lanes),
+                params + a.stages * groups * stage);
+    }
+  }
+  // Element by element.
+  int s = 0;
+  while (s < 2 && dim > kScalars[s] * kWarp) ++s;
+  a.lanes = int32_t((dim + kScalars[s] * kWarp - 1) / (kScalars[s] * kWarp)) * kWarp;
+  // Threads without elements read behind the staged vectors' ends.
+  const int64_t smem = params + int64_t(kScalars[s]) * kWarp * 4;
+  if (a.lanes > 512 || smem > kMostShared) return cudaSuccess;
+  int64_t groups = std::max<int64_t>(1, std::min<int64_t>(256 / a.lanes, a.n_rows));
+  const int64_t resident =
+      std::max<int64_t>(1, std::min<int64_t>(1024 / (groups * a.lanes), kMostShared / smem));
+  return go(k.scalar[a.lanes > kWarp ? 3 : s],
+            std::min(resident * kSms, (a.n_rows + groups - 1) / groups),
+            int(groups * a.lanes), smem);
+}
+
 }  // namespace
 
 extern "C" {
@@ -101,6 +173,14 @@ LAMB_API int train_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, 
   if (dim == 0) return fail(LAMB_ERR_INVALID, "dim must be at least 1");
   if (!(eps >= 0.f && eps <= FLT_MAX)) return fail(LAMB_ERR_INVALID, "eps must be finite and >= 0");
   if (n_rows == 0) return LAMB_OK;
+  NormArgs f{};
+  f.x = x, f.weight = weight, f.bias = bias, f.y = y, f.stats = stats;
+  f.n_rows = n_rows, f.x_stride = x_stride, f.y_stride = y_stride;
+  f.eps = eps, f.dim = int32_t(dim), f.param_type = param_dtype;
+  bool done = false;
+  const cudaError_t ce =
+      launch_rows(f, x_dtype, y_dtype, static_cast<cudaStream_t>(stream), &done);
+  if (done || ce != cudaSuccess) return launched("layer_norm", ce);
   WideArgs a{};
   a.x = x, a.weight = weight, a.bias = bias, a.y = y, a.stats = stats;
   a.n_rows = n_rows, a.dim = dim, a.x_stride = x_stride, a.y_stride = y_stride;

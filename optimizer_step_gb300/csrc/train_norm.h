@@ -43,12 +43,66 @@ __device__ __forceinline__ float cta_max(float x, float* part) {
   return x;
 }
 
+// The threads that share a row: part of a warp (a power of two), a warp, or several
+// warps with a named barrier and, for each of kSlots sums, a place a warp in shared
+// memory.  A place may be used again when another sum has been taken in between.
+enum class Span { kPart, kWarp, kWarps };
+constexpr int kSlots = 5;
+
+struct Group {
+  int lanes;
+  int lane;     // of this thread
+  int barrier;  // kWarps
+  float* part;  // kWarps: [kSlots][32 a CTA], at this group's first warp
+
+  template <Span S, class F>
+  __device__ __forceinline__ float join(float x, int slot, float none, F&& f) const {
+    if constexpr (S == Span::kPart) {
+      for (int d = 1; d < lanes; d *= 2) x = f(x, __shfl_xor_sync(kAll, x, d));
+      return x;
+    }
+#pragma unroll
+    for (int d = 1; d < traingb::kWarp; d *= 2) x = f(x, __shfl_xor_sync(kAll, x, d));
+    if constexpr (S == Span::kWarps) {
+      float* p = part + slot * traingb::kWarp;
+      if ((lane & 31) == 0) p[lane >> 5] = x;
+      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(lanes) : "memory");
+      x = (lane & 31) < lanes / traingb::kWarp ? p[lane & 31] : none;
+#pragma unroll
+      for (int d = 1; d < traingb::kWarp; d *= 2) x = f(x, __shfl_xor_sync(kAll, x, d));
+    }
+    return x;
+  }
+  template <Span S>
+  __device__ __forceinline__ float sum(float x, int slot) const {
+    return join<S>(x, slot, 0.f, [](float a, float b) { return a + b; });
+  }
+  template <Span S>
+  __device__ __forceinline__ float largest(float x, int slot) const {
+    return join<S>(x, slot, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
+  }
+};
+
+__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+  const uint32_t t = uint32_t(__cvta_generic_to_shared(to));
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(t), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Whether the squares that gave a variance kept their bits: none left fp32's
 // range at the top, and those that did at the bottom are nothing beside eps.
 __device__ __forceinline__ bool in_range(float var, float eps) {
   return var <= FLT_MAX && var + eps > 0x1p-80f;
 }
-__device__ __forceinline__ float rstd_of(float var, float eps) { return 1.f / sqrtf(var + eps); }
+// 1 / sqrt(var + eps), by a step of Newton's method on the instruction's result.
+__device__ __forceinline__ float rstd_of(float var, float eps) {
+  const float v = var + eps, r = rsqrtf(v);
+  return fmaf(r * 0.5f, fmaf(-v * r, r, 1.f), r);
+}
 // A power of two that brings a row with this largest magnitude near 1.
 __device__ __forceinline__ float scale_of(float top) {
   if (!(top > 0.f && top <= FLT_MAX)) return 1.f;
