@@ -1,31 +1,10 @@
 // The loss against a teacher's top logits and the true labels, and its gradient
 // (train_ops.h).
-#include "train_norm.h"
+#include "train_distill_rows.h"
 
 using namespace traingb;
 
 namespace {
-
-constexpr int kMaxTop = 1024;
-constexpr float kLog2e = 1.4426950408889634f;
-
-struct DistillArgs {
-  const void* logits;
-  const void* top_ids;
-  const void* top_logits;
-  const void* labels;
-  const float* row_grad;
-  float* loss;
-  void* grad;
-  int64_t stride, ids_stride, top_stride, grad_stride, ignore_id;
-  int32_t vocab, top_k;
-  float inv_temperature, soft_weight, hard_weight, temperature, scale;
-  int32_t type, grad_type, ids64, top_type, labels64;
-};
-
-__device__ __forceinline__ int64_t read_id(const void* p, int64_t i, int32_t is64) {
-  return is64 ? static_cast<const int64_t*>(p)[i] : int64_t(static_cast<const int32_t*>(p)[i]);
-}
 
 constexpr int kThreads = 512;
 
@@ -155,6 +134,51 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
   });
 }
 
+constexpr int kSms = 152;
+constexpr int64_t kMostShared = 96 * 1024;  // a CTA's dynamic shared memory
+constexpr int64_t kSliceBytes = 64 * 1024;   // three CTAs an SM
+
+// Launches the kernel for rows that stay in shared memory, if one holds them; sets `done`.
+cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
+  *done = false;
+  const int e = 16 / size_of(a.type);
+  const int64_t units = a.vocab / e;
+  const auto phase = [&](const void* p, int32_t type) {
+    return int32_t(reinterpret_cast<uintptr_t>(p) / uintptr_t(size_of(type)) % uintptr_t(e));
+  };
+  a.phase = phase(a.logits, a.type), a.row_phase = int32_t(a.stride % e);
+  a.whole = !a.grad || (phase(a.grad, a.grad_type) == a.phase && a.grad_stride % e == a.row_phase);
+  a.ctas = 1;
+  while (units * 16 > a.ctas * kSliceBytes) a.ctas *= 2;
+  if (a.ctas > kMostCtas || units == 0) return cudaSuccess;
+  a.slice = int32_t((units + a.ctas - 1) / a.ctas);
+  int threads = kDistillThreads;
+  while (threads > kWarp && a.slice < threads * 8) threads /= 2;
+  const int64_t smem = int64_t(a.slice) * 16 + 2 * 3 * 4 * int64_t(a.top_k + 1);
+  if (smem > kMostShared) return cudaSuccess;
+  // Two softmaxes only where the terms are at two temperatures.
+  const bool soft = a.top_k > 0 && a.soft_weight != 0.f, hard = a.labels && a.hard_weight != 0.f;
+  const int temps = soft && hard && a.temperature != 1.f;
+  const DistillKernels& k = a.type == TRAIN_BF16   ? distill_kernels_bf16()
+                            : a.type == TRAIN_FP16 ? distill_kernels_fp16()
+                                                   : distill_kernels_fp32();
+  const DistillKernel kernel = a.grad ? k.grad[a.grad_type][temps] : k.loss[temps];
+  const void* f = reinterpret_cast<const void*>(kernel);
+  cudaError_t ce = cudaSuccess;
+  if (smem > 32 * 1024)
+    ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+  if (ce == cudaSuccess && a.ctas > 8)
+    ce = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (ce != cudaSuccess) return ce;
+  const int64_t resident = std::max<int64_t>(
+      1, std::min<int64_t>(std::min(24, 3 * kDistillThreads / threads),
+                           (227 * 1024) / (smem + 8 * 1024)));
+  const int64_t clusters = std::min<int64_t>(a.n_rows, std::max<int64_t>(1, resident * kSms / a.ctas));
+  *done = true;
+  return launch(kernel, dim3(unsigned(clusters * a.ctas)), threads, size_t(smem), stream, true,
+                a.ctas, a);
+}
+
 int check_ids(const char* name, const void* p, int32_t dtype, int64_t n) {
   if (dtype != TRAIN_INT32 && dtype != TRAIN_INT64)
     return fail(LAMB_ERR_INVALID, std::string(name) + ": unknown type");
@@ -216,6 +240,10 @@ LAMB_API int train_distill(const void* logits, int32_t logits_dtype, int64_t log
   a.type = logits_dtype, a.grad_type = grad_dtype;
   a.ids64 = top_ids_dtype == TRAIN_INT64, a.labels64 = labels_dtype == TRAIN_INT64;
   a.top_type = top_logits_dtype;
+  a.n_rows = n_rows;
+  bool done = false;
+  const cudaError_t ce = launch_rows(a, static_cast<cudaStream_t>(stream), &done);
+  if (done || ce != cudaSuccess) return launched("distill", ce);
   return launched("distill", launch(row_kernel, dim3(unsigned(n_rows)), kThreads, 0,
                                     static_cast<cudaStream_t>(stream), true, 1, a));
 }
