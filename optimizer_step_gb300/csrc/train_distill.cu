@@ -154,15 +154,17 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   a.slice = int32_t((units + a.ctas - 1) / a.ctas);
   int threads = kDistillThreads;
   while (threads > kWarp && a.slice < threads * 8) threads /= 2;
-  const int64_t smem = int64_t(a.slice) * 16 + 2 * 3 * 4 * int64_t(a.top_k + 1);
+  const int64_t smem = int64_t(a.slice) * 16 + 2 * 3 * 4 * int64_t((a.top_k + 4) / 4 * 4);
   if (smem > kMostShared) return cudaSuccess;
   // Two softmaxes only where the terms are at two temperatures.
   const bool soft = a.top_k > 0 && a.soft_weight != 0.f, hard = a.labels && a.hard_weight != 0.f;
-  const int temps = soft && hard && a.temperature != 1.f;
+  const int terms = !soft || !hard || a.temperature == 1.f ? kOne
+                    : a.temperature == 2.f                 ? kSquares
+                                                           : kTwo;
   const DistillKernels& k = a.type == TRAIN_BF16   ? distill_kernels_bf16()
                             : a.type == TRAIN_FP16 ? distill_kernels_fp16()
                                                    : distill_kernels_fp32();
-  const DistillKernel kernel = a.grad ? k.grad[a.grad_type][temps] : k.loss[temps];
+  const DistillKernel kernel = a.grad ? k.grad[a.grad_type][terms] : k.loss[terms];
   const void* f = reinterpret_cast<const void*>(kernel);
   cudaError_t ce = cudaSuccess;
   if (smem > 32 * 1024)

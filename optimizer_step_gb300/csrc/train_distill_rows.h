@@ -5,6 +5,8 @@
 
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "train_norm.h"
 
 namespace traingb {
@@ -64,58 +66,67 @@ struct Unit {
     return get2(p, i);
   }
 };
-template <int ZT>
-__device__ __forceinline__ float largest(const Unit<ZT>& a, const Unit<ZT>& b) {
+template <int ZT, int N>
+__device__ __forceinline__ float largest(const Unit<ZT> (&x)[N]) {
   if constexpr (ZT == TRAIN_FP32) {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float lo, hi;
-      split(a.get(i), lo, hi);
-      m = fmaxf(m, fmaxf(lo, hi));
-      split(b.get(i), lo, hi);
-      m = fmaxf(m, fmaxf(lo, hi));
-    }
+    for (int k = 0; k < N; ++k)
+      m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(x[k].q.x), __uint_as_float(x[k].q.y))),
+                fmaxf(__uint_as_float(x[k].q.z), __uint_as_float(x[k].q.w)));
     return m;
   } else {
-    const uint32_t w[8] = {a.q.x, a.q.y, a.q.z, a.q.w, b.q.x, b.q.y, b.q.z, b.q.w};
-    if constexpr (ZT == TRAIN_BF16) {
-      const auto* h = reinterpret_cast<const __nv_bfloat162*>(w);
-      const auto m = __hmax2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])),
-                             __hmax2(__hmax2(h[4], h[5]), __hmax2(h[6], h[7])));
-      return fmaxf(__low2float(m), __high2float(m));
-    } else {
-      const auto* h = reinterpret_cast<const __half2*>(w);
-      const auto m = __hmax2(__hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3])),
-                             __hmax2(__hmax2(h[4], h[5]), __hmax2(h[6], h[7])));
-      return fmaxf(__low2float(m), __high2float(m));
-    }
+    using H = std::conditional_t<ZT == TRAIN_BF16, __nv_bfloat162, __half2>;
+    const auto as = [](const uint32_t& w) { return *reinterpret_cast<const H*>(&w); };
+    H m = as(x[0].q.x);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      m = __hmax2(__hmax2(m, __hmax2(as(x[k].q.x), as(x[k].q.y))),
+                  __hmax2(as(x[k].q.z), as(x[k].q.w)));
+    return fmaxf(__low2float(m), __high2float(m));
   }
 }
 
-// Sums of exponentials relative to a largest value: of one temperature or of two.
-// The largest value starts at the lowest finite one, so that it is never -inf.
-template <int TEMPS>
+// The softmaxes that a row needs: one (one term, or both at temperature 1), two, or two
+// of which the hard term's exponentials are the squares of the soft term's.
+constexpr int kOne = 0, kTwo = 1, kSquares = 2;
+
+// Sums of exponentials relative to a largest value.  That starts at the lowest finite
+// one, so that it is never -inf.
+template <int TERMS>
 struct Sums {
+  static constexpr int N = TERMS == kOne ? 1 : 2;
   float top = -FLT_MAX;
-  float s[TEMPS] = {};
-  __device__ __forceinline__ void raise(float to, const float (&c)[TEMPS]) {
-    const float d = top - to;
+  float s[N] = {};
+  // Factors that take sums relative to `top` to ones relative to `to`.
+  static __device__ __forceinline__ void factors(float d, const float (&c)[N], float (&f)[N]) {
+    f[0] = exp2_of(d * c[0]);
+    if constexpr (TERMS == kTwo) f[1] = exp2_of(d * c[1]);
+    if constexpr (TERMS == kSquares) f[1] = f[0] * f[0];
+  }
+  __device__ __forceinline__ void raise(float to, const float (&c)[N]) {
+    float f[N];
+    factors(top - to, c, f);
 #pragma unroll
-    for (int k = 0; k < TEMPS; ++k) s[k] *= exp2_of(d * c[k]);
+    for (int k = 0; k < N; ++k) s[k] *= f[k];
     top = to;
   }
-  __device__ __forceinline__ void join_warp(const float (&c)[TEMPS]) {
-    raise(warp_max(top), c);
+  // Over `lanes` neighbouring lanes.
+  __device__ __forceinline__ void join(int lanes, const float (&c)[N]) {
+    float to = top;
+    for (int d = 1; d < lanes; d *= 2) to = fmaxf(to, __shfl_xor_sync(kAll, to, d));
+    raise(to, c);
+    for (int d = 1; d < lanes; d *= 2)
 #pragma unroll
-    for (int k = 0; k < TEMPS; ++k) s[k] = warp_sum(s[k]);
+      for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(kAll, s[k], d);
   }
 };
 
 constexpr int kDistillThreads = 256;
 constexpr int kDistillWarps = kDistillThreads / kWarp;
 constexpr int kMostCtas = 16;
-constexpr int kParts = 4;  // of a row, each waited for by itself
+constexpr int kParts = 2;   // of a row, each waited for by itself
+constexpr int kAtOnce = 4;  // units a thread reads together
 
 // A row's slice is copied into shared memory asynchronously, in units of 16 bytes, and
 // read there twice: once for the running largest value and sums of exponentials, once
@@ -125,8 +136,8 @@ constexpr int kParts = 4;  // of a row, each waited for by itself
 // first CTA, one element each.  The teacher's entries and the label are gathered while
 // the row is on its way; the tokens they name are written again, all of a token's
 // shares together, when the others are done.
-//   ZT, GT  types of logits and grad        TEMPS  1: one softmax serves both terms
-template <int ZT, int GT, int TEMPS, bool GRAD>
+//   ZT, GT  types of logits and grad        TERMS  the softmaxes (kOne and so on)
+template <int ZT, int GT, int TERMS, bool GRAD>
 __global__ void __launch_bounds__(kDistillThreads, 3)
     distill_kernel(const __grid_constant__ DistillArgs a) {
   namespace cg = cooperative_groups;
@@ -142,7 +153,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   __shared__ float terms[2][kDistillWarps];
   const int tid = threadIdx.x, threads = blockDim.x, warps = threads / kWarp;
   const int warp = tid / kWarp, lane = tid % kWarp;
-  const int vocab = a.vocab, room = a.top_k + 1;
+  const int vocab = a.vocab, room = (a.top_k + 4) / 4 * 4;
   const int rank = a.ctas == 1 ? 0 : int(blockIdx.x) % a.ctas;
   uint4* slot = reinterpret_cast<uint4*>(smem);
   unsigned char* lists = smem + size_t(a.slice) * 16;
@@ -150,9 +161,10 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   const bool soft = a.top_k > 0 && a.soft_weight != 0.f;
   const bool hard = a.labels && a.hard_weight != 0.f;
   // Scales of the exponents: the soft term's and, of two, behind it the hard term's.
-  float c[TEMPS];
+  constexpr int N = Sums<TERMS>::N;
+  float c[N];
   c[0] = soft ? a.inv_temperature * kLog2e : kLog2e;
-  if constexpr (TEMPS == 2) c[1] = kLog2e;
+  if constexpr (N == 2) c[1] = kLog2e;
   const float ct = a.inv_temperature * kLog2e;
 
   cg::cluster_group cluster = cg::this_cluster();
@@ -160,8 +172,11 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   pdl_wait();
 
   const int64_t step = int64_t(gridDim.x) / a.ctas;
-  const int per_thread = (a.slice + threads - 1) / threads;
-  const int per_part = ((per_thread + kParts - 1) / kParts + 1) / 2 * 2;
+  // Of a slice's kParts parts each warp has a run of `run` units, 32 side by side at a time.
+  const int share = kParts * warps * kWarp;
+  const int run = (a.slice + share - 1) / share * kWarp;
+  const int at0 = rank * a.slice;  // the slice's first unit
+  const auto first_of = [&](int part) { return (part * warps + warp) * run; };
   const auto head_of = [&](int64_t row) {
     return (E - (a.phase + int(row % E) * a.row_phase) % E) % E;
   };
@@ -179,21 +194,40 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     return (!a.labels || (label != a.ignore_id && label >= 0 && label < vocab)) &&
            (soft || hard) && (a.loss || up != 0.f);
   };
-  const auto copy = [&](const TZ* from, int units, int j) {
-    const int u = rank * a.slice + j * threads + tid;
-    if (j * threads + tid < a.slice && u < units)
-      copy_async16(slot + j * threads + tid, from + int64_t(u) * E);
+  const auto mine_of = [&](int units) { return min(a.slice, units - at0); };
+  const auto copy_part = [&](const TZ* from, int mine, int part) {
+    const int first = first_of(part), end = min(mine, first + run);
+    uint4* to = slot + first + lane;
+    from += (first + lane) * E;
+    for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (i + k * kWarp < end) copy_async16(to + k * kWarp, from + k * (kWarp * E));
+      to += kAtOnce * kWarp, from += kAtOnce * kWarp * E;
+    }
+    copy_commit();
   };
+  // The teacher's entry that this thread has of the first `threads` of a row.
+  const auto entry_of = [&](int64_t row, int k, int64_t& i, float& t) {
+    i = read_id(a.top_ids, row * a.ids_stride + k, a.ids64);
+    by_type(a.top_type, [&](auto T) {
+      constexpr int TT = decltype(T)::value;
+      t = to_float<TT>(
+          static_cast<const typename TypeOf<TT>::T*>(a.top_logits)[row * a.top_stride + k]);
+    });
+  };
+  const bool has_entry = soft && tid < a.top_k;
+  const int entry_warps = soft ? min(warps, (a.top_k + kWarp - 1) / kWarp) : 0;
+  int64_t entry = -1;
+  float entry_t = 0.f;
   int64_t row = int64_t(blockIdx.x) / a.ctas;
   if (row < a.n_rows) {
     look(row, label, up);
-    const bool live = live_of(label, up);
-    const int head = head_of(row), units = (vocab - head) / E;
-    for (int part = 0; part < kParts; ++part) {
-      for (int j = part * per_part; live && j < min(per_thread, (part + 1) * per_part); ++j)
-        copy(row_of(row) + head, units, j);
-      copy_commit();
-    }
+    if (has_entry) entry_of(row, tid, entry, entry_t);
+    const int head = head_of(row);
+    const int mine = live_of(label, up) ? mine_of((vocab - head) / E) : 0;
+    for (int part = 0; part < kParts; ++part)
+      copy_part(row_of(row) + head + int64_t(at0) * E, mine, part);
   }
   int parity = 0;
   for (; row < a.n_rows; row += step, parity ^= 1) {
@@ -203,20 +237,20 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     const TZ* z = row_of(row);
     TG* grad = GRAD ? static_cast<TG*>(a.grad) + row * a.grad_stride : nullptr;
     const int head = head_of(row), units = (vocab - head) / E;
-    const int mine = min(a.slice, units - rank * a.slice);  // units here; < 0: none
+    const int mine = mine_of(units);  // units here; < 0: none
     const bool live = live_of(label, up);
     // The next row.
     const int64_t next = row + step;
     int64_t next_label = -1;
     float next_up = 0.f;
-    bool next_live = false;
-    int next_head = 0, next_units = 0;
+    const TZ* next_from = row_of(next) + int64_t(at0) * E;
+    int next_mine = 0;  // none if it is not read
     if (next < a.n_rows) {
       look(next, next_label, next_up);
-      next_live = live_of(next_label, next_up);
-      next_head = head_of(next), next_units = (vocab - next_head) / E;
+      const int next_head = head_of(next);
+      next_from += next_head;
+      if (live_of(next_label, next_up)) next_mine = mine_of((vocab - next_head) / E);
     }
-    const TZ* next_from = row_of(next) + next_head;
     // The column of this thread's single element, if it has one.
     int single = -1;
     if (rank == 0 && tid < kWarp) {
@@ -224,129 +258,142 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
       else if (kWarp - 1 - tid < (vocab - head) % E) single = vocab - kWarp + tid;
     }
     // The teacher's entries.
-    float best = -INFINITY, size = 0.f;
-    if (live && soft) {
-      for (int k = tid; k < a.top_k; k += threads) {
-        const int64_t i = read_id(a.top_ids, row * a.ids_stride + k, a.ids64);
-        float t = 0.f;
-        by_type(a.top_type, [&](auto T) {
-          constexpr int TT = decltype(T)::value;
-          t = to_float<TT>(static_cast<const typename TypeOf<TT>::T*>(
-              a.top_logits)[row * a.top_stride + k]);
-        });
-        const bool valid = i >= 0 && i < vocab && t != -INFINITY;
-        id[k] = valid ? int32_t(i) : -1;
-        coef[k] = t;
-        if (!valid) continue;
-        zed[k] = to_float<ZT>(z[i]);
-        if (t > best) {
-          size = size * exp2_of((best - t) * ct) + 1.f;
-          best = t;
-        } else {
-          size += t == best && t < INFINITY ? 1.f : exp2_of((t - best) * ct);
-        }
+    float best = -INFINITY, size = 0.f, entry_z = 0.f;
+    const auto take = [&](int k, int64_t i, float t) {
+      const bool valid = i >= 0 && i < vocab && t != -INFINITY;
+      id[k] = valid ? int32_t(i) : -1;
+      coef[k] = t;
+      if (!valid) return false;
+      if (t > best) {
+        size = size * exp2_of((best - t) * ct) + 1.f;
+        best = t;
+      } else {
+        size += t == best && t < INFINITY ? 1.f : exp2_of((t - best) * ct);
+      }
+      return true;
+    };
+    if (live && has_entry) {
+      if (take(tid, entry, entry_t)) entry_z = to_float<ZT>(z[entry]);
+      for (int k = tid + threads; k < a.top_k; k += threads) {
+        int64_t i;
+        float t;
+        entry_of(row, k, i, t);
+        if (take(k, i, t)) zed[k] = to_float<ZT>(z[i]);
       }
     }
+    // The next row's, while this one is worked on.
+    if (has_entry && next < a.n_rows) entry_of(next, tid, entry, entry_t);
     float edge = -INFINITY;
     if (live && single >= 0) edge = to_float<ZT>(z[single]);
+    float label_z = 0.f;
     if (tid == 0) {
-      id[a.top_k] = live && hard ? int32_t(label) : -1;
-      zed[a.top_k] = live && hard ? to_float<ZT>(z[label]) : 0.f;
+      for (int k = a.top_k; k < room; ++k) id[k] = -1;
+      if (live && hard) id[a.top_k] = int32_t(label), label_z = to_float<ZT>(z[label]);
     }
     // The largest value and the sums.
-    Sums<TEMPS> sums;
+    Sums<TERMS> sums;
     if (live) {
       for (int part = 0; part < kParts; ++part) {
         if constexpr (GRAD) {
-          if (part == 0) copy_wait<3>();
-          else if (part == 1) copy_wait<2>();
-          else if (part == 2) copy_wait<1>();
+          if (part == 0) copy_wait<kParts - 1>();
           else copy_wait<0>();
         } else {
-          copy_wait<3>();
+          copy_wait<kParts - 1>();
         }
-        const int end = min(per_thread, (part + 1) * per_part);
-        for (int j = part * per_part; j < end; j += 2) {
-          Unit<ZT> x, y;
-          x.none(), y.none();
-          const int i = j * threads + tid;
-          if (i < mine) x.q = slot[i];
-          if (i + threads < mine) y.q = slot[i + threads];
-          sums.raise(fmaxf(sums.top, largest(x, y)), c);
+        const int first = first_of(part), end = min(mine, first + run);
+        for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
+          Unit<ZT> x[kAtOnce];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            x[k].none();
+            if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
+          }
+          sums.raise(fmaxf(sums.top, largest(x)), c);
           const F2 down = pair(-sums.top);
-          F2 t[TEMPS];
+          F2 t[N];
 #pragma unroll
-          for (int k = 0; k < TEMPS; ++k) t[k] = pair(sums.s[k], 0.f);
+          for (int n = 0; n < N; ++n) t[n] = pair(sums.s[n], 0.f);
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            const F2 d = add2(x.get(i), down), e = add2(y.get(i), down);
+          for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
-            for (int k = 0; k < TEMPS; ++k)
-              t[k] = add2(t[k], add2(exp2_of(mul2(d, pair(c[k]))), exp2_of(mul2(e, pair(c[k])))));
-          }
-#pragma unroll
-          for (int k = 0; k < TEMPS; ++k) sums.s[k] = sum2(t[k]);
-          if constexpr (!GRAD) {
-            if (next_live) {
-              copy(next_from, next_units, j);
-              if (j + 1 < end) copy(next_from, next_units, j + 1);
+            for (int h = 0; h < E / 2; ++h) {
+              const F2 d = add2(x[k].get(h), down);
+              const F2 e = exp2_of(mul2(d, pair(c[0])));
+              t[0] = add2(t[0], e);
+              if constexpr (TERMS == kTwo) t[1] = add2(t[1], exp2_of(mul2(d, pair(c[1]))));
+              if constexpr (TERMS == kSquares) t[1] = fma2(e, e, t[1]);
             }
-          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) sums.s[n] = sum2(t[n]);
         }
-        if constexpr (!GRAD) copy_commit();
+        if constexpr (!GRAD) copy_part(next_from, next_mine, part);
       }
       if (single >= 0) {
         sums.raise(fmaxf(sums.top, edge), c);
+        float f[N];
+        sums.factors(edge - sums.top, c, f);
 #pragma unroll
-        for (int k = 0; k < TEMPS; ++k) sums.s[k] += exp2_of((edge - sums.top) * c[k]);
+        for (int n = 0; n < N; ++n) sums.s[n] += f[n];
       }
     } else if (!GRAD) {
-      for (int part = 0; part < kParts; ++part) {
-        for (int j = part * per_part; next_live && j < min(per_thread, (part + 1) * per_part); ++j)
-          copy(next_from, next_units, j);
-        copy_commit();
-      }
+      for (int part = 0; part < kParts; ++part) copy_part(next_from, next_mine, part);
     }
     // Over the warps of the row's CTAs; the teacher's, which each CTA has, over its own.
-    const float warp_best = warp_max(best);
-    size = warp_sum(size == 0.f ? 0.f : best == warp_best ? size : size * exp2_of((best - warp_best) * ct));
-    if (live) sums.join_warp(c);
-    if (lane == 0) teacher[parity][warp] = make_float2(warp_best, size);
+    const auto join_teacher = [&](int lanes) {
+      float to = best;
+      for (int d = 1; d < lanes; d *= 2) to = fmaxf(to, __shfl_xor_sync(kAll, to, d));
+      if (best != to && size != 0.f) size *= exp2_of((best - to) * ct);
+      for (int d = 1; d < lanes; d *= 2) size += __shfl_xor_sync(kAll, size, d);
+      best = to;
+    };
+    if (live) sums.join(kWarp, c);
+    if (warp < entry_warps) {
+      if (has_entry) zed[tid] = entry_z;
+      join_teacher(kWarp);
+      if (lane == 0) teacher[parity][warp] = make_float2(best, size);
+    }
+    if (tid == 0) zed[a.top_k] = label_z;
     if (lane < a.ctas) {
       Part* to = &parts[parity][rank * warps + warp];
       if (a.ctas > 1) to = cluster.map_shared_rank(to, lane);
-      to->top = sums.top, to->s[0] = sums.s[0], to->s[1] = sums.s[TEMPS - 1];
+      to->top = sums.top, to->s[0] = sums.s[0], to->s[1] = sums.s[N - 1];
     }
     if (a.ctas > 1) cluster.sync();
     else __syncthreads();
-    best = lane < warps ? teacher[parity][lane].x : -INFINITY;
-    size = lane < warps ? teacher[parity][lane].y : 0.f;
-    const float all_best = warp_max(best);
-    size = warp_sum(size == 0.f ? 0.f : best == all_best ? size : size * exp2_of((best - all_best) * ct));
-    best = all_best;
+    if (soft) {
+      best = -INFINITY, size = 0.f;
+      if ((lane & (warps - 1)) < entry_warps) {
+        const float2 p = teacher[parity][lane & (warps - 1)];
+        best = p.x, size = p.y;
+      }
+      join_teacher(warps);
+    }
     const bool any = size != 0.f;  // NaN too
     const bool work = live && (any || hard);
     if (work) {
-      Sums<TEMPS> all;
-      for (int k = lane; k < a.ctas * warps; k += kWarp) {
-        const Part p = parts[parity][k];
-        const float to = fmaxf(all.top, p.top);
-        all.raise(to, c);
+      const int held = a.ctas * warps;  // a power of two
+      Part p = parts[parity][lane & (held - 1)];
+      sums.top = p.top, sums.s[0] = p.s[0], sums.s[N - 1] = p.s[N - 1];
+      for (int k = kWarp; k < held; k += kWarp) {
+        p = parts[parity][k + lane];
+        const float to = fmaxf(sums.top, p.top);
+        float f[N];
+        sums.raise(to, c);
+        sums.factors(p.top - to, c, f);
 #pragma unroll
-        for (int i = 0; i < TEMPS; ++i) all.s[i] += p.s[i] * exp2_of((p.top - to) * c[i]);
+        for (int n = 0; n < N; ++n) sums.s[n] += p.s[n] * f[n];
       }
-      all.join_warp(c);
-      sums = all;
+      sums.join(min(held, kWarp), c);
     }
     const float top = sums.top;
     // Nothing but -inf: no distribution.
-    if (sums.s[0] == 0.f) sums.s[0] = sums.s[TEMPS - 1] = NAN;
-    const float soft_sum = sums.s[0], hard_sum = sums.s[TEMPS - 1];
+    if (sums.s[0] == 0.f) sums.s[0] = sums.s[N - 1] = NAN;
+    const float soft_sum = sums.s[0], hard_sum = sums.s[N - 1];
     // The terms of the loss, and what each entry takes off the gradient.
-    float sum = 0.f;
-    if (work && any) {
+    if (warp < entry_warps && work && any) {
+      float sum = 0.f;
       const float log_size = logf(size), log_soft = logf(soft_sum), inv = 1.f / size;
-      const float weight = a.soft_weight * a.temperature;
+      const float weight = a.soft_weight * a.temperature * up;
       for (int k = tid; k < a.top_k; k += threads) {
         if (id[k] < 0) {
           coef[k] = 0.f;
@@ -356,23 +403,26 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
         const float p = exp2_of(d * ct) * inv;
         const float q = (zed[k] - top) * a.inv_temperature - log_soft;
         sum += zed[k] == -INFINITY ? INFINITY : p * (d * a.inv_temperature - log_size - q);
-        coef[k] = weight * p * up;
+        coef[k] = weight * p;
       }
-    } else if (GRAD && work) {
+      sum = warp_sum(sum);
+      if (lane == 0) terms[parity][warp] = sum;
+    } else if (GRAD && work && !any) {
       for (int k = tid; k < a.top_k; k += threads) id[k] = -1;
     }
     if (GRAD && tid == 0) coef[a.top_k] = a.hard_weight * up;
-    sum = warp_sum(sum);
-    if (lane == 0) terms[parity][warp] = sum;
     if constexpr (GRAD) {
       const bool zero = !work || up == 0.f;
-      float w[TEMPS];  // weights of the exponentials
-      w[0] = soft ? (any ? up * a.soft_weight * a.temperature / soft_sum : 0.f) : 0.f;
-      w[TEMPS - 1] = (TEMPS == 1 ? w[0] : 0.f) + (hard ? up * a.hard_weight / hard_sum : 0.f);
+      float w[N];  // weights of the exponentials
+      w[0] = soft && any ? up * a.soft_weight * a.temperature / soft_sum : 0.f;
+      w[N - 1] = (N == 1 ? w[0] : 0.f) + (hard ? up * a.hard_weight / hard_sum : 0.f);
       const auto smooth = [&](F2 v) {
         const F2 d = add2(v, pair(-top));
-        F2 g = mul2(exp2_of(mul2(d, pair(c[0]))), pair(w[0]));
-        if constexpr (TEMPS == 2) g = fma2(exp2_of(mul2(d, pair(c[1]))), pair(w[1]), g);
+        const F2 e = exp2_of(mul2(d, pair(c[0])));
+        if constexpr (TERMS == kSquares) return mul2(e, fma2(e, pair(w[1]), pair(w[0])));
+        const F2 g = mul2(e, pair(w[0]));
+        if constexpr (TERMS == kTwo)
+          return fma2(exp2_of(mul2(d, pair(c[1]))), pair(w[1]), g);
         return g;
       };
       const auto smooth1 = [&](float v) {
@@ -380,39 +430,42 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
         split(smooth(pair(v)), lo, hi);
         return lo;
       };
+      TG* to = grad + head + int64_t(at0) * E;
       if (a.whole) {
-        TG* to = grad + head + int64_t(rank) * a.slice * E;
         for (int part = 0; part < kParts; ++part) {
-          for (int j = part * per_part; j < min(per_thread, (part + 1) * per_part); ++j) {
-            const int i = j * threads + tid;
-            if (i < mine) {
-              Pack<GT, E> g;
-              g.clear();
-              if (!zero) {
-                Unit<ZT> x;
-                x.q = slot[i];
+          const int first = first_of(part), end = min(mine, first + run);
+          TG* out = to + (first + lane) * E;
+          if (zero) {
+            Pack<GT, E> g;
+            g.clear();
+            for (int i = first + lane; i < end; i += kWarp, out += kWarp * E) g.store(out);
+          } else {
+            constexpr int U = 2;
+            for (int i = first + lane; i < end; i += U * kWarp, out += U * kWarp * E) {
+              Unit<ZT> x[U];
 #pragma unroll
-                for (int k = 0; k < E / 2; ++k) set2(g, k, smooth(x.get(k)));
+              for (int k = 0; k < U; ++k) {
+                x[k].none();
+                if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
               }
-              g.store(to + int64_t(i) * E);
+#pragma unroll
+              for (int k = 0; k < U; ++k) {
+                Pack<GT, E> g;
+#pragma unroll
+                for (int h = 0; h < E / 2; ++h) set2(g, h, smooth(x[k].get(h)));
+                if (i + k * kWarp < end) g.store(out + k * (kWarp * E));
+              }
             }
-            if (next_live) copy(next_from, next_units, j);
           }
-          copy_commit();
+          copy_part(next_from, next_mine, part);
         }
       } else {
         // Element by element; the next row may come when all are through.
         const TZ* from = reinterpret_cast<const TZ*>(slot);
-        TG* to = grad + head + int64_t(rank) * a.slice * E;
         for (int i = tid; i < mine * E; i += threads)
           to[i] = zero ? TG(0) : from_float<GT>(smooth1(to_float<ZT>(from[i])));
         __syncthreads();
-        for (int part = 0; part < kParts; ++part) {
-          for (int j = part * per_part; next_live && j < min(per_thread, (part + 1) * per_part);
-               ++j)
-            copy(next_from, next_units, j);
-          copy_commit();
-        }
+        for (int part = 0; part < kParts; ++part) copy_part(next_from, next_mine, part);
       }
       if (single >= 0) grad[single] = zero ? TG(0) : from_float<GT>(smooth1(edge));
       __syncthreads();
@@ -424,8 +477,16 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
           const bool inside = token >= lo && token < hi;
           const bool end = rank == 0 && (token < head || token >= head + units * E);
           if (token < 0 || !(inside || end)) continue;
-          float off = 0.f;
-          for (int o = 0; o <= a.top_k; ++o) off += id[o] == token ? coef[o] : 0.f;
+          float off = coef[k];
+          int named = 0;
+          for (int o = 0; o < room; o += 4) {
+            const int4 i = *reinterpret_cast<const int4*>(id + o);
+            named += (i.x == token) + (i.y == token) + (i.z == token) + (i.w == token);
+          }
+          if (named > 1) {
+            off = 0.f;
+            for (int o = 0; o <= a.top_k; ++o) off += id[o] == token ? coef[o] : 0.f;
+          }
           grad[token] = from_float<GT>(smooth1(zed[k]) - off);
         }
       }
@@ -435,7 +496,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     if (a.loss && rank == 0 && tid == 0) {
       float loss = 0.f;
       if (work && any) {
-        for (int k = 0; k < warps; ++k) loss += terms[parity][k];
+        for (int k = 0; k < entry_warps; ++k) loss += terms[parity][k];
         // Without a distribution a masked token's term means nothing.
         if (soft_sum != soft_sum) loss = soft_sum;
         loss *= a.soft_weight * a.temperature * a.temperature;
@@ -449,18 +510,22 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   if (a.ctas > 1) cluster.sync();
 }
 
-// The kernels of one type of logits: [type of grad][temperatures - 1], and without grad.
+// The kernels of one type of logits: [type of grad][terms], and without grad.
 using DistillKernel = void (*)(DistillArgs);
 struct DistillKernels {
-  DistillKernel grad[3][2];
-  DistillKernel loss[2];
+  DistillKernel grad[3][3];
+  DistillKernel loss[3];
 };
 template <int ZT>
 constexpr DistillKernels distill_kernels() {
-  return {{{distill_kernel<ZT, TRAIN_BF16, 1, true>, distill_kernel<ZT, TRAIN_BF16, 2, true>},
-           {distill_kernel<ZT, TRAIN_FP16, 1, true>, distill_kernel<ZT, TRAIN_FP16, 2, true>},
-           {distill_kernel<ZT, TRAIN_FP32, 1, true>, distill_kernel<ZT, TRAIN_FP32, 2, true>}},
-          {distill_kernel<ZT, TRAIN_FP32, 1, false>, distill_kernel<ZT, TRAIN_FP32, 2, false>}};
+  return {{{distill_kernel<ZT, TRAIN_BF16, kOne, true>, distill_kernel<ZT, TRAIN_BF16, kTwo, true>,
+            distill_kernel<ZT, TRAIN_BF16, kSquares, true>},
+           {distill_kernel<ZT, TRAIN_FP16, kOne, true>, distill_kernel<ZT, TRAIN_FP16, kTwo, true>,
+            distill_kernel<ZT, TRAIN_FP16, kSquares, true>},
+           {distill_kernel<ZT, TRAIN_FP32, kOne, true>, distill_kernel<ZT, TRAIN_FP32, kTwo, true>,
+            distill_kernel<ZT, TRAIN_FP32, kSquares, true>}},
+          {distill_kernel<ZT, TRAIN_FP32, kOne, false>, distill_kernel<ZT, TRAIN_FP32, kTwo, false>,
+           distill_kernel<ZT, TRAIN_FP32, kSquares, false>}};
 }
 
 // Each defined in a translation unit of its own.
