@@ -22,11 +22,13 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["lamb_kernels.cu", "lamb_api.cpp", "lamb_plan.cpp", "lamb_noalloc.cu",
            "lamb_ptrs.cu", "train_embed.cu", "train_embed_grad.cu", "train_clip.cu",
            "train_norm.cu", "train_norm_bf16.cu", "train_norm_fp16.cu", "train_norm_fp32.cu",
-           "train_norm_grad.cu", "train_distill.cu", "train_distill_bf16.cu",
+           "train_norm_grad.cu", "train_norm_grad_bf16.cu", "train_norm_grad_fp16.cu",
+           "train_norm_grad_fp32.cu", "train_distill.cu", "train_distill_bf16.cu",
            "train_distill_fp16.cu", "train_distill_fp32.cu"]
 HEADERS = [os.path.join(INCLUDE, "lamb.h"), os.path.join(INCLUDE, "train_ops.h"),
            os.path.join(CSRC, "lamb_internal.h"), os.path.join(CSRC, "train_internal.h"),
            os.path.join(CSRC, "train_norm.h"), os.path.join(CSRC, "train_norm_rows.h"),
+           os.path.join(CSRC, "train_norm_grad_rows.h"),
            os.path.join(CSRC, "train_distill_rows.h")]
 
 

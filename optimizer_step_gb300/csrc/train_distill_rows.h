@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
-        if (i + k * kWarp < end) copy_async16(to + k * kWarp, from + k * (kWarp * E));
+        if (i + k * kWarp < end) copy_async(to + k * kWarp, from + k * (kWarp * E));
       to += kAtOnce * kWarp, from += kAtOnce * kWarp * E;
     }
     copy_commit();

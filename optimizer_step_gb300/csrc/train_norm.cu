@@ -100,7 +100,7 @@ cudaError_t launch_rows(NormArgs& a, int32_t x_dtype, int32_t y_dtype, cudaStrea
   };
   const auto go = [&](NormKernel kernel, int64_t ctas, int threads, int64_t smem) {
     *done = true;
-    if (smem > 48 * 1024) {
+    if (smem > 40 * 1024) {
       const cudaError_t ce =
           cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));

@@ -77,15 +77,38 @@ struct Group {
   __device__ __forceinline__ float sum(float x, int slot) const {
     return join<S>(x, slot, 0.f, [](float a, float b) { return a + b; });
   }
+  // Two sums at once.
+  template <Span S>
+  __device__ __forceinline__ void sums(float& x, float& y, int slot) const {
+    if constexpr (S == Span::kPart) {
+      for (int d = 1; d < lanes; d *= 2)
+        x += __shfl_xor_sync(kAll, x, d), y += __shfl_xor_sync(kAll, y, d);
+      return;
+    }
+    x = warp_sum(x), y = warp_sum(y);
+    if constexpr (S == Span::kWarps) {
+      float* p = part + 2 * slot * traingb::kWarp;
+      if ((lane & 31) == 0) p[lane >> 5] = x, p[traingb::kWarp + (lane >> 5)] = y;
+      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(lanes) : "memory");
+      const bool held = (lane & 31) < lanes / traingb::kWarp;
+      x = warp_sum(held ? p[lane & 31] : 0.f);
+      y = warp_sum(held ? p[traingb::kWarp + (lane & 31)] : 0.f);
+    }
+  }
   template <Span S>
   __device__ __forceinline__ float largest(float x, int slot) const {
     return join<S>(x, slot, -INFINITY, [](float a, float b) { return fmaxf(a, b); });
   }
 };
 
-__device__ __forceinline__ void copy_async16(void* to, const void* from) {
+template <int BYTES = 16>
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  static_assert(BYTES == 8 || BYTES == 16, "");
   const uint32_t t = uint32_t(__cvta_generic_to_shared(to));
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(t), "l"(from) : "memory");
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(t), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(t), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

@@ -1,27 +1,15 @@
 // Layer norm's backward pass (train_ops.h).
-#include "train_norm.h"
+#include "train_norm_grad_rows.h"
 
 using namespace traingb;
 
 namespace {
 
-struct GradArgs {
-  const void* dy;
-  const void* x;
-  const void* weight;
-  const float* stats;
-  void* dx;
-  float* partial;  // [pieces][2][dim]: of the weight's and the bias's gradient
-  int64_t n_rows, dim, dy_stride, x_stride, dx_stride;
-  int64_t rows_per_piece;
-  int32_t dy_type, x_type, param_type;
-};
-
 // ------------------------------------------------------------ rows of any width
 constexpr int kWideThreads = 512;
 
 // dx, one CTA a row.
-__global__ void __launch_bounds__(kWideThreads) wide_dx_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kWideThreads) wide_dx_kernel(const NormGradArgs a) {
   __shared__ float part[2][kWideThreads / kWarp];
   pdl_wait();
   const int64_t row = blockIdx.x;
@@ -59,7 +47,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_dx_kernel(const GradArgs a)
 
 // Partial sums over rows_per_piece rows, a CTA for 32 columns.
 constexpr int kSlabWarps = 8;
-__global__ void __launch_bounds__(kSlabWarps* kWarp) wide_partial_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kSlabWarps* kWarp) wide_partial_kernel(const NormGradArgs a) {
   __shared__ float part[2][kSlabWarps][kWarp];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -130,16 +118,87 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const JoinArgs 
 }
 
 // ------------------------------------------------------------------------- plan
-struct Plan {
-  int64_t pieces, rows_per_piece;
-};
+constexpr int kSms = 152;
+constexpr int kMostPieces = 256;
+constexpr int kMostLanes = 512;  // threads a CTA
+constexpr int64_t kMostShared = 224 * 1024;  // a CTA's dynamic shared memory
 
-Plan plan(int64_t n_rows, int64_t dim) {
-  Plan p{};
-  if (n_rows == 0) return p;
-  p.rows_per_piece = std::max<int64_t>(64, (n_rows + 255) / 256);
-  p.pieces = (n_rows + p.rows_per_piece - 1) / p.rows_per_piece;
-  return p;
+// Pieces that any of the kernels below may write.
+int64_t most_pieces(int64_t n_rows) {
+  return n_rows == 0 ? 0 : std::min<int64_t>(kMostPieces, n_rows);
+}
+
+// Launches the kernel for rows that stay on chip, if there is one; sets `pieces`.
+cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
+  *pieces = 0;
+  const int64_t dim = a.dim;
+  const NormGradKernels& k = a.x_type == TRAIN_BF16   ? norm_grad_kernels_bf16(a.dy_type)
+                             : a.x_type == TRAIN_FP16 ? norm_grad_kernels_fp16(a.dy_type)
+                                                      : norm_grad_kernels_fp32(a.dy_type);
+  const int64_t e = a.x_type == TRAIN_FP32 || a.dy_type == TRAIN_FP32 ? 4 : 8;
+  const auto phase = [&](const void* p, int32_t type) {
+    return int64_t(reinterpret_cast<uintptr_t>(p) / uintptr_t(size_of(type))) % e;
+  };
+  const auto go = [&](NormGradKernel kernel, int64_t ctas, int64_t groups, int64_t smem) {
+    // A CTA for each row that begins differently, but none without rows.
+    ctas = std::min((ctas + a.period - 1) / a.period * a.period, a.n_rows);
+    if (ctas < a.period) ctas = std::min<int64_t>(a.n_rows, a.period);
+    else ctas = ctas / a.period * a.period;
+    smem = std::max(smem, groups * 2 * dim * 4);
+    *pieces = ctas;
+    if (smem > 40 * 1024) {
+      const cudaError_t ce =
+          cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+      if (ce != cudaSuccess) return ce;
+    }
+    return launch(kernel, dim3(unsigned(ctas)), int(groups * a.lanes), size_t(smem), stream, true,
+                  1, a);
+  };
+  a.period = 1;
+  const int64_t px = phase(a.x, a.x_type), row = a.x_stride % e;
+  const bool alike = px == phase(a.dy, a.dy_type) && row == a.dy_stride % e &&
+                     (!a.dx || (px == phase(a.dx, a.x_type) && row == a.dx_stride % e));
+  const bool whole = alike && px == 0 && row == 0 && dim % e == 0;
+  if (alike && (whole || dim >= 256)) {
+    a.phase = int32_t(px), a.row_phase = int32_t(row);
+    while (a.period * row % e != 0) a.period *= 2;
+    const int64_t units = dim / e;
+    int shape = 0;
+    int64_t m = 1;  // units a thread
+    if (units < kWarp && whole) {
+      a.lanes = 1;
+      while (a.lanes < units) a.lanes *= 2;
+    } else {
+      m = (units * e <= 8 * kWarp ? 8 : units * e <= 16 * kMostLanes ? 16 : 24) / e;
+      a.lanes = int32_t((units + m * kWarp - 1) / (m * kWarp)) * kWarp;
+      shape = a.lanes > kWarp ? 1 + m * e / 8 : m * e / 8;
+    }
+    if (a.lanes <= kMostLanes) {
+      const int64_t stage = m * e * a.lanes * (size_of(a.x_type) + size_of(a.dy_type));
+      int64_t groups = std::min<int64_t>(kMostLanes / a.lanes, a.lanes > kWarp ? 15 : kMostLanes);
+      // Few rows: CTAs of a few rounds each rather than many pieces.
+      const int64_t fill = kWarp / std::min<int64_t>(a.lanes, kWarp);  // groups a warp
+      groups = std::min(groups, ((a.n_rows + kSms - 1) / kSms + fill - 1) / fill * fill);
+      while (groups > fill && groups * std::max(2 * stage, 8 * dim) > kMostShared) groups -= fill;
+      if (groups * std::max(2 * stage, 8 * dim) <= kMostShared) {
+        a.stages = int32_t(std::min<int64_t>(4, kMostShared / (groups * stage)));
+        return go(k.ring[shape], std::min<int64_t>(kSms, (a.n_rows + groups - 1) / groups), groups,
+                  a.stages * groups * stage);
+      }
+    }
+    a.period = 1;
+  }
+  // Element by element.
+  const int s = dim <= kGradScalars[0] * kWarp ? 0 : 1;
+  const int64_t span = kGradScalars[s] * kWarp;
+  a.lanes = int32_t((dim + span - 1) / span) * kWarp;
+  if (a.lanes > 512 || dim * 8 > kMostShared) return cudaSuccess;
+  int64_t groups = std::max<int64_t>(1, std::min<int64_t>(512 / a.lanes, a.lanes > kWarp ? 15 : 16));
+  groups = std::min(groups, (a.n_rows + kSms - 1) / kSms);
+  while (groups > 1 && groups * dim * 8 > kMostShared) --groups;
+  return go(k.scalar[a.lanes > kWarp ? 2 : s],
+            std::min<int64_t>(kSms, (a.n_rows + groups - 1) / groups), groups, 0);
 }
 
 constexpr int64_t kMaxElements = int64_t(1) << 40;
@@ -160,7 +219,7 @@ LAMB_API int train_layer_norm_grad_workspace(int64_t n_rows, int64_t dim, int64_
   if (!bytes) return fail(LAMB_ERR_INVALID, "bytes is NULL");
   const int rc = check_sizes(n_rows, dim);
   if (rc != LAMB_OK) return rc;
-  *bytes = plan(n_rows, dim).pieces * 2 * dim * 4;
+  *bytes = most_pieces(n_rows) * 2 * dim * 4;
   return LAMB_OK;
 }
 
@@ -186,33 +245,39 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
     return fail(LAMB_ERR_INVALID, "accumulate must be 0 or 1");
   if (n_rows > 0 && !stats) return fail(LAMB_ERR_INVALID, "stats is NULL");
   const bool params = weight_grad || bias_grad;
-  const Plan p = plan(n_rows, dim);
-  if (params && p.pieces > 0) {
-    if (!workspace || workspace_bytes < p.pieces * 2 * dim * 4)
+  if (params && n_rows > 0) {
+    if (!workspace || workspace_bytes < most_pieces(n_rows) * 2 * dim * 4)
       return fail(LAMB_ERR_INVALID, "workspace is missing or too small");
     if (reinterpret_cast<uintptr_t>(workspace) % 16)
       return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
   }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  GradArgs a{};
+  NormGradArgs a{};
   a.dy = grad_out, a.x = x, a.weight = weight, a.stats = stats, a.dx = x_grad;
-  a.partial = static_cast<float*>(workspace);
+  a.partial = params ? static_cast<float*>(workspace) : nullptr;
   a.n_rows = n_rows, a.dim = dim;
   a.dy_stride = grad_out_stride, a.x_stride = x_stride, a.dx_stride = x_grad_stride;
-  a.rows_per_piece = p.rows_per_piece;
   a.dy_type = grad_out_dtype, a.x_type = x_dtype, a.param_type = weight_dtype;
   cudaError_t ce = cudaSuccess;
-  // The sums first: dx may take the place of grad_out.
-  if (params && n_rows > 0)
-    ce = launch(wide_partial_kernel,
-                dim3(unsigned((dim + kWarp - 1) / kWarp), unsigned(p.pieces)),
-                kSlabWarps * kWarp, 0, st, true, 1, a);
-  if (ce == cudaSuccess && x_grad && n_rows > 0)
-    ce = launch(wide_dx_kernel, dim3(unsigned(n_rows)), kWideThreads, 0, st, true, 1, a);
+  int64_t pieces = 0;
+  if (n_rows > 0 && (params || x_grad)) {
+    ce = launch_rows(a, st, &pieces);
+    if (ce == cudaSuccess && pieces == 0) {
+      a.rows_per_piece = std::max<int64_t>(64, (n_rows + kMostPieces - 1) / kMostPieces);
+      pieces = (n_rows + a.rows_per_piece - 1) / a.rows_per_piece;
+      // The sums first: dx may take the place of grad_out.
+      if (params)
+        ce = launch(wide_partial_kernel,
+                    dim3(unsigned((dim + kWarp - 1) / kWarp), unsigned(pieces)),
+                    kSlabWarps * kWarp, 0, st, true, 1, a);
+      if (ce == cudaSuccess && x_grad)
+        ce = launch(wide_dx_kernel, dim3(unsigned(n_rows)), kWideThreads, 0, st, true, 1, a);
+    }
+  }
   if (ce == cudaSuccess && params && !(n_rows == 0 && accumulate)) {
     JoinArgs j{};
     j.partial = a.partial, j.weight_grad = weight_grad, j.bias_grad = bias_grad;
-    j.dim = dim, j.pieces = p.pieces;
+    j.dim = dim, j.pieces = pieces;
     j.type = param_grad_dtype, j.accumulate = accumulate;
     ce = launch(join_kernel, dim3(unsigned((dim + kWarp - 1) / kWarp)), kJoinWarps * kWarp, 0,
                 st, true, 1, j);

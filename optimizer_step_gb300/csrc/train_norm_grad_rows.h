@@ -1,0 +1,304 @@
+// Layer norm's backward pass for rows that stay on chip (train_ops.h): the kernels,
+// compiled once for each type of x.  Not part of the public interface.
+#pragma once
+
+#include "train_norm.h"
+
+namespace traingb {
+
+struct NormGradArgs {
+  const void* dy;
+  const void* x;
+  const void* weight;
+  const float* stats;
+  void* dx;        // NULL: not wanted
+  float* partial;  // [pieces][2][dim]: of the weight's and the bias's gradient; NULL too
+  int64_t n_rows, dim, dy_stride, x_stride, dx_stride;
+  int64_t rows_per_piece;
+  int32_t dy_type, x_type, param_type;
+  // Of rows on chip.
+  int32_t lanes;             // threads a row
+  int32_t period;            // rows this far apart begin equally far from a unit's boundary
+  int32_t phase, row_phase;  // elements from one to the first row; from row to row
+  int32_t stages;            // of the ring
+};
+
+// The weight's element at a column, or 1.
+template <int N, class At>
+__device__ __forceinline__ void load_weight(const NormGradArgs& a, float (&w)[N], At&& at) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = 1.f;
+  if (!a.weight) return;
+  by_type(a.param_type, [&](auto P) {
+    constexpr int PT = decltype(P)::value;
+    const auto* p = static_cast<const typename TypeOf<PT>::T*>(a.weight);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int column = at(i);
+      if (column >= 0) w[i] = to_float<PT>(p[column]);
+    }
+  });
+}
+
+// Adds up the groups' sums, each at [group][2][dim] in `sums`, for this CTA's piece.
+__device__ __forceinline__ void write_piece(const NormGradArgs& a, const float* sums, int groups) {
+  const int n = 2 * int(a.dim);
+  float* to = a.partial + int64_t(blockIdx.x) * n;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    float s = sums[i];
+    for (int k = 1; k < groups; ++k) s += sums[int64_t(k) * n + i];
+    to[i] = s;
+  }
+}
+
+// Rows come through a ring of asynchronous copies as in the forward pass: units of E
+// elements of x and grad_out, M of each a thread.  A thread keeps the weight and the
+// sums over the rows for its columns in registers, which leaves no room for the row's
+// elements: they are read from the ring once for the two sums along the row and the
+// sums down the columns, and again for x_grad.  At the end the CTA's groups are added
+// and written as one piece; join_kernel adds the pieces.
+template <int XT, int YT, int M, Span S>
+__global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ NormGradArgs a) {
+  using TX = typename TypeOf<XT>::T;
+  using TY = typename TypeOf<YT>::T;
+  constexpr int E = XT == TRAIN_FP32 || YT == TRAIN_FP32 ? 4 : 8;
+  constexpr int C = M * E / 2;  // pairs a thread
+  constexpr int BX = E * int(sizeof(TX)), BY = E * int(sizeof(TY));
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part[4 * kWarp];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  const int lanes = S == Span::kWarp ? kWarp : a.lanes;
+  const int groups = threads / lanes, index = tid / lanes;
+  const Group g{lanes, tid - index * lanes, index + 1, part + index * (lanes / kWarp)};
+  const int dim = int(a.dim);
+  unsigned char* ring_x = smem;
+  unsigned char* ring_y = smem + size_t(a.stages) * M * threads * BX;
+  const int turn = int(blockIdx.x) % a.period;
+  const int head = S == Span::kPart ? 0 : (E - (a.phase + turn * a.row_phase) % E) % E;
+  const int units = (dim - head) / E;
+  // This thread's units: `first` and every 32nd behind it (one where less than a warp
+  // has the row).
+  const int first = S == Span::kPart ? g.lane
+                                     : (g.lane >> 5) * (kWarp * M) + (g.lane & 31);
+  const int left = units - first;
+  // The column of its single element, if it has one.
+  int single = -1;
+  if (S != Span::kPart) {
+    if (g.lane < head) single = g.lane;
+    else if (g.lane < kWarp && kWarp - 1 - g.lane < (dim - head) % E)
+      single = dim - kWarp + g.lane;
+  }
+
+  pdl_wait();
+  const int64_t step = int64_t(max(1, int(gridDim.x) / a.period) * groups) * a.period;
+  int64_t row = int64_t(int(blockIdx.x) / a.period * groups + index) * a.period + turn;
+  const int64_t at = head + int64_t(first) * E;
+  const TX* next_x = static_cast<const TX*>(a.x) + row * a.x_stride + at;
+  const TY* next_y = static_cast<const TY*>(a.dy) + row * a.dy_stride + at;
+  int64_t next_row = row;
+  int in = 0, out = 0;
+  const auto copy = [&] {
+    if (next_row < a.n_rows) {
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        if (m * kWarp < left) {
+          copy_async<BX>(ring_x + size_t((in * M + m) * threads + tid) * BX,
+                         next_x + m * (kWarp * E));
+          copy_async<BY>(ring_y + size_t((in * M + m) * threads + tid) * BY,
+                         next_y + m * (kWarp * E));
+        }
+    }
+    copy_commit();
+    next_x += step * a.x_stride, next_y += step * a.dy_stride, next_row += step;
+    in = in + 1 == a.stages ? 0 : in + 1;
+  };
+  for (int k = 1; k < a.stages; ++k) copy();
+  // What a row has besides: its stats and this thread's single elements.
+  float mean = 0.f, rstd = 0.f, xe = 0.f, ye = 0.f;
+  const auto look = [&](int64_t r) {
+    if (r >= a.n_rows) return;
+    mean = a.stats[r], rstd = a.stats[a.n_rows + r];
+    if (single >= 0) {
+      xe = to_float<XT>(static_cast<const TX*>(a.x)[r * a.x_stride + single]);
+      ye = to_float<YT>(static_cast<const TY*>(a.dy)[r * a.dy_stride + single]);
+    }
+  };
+  look(row);
+  float wf[2 * C], we[1];
+  load_weight(a, wf, [&](int i) {
+    return i / E * kWarp < left ? int(at) + i / E * (kWarp * E) + i % E : -1;
+  });
+  load_weight(a, we, [&](int) { return single; });
+  F2 w[C], dw[C], db[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) w[c] = pair(wf[2 * c], wf[2 * c + 1]), dw[c] = db[c] = pair(0.f);
+  float dwe = 0.f, dbe = 0.f;
+  const float inv = 1.f / float(dim);
+  int parity = 0;
+  const int64_t rounds = row < a.n_rows ? (a.n_rows - row + step - 1) / step : 0;
+  // Where groups share a warp, the warp's first has the most rows.
+  const int64_t turns = S == Span::kPart ? __shfl_sync(kAll, rounds, 0) : rounds;
+  for (int64_t k = 0; k < turns; ++k, row += step) {
+    const bool held = S != Span::kPart || row < a.n_rows;
+    copy();
+    const float shift1 = -mean, scale1 = rstd;
+    const float xs = (xe - mean) * rstd, ys = ye;
+    look(row + step);
+    if (a.stages == 4) copy_wait<3>();
+    else if (a.stages == 3) copy_wait<2>();
+    else copy_wait<1>();
+    const F2 shift = pair(shift1), scale = pair(scale1);
+    const auto unit = [&](int m, Pack<XT, E>& x, Pack<YT, E>& y) {
+      const unsigned char* p = ring_x + size_t((out * M + m) * threads + tid) * BX;
+      const unsigned char* q = ring_y + size_t((out * M + m) * threads + tid) * BY;
+      x.load_kept(reinterpret_cast<const TX*>(p));
+      y.load_kept(reinterpret_cast<const TY*>(q));
+    };
+    F2 along1 = pair(0.f), alongx = pair(0.f);
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      if (m * kWarp >= left || !held) continue;
+      Pack<XT, E> x;
+      Pack<YT, E> y;
+      unit(m, x, y);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        const int c = m * (E / 2) + i;
+        const F2 d = mul2(add2(get2(x, i), shift), scale), v = get2(y, i), gw = mul2(v, w[c]);
+        along1 = add2(along1, gw);
+        alongx = fma2(gw, d, alongx);
+        db[c] = add2(db[c], v);
+        dw[c] = fma2(v, d, dw[c]);
+      }
+    }
+    float s = sum2(along1), t = sum2(alongx);
+    if (single >= 0) {
+      s += ys * we[0], t += ys * we[0] * xs;
+      dbe += ys, dwe += ys * xs;
+    }
+    if (a.dx) {
+      g.sums<S>(s, t, parity);
+      parity ^= 1;
+      s *= inv, t *= inv;
+      const F2 minus1 = pair(-s), minusx = pair(-t);
+      TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride;
+      asm volatile("" ::: "memory");  // read again, not kept
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        if (m * kWarp >= left || !held) continue;
+        Pack<XT, E> x, o;
+        Pack<YT, E> y;
+        unit(m, x, y);
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+          const F2 d = mul2(add2(get2(x, i), shift), scale);
+          const F2 gw = mul2(get2(y, i), w[m * (E / 2) + i]);
+          set2(o, i, mul2(fma2(d, minusx, add2(gw, minus1)), scale));
+        }
+        o.store(to + at + m * (kWarp * E));
+      }
+      if (single >= 0)
+        to[single] = from_float<XT>(scale1 * (ys * we[0] - s - xs * t));
+    }
+    out = out + 1 == a.stages ? 0 : out + 1;
+  }
+  if (!a.partial) return;
+  pdl_trigger();
+  // The ring's memory is free when all groups are through.
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(smem) + int64_t(index) * 2 * dim;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int m = 2 * c / E;
+    if (m * kWarp >= left) continue;
+    const int column = int(at) + m * (kWarp * E) + 2 * c % E;
+    split(dw[c], sums[column], sums[column + 1]);
+    split(db[c], sums[dim + column], sums[dim + column + 1]);
+  }
+  if (single >= 0) sums[single] = dwe, sums[dim + single] = dbe;
+  write_piece(a, reinterpret_cast<const float*>(smem), groups);
+}
+
+// Element by element, M a thread, straight from memory: for rows of x, grad_out and
+// x_grad that do not begin equally far from a unit's boundary, and short odd ones.
+template <int XT, int YT, int M, Span S>
+__global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant__ NormGradArgs a) {
+  using TX = typename TypeOf<XT>::T;
+  using TY = typename TypeOf<YT>::T;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ float part[4 * kWarp];
+  const int tid = threadIdx.x;
+  const int lanes = S == Span::kWarp ? kWarp : a.lanes;
+  const int groups = int(blockDim.x) / lanes, index = tid / lanes;
+  const Group g{lanes, tid - index * lanes, index + 1, part + index * (lanes / kWarp)};
+  const int dim = int(a.dim);
+  const int first = (g.lane >> 5) * (kWarp * M) + (g.lane & 31);
+  const int left = dim - first;
+  pdl_wait();
+  float w[M], dw[M] = {}, db[M] = {};
+  load_weight(a, w, [&](int i) { return i * kWarp < left ? first + i * kWarp : -1; });
+  const float inv = 1.f / float(dim);
+  const int64_t step = int64_t(gridDim.x) * groups;
+  int parity = 0;
+  for (int64_t row = int64_t(blockIdx.x) * groups + index; row < a.n_rows; row += step) {
+    const float mean = a.stats[row], rstd = a.stats[a.n_rows + row];
+    const TX* px = static_cast<const TX*>(a.x) + row * a.x_stride + first;
+    const TY* py = static_cast<const TY*>(a.dy) + row * a.dy_stride + first;
+    float x[M], y[M], s = 0.f, t = 0.f;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      x[m] = y[m] = 0.f;
+      if (m * kWarp < left) x[m] = to_float<XT>(px[m * kWarp]), y[m] = to_float<YT>(py[m * kWarp]);
+    }
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      x[m] = m * kWarp < left ? (x[m] - mean) * rstd : 0.f;
+      db[m] += y[m], dw[m] += y[m] * x[m];
+      y[m] *= w[m];
+      s += y[m], t += y[m] * x[m];
+    }
+    if (a.dx) {
+      g.sums<S>(s, t, parity);
+      parity ^= 1;
+      s *= inv, t *= inv;
+      TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride + first;
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        if (m * kWarp < left) to[m * kWarp] = from_float<XT>(rstd * (y[m] - s - x[m] * t));
+    }
+  }
+  if (!a.partial) return;
+  pdl_trigger();
+  float* sums = reinterpret_cast<float*>(smem) + int64_t(index) * 2 * dim + first;
+#pragma unroll
+  for (int m = 0; m < M; ++m)
+    if (m * kWarp < left) sums[m * kWarp] = dw[m], sums[dim + m * kWarp] = db[m];
+  write_piece(a, reinterpret_cast<const float*>(smem), groups);
+}
+
+// The kernels of two types.
+using NormGradKernel = void (*)(NormGradArgs);
+constexpr int kGradScalars[2] = {8, 16};  // elements a thread
+struct NormGradKernels {
+  // Part of a warp or a warp with 8 elements a thread, a warp with 16, several with 16 or 24.
+  NormGradKernel ring[5];
+  NormGradKernel scalar[3];  // a warp with 8 or 16 elements a thread, several with 16
+};
+template <int XT, int YT>
+constexpr NormGradKernels norm_grad_kernels() {
+  constexpr int M = XT == TRAIN_FP32 || YT == TRAIN_FP32 ? 2 : 1;  // units of 8 elements
+  return {{grad_ring_kernel<XT, YT, 1, Span::kPart>, grad_ring_kernel<XT, YT, M, Span::kWarp>,
+           grad_ring_kernel<XT, YT, 2 * M, Span::kWarp>,
+           grad_ring_kernel<XT, YT, 2 * M, Span::kWarps>,
+           grad_ring_kernel<XT, YT, 3 * M, Span::kWarps>},
+          {grad_scalar_kernel<XT, YT, 8, Span::kWarp>, grad_scalar_kernel<XT, YT, 16, Span::kWarp>,
+           grad_scalar_kernel<XT, YT, 16, Span::kWarps>}};
+}
+
+// Each defined in a translation unit of its own.
+const NormGradKernels& norm_grad_kernels_bf16(int y_type);
+const NormGradKernels& norm_grad_kernels_fp16(int y_type);
+const NormGradKernels& norm_grad_kernels_fp32(int y_type);
+
+}  // namespace traingb

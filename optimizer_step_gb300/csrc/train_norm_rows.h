@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
 #pragma unroll
       for (int m = 0; m < M; ++m)
         if (m * kWarp < left)
-          copy_async16(ring + (in * M + m) * threads + tid, p + m * (kWarp * E));
+          copy_async(ring + (in * M + m) * threads + tid, p + m * (kWarp * E));
     }
     copy_commit();
     next += step * a.x_stride, next_row += step;
