@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   const int vocab = a.vocab, room = (a.top_k + 4) / 4 * 4;
   const int rank = a.ctas == 1 ? 0 : int(blockIdx.x) % a.ctas;
   uint4* slot = reinterpret_cast<uint4*>(smem);
+  const uint32_t slot_address = shared_address(smem);
   unsigned char* lists = smem + size_t(a.slice) * 16;
 
   const bool soft = a.top_k > 0 && a.soft_weight != 0.f;
@@ -197,13 +198,13 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   const auto mine_of = [&](int units) { return min(a.slice, units - at0); };
   const auto copy_part = [&](const TZ* from, int mine, int part) {
     const int first = first_of(part), end = min(mine, first + run);
-    uint4* to = slot + first + lane;
+    uint32_t to = slot_address + (first + lane) * 16;
     from += (first + lane) * E;
     for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
-        if (i + k * kWarp < end) copy_async(to + k * kWarp, from + k * (kWarp * E));
-      to += kAtOnce * kWarp, from += kAtOnce * kWarp * E;
+        if (i + k * kWarp < end) copy_async<16>(to + k * (kWarp * 16), from + k * (kWarp * E));
+      to += kAtOnce * kWarp * 16, from += kAtOnce * kWarp * E;
     }
     copy_commit();
   };

@@ -77,7 +77,8 @@ struct Group {
   __device__ __forceinline__ float sum(float x, int slot) const {
     return join<S>(x, slot, 0.f, [](float a, float b) { return a + b; });
   }
-  // Two sums at once.
+  // Two sums at once, of at most 16 warps: after the first step half of the lanes carry
+  // one and half the other.
   template <Span S>
   __device__ __forceinline__ void sums(float& x, float& y, int slot) const {
     if constexpr (S == Span::kPart) {
@@ -85,15 +86,21 @@ struct Group {
         x += __shfl_xor_sync(kAll, x, d), y += __shfl_xor_sync(kAll, y, d);
       return;
     }
-    x = warp_sum(x), y = warp_sum(y);
+    const bool upper = lane & 16;
+    float v = upper ? y : x;
+    v += __shfl_xor_sync(kAll, upper ? x : y, 16);
+#pragma unroll
+    for (int d = 8; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
     if constexpr (S == Span::kWarps) {
-      float* p = part + 2 * slot * traingb::kWarp;
-      if ((lane & 31) == 0) p[lane >> 5] = x, p[traingb::kWarp + (lane >> 5)] = y;
+      float* p = part + 2 * slot * traingb::kWarp + (upper ? traingb::kWarp : 0);
+      if ((lane & 15) == 0) p[lane >> 5] = v;
       asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(lanes) : "memory");
-      const bool held = (lane & 31) < lanes / traingb::kWarp;
-      x = warp_sum(held ? p[lane & 31] : 0.f);
-      y = warp_sum(held ? p[traingb::kWarp + (lane & 31)] : 0.f);
+      v = (lane & 15) < lanes / traingb::kWarp ? p[lane & 15] : 0.f;
+#pragma unroll
+      for (int d = 8; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
     }
+    const float w = __shfl_xor_sync(kAll, v, 16);
+    x = upper ? w : v, y = upper ? v : w;
   }
   template <Span S>
   __device__ __forceinline__ float largest(float x, int slot) const {
@@ -101,14 +108,32 @@ struct Group {
   }
 };
 
-template <int BYTES = 16>
-__device__ __forceinline__ void copy_async(void* to, const void* from) {
+__device__ __forceinline__ uint32_t shared_address(const void* p) {
+  return uint32_t(__cvta_generic_to_shared(p));
+}
+// BYTES from global to shared memory, both aligned to them.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from) {
   static_assert(BYTES == 8 || BYTES == 16, "");
-  const uint32_t t = uint32_t(__cvta_generic_to_shared(to));
   if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(t), "l"(from) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(t), "l"(from) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(to), "l"(from) : "memory");
+}
+template <int DT, int VEC>
+__device__ __forceinline__ void load_shared(Pack<DT, VEC>& p, uint32_t from) {
+  constexpr int B = Pack<DT, VEC>::kBytes;
+  static_assert(B == 8 || B == 16, "");
+  if constexpr (B == 16)
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(p.w[0]), "=r"(p.w[1]), "=r"(p.w[2]), "=r"(p.w[3])
+                 : "r"(from)
+                 : "memory");
+  else
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                 : "=r"(p.w[0]), "=r"(p.w[1])
+                 : "r"(from)
+                 : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

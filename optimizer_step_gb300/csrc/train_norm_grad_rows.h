@@ -72,8 +72,12 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
   const int groups = threads / lanes, index = tid / lanes;
   const Group g{lanes, tid - index * lanes, index + 1, part + index * (lanes / kWarp)};
   const int dim = int(a.dim);
-  unsigned char* ring_x = smem;
-  unsigned char* ring_y = smem + size_t(a.stages) * M * threads * BX;
+  // A stage of the ring: x's units, then grad_out's; each warp's M times 32 together.
+  const uint32_t half = uint32_t(threads * M * BX);
+  const uint32_t stage = half + uint32_t(threads * M * BY);
+  const uint32_t ring = shared_address(smem), ring_end = ring + uint32_t(a.stages) * stage;
+  const uint32_t mine = uint32_t((tid >> 5) * (kWarp * M) + (tid & 31));
+  const uint32_t mine_x = mine * BX, mine_y = half + mine * BY;
   const int turn = int(blockIdx.x) % a.period;
   const int head = S == Span::kPart ? 0 : (E - (a.phase + turn * a.row_phase) % E) % E;
   const int units = (dim - head) / E;
@@ -94,37 +98,44 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
   const int64_t step = int64_t(max(1, int(gridDim.x) / a.period) * groups) * a.period;
   int64_t row = int64_t(int(blockIdx.x) / a.period * groups + index) * a.period + turn;
   const int64_t at = head + int64_t(first) * E;
-  const TX* next_x = static_cast<const TX*>(a.x) + row * a.x_stride + at;
-  const TY* next_y = static_cast<const TY*>(a.dy) + row * a.dy_stride + at;
-  int64_t next_row = row;
-  int in = 0, out = 0;
+  // This thread's first unit, of the row to copy and of the row of x_grad to write.
+  const TX* from_x = static_cast<const TX*>(a.x) + row * a.x_stride + at;
+  const TY* from_y = static_cast<const TY*>(a.dy) + row * a.dy_stride + at;
+  TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride + at;
+  const int64_t step_x = step * a.x_stride, step_y = step * a.dy_stride;
+  const int64_t step_to = step * a.dx_stride;
+  const int64_t rounds = row < a.n_rows ? (a.n_rows - row + step - 1) / step : 0;
+  int64_t to_copy = rounds;
+  uint32_t in = ring, out = ring;
   const auto copy = [&] {
-    if (next_row < a.n_rows) {
+    if (to_copy > 0) {
 #pragma unroll
       for (int m = 0; m < M; ++m)
         if (m * kWarp < left) {
-          copy_async<BX>(ring_x + size_t((in * M + m) * threads + tid) * BX,
-                         next_x + m * (kWarp * E));
-          copy_async<BY>(ring_y + size_t((in * M + m) * threads + tid) * BY,
-                         next_y + m * (kWarp * E));
+          copy_async<BX>(in + mine_x + m * (kWarp * BX), from_x + m * (kWarp * E));
+          copy_async<BY>(in + mine_y + m * (kWarp * BY), from_y + m * (kWarp * E));
         }
     }
     copy_commit();
-    next_x += step * a.x_stride, next_y += step * a.dy_stride, next_row += step;
-    in = in + 1 == a.stages ? 0 : in + 1;
+    from_x += step_x, from_y += step_y, --to_copy;
+    in += stage;
+    if (in == ring_end) in = ring;
   };
   for (int k = 1; k < a.stages; ++k) copy();
   // What a row has besides: its stats and this thread's single elements.
+  const float* stats = a.stats + row;
+  const TX* edge_x = static_cast<const TX*>(a.x) + row * a.x_stride + single;
+  const TY* edge_y = static_cast<const TY*>(a.dy) + row * a.dy_stride + single;
   float mean = 0.f, rstd = 0.f, xe = 0.f, ye = 0.f;
-  const auto look = [&](int64_t r) {
-    if (r >= a.n_rows) return;
-    mean = a.stats[r], rstd = a.stats[a.n_rows + r];
-    if (single >= 0) {
-      xe = to_float<XT>(static_cast<const TX*>(a.x)[r * a.x_stride + single]);
-      ye = to_float<YT>(static_cast<const TY*>(a.dy)[r * a.dy_stride + single]);
+  int64_t to_look = rounds;
+  const auto look = [&] {
+    if (to_look > 0) {
+      mean = stats[0], rstd = stats[a.n_rows];
+      if (single >= 0) xe = to_float<XT>(*edge_x), ye = to_float<YT>(*edge_y);
     }
+    stats += step, edge_x += step_x, edge_y += step_y, --to_look;
   };
-  look(row);
+  look();
   float wf[2 * C], we[1];
   load_weight(a, wf, [&](int i) {
     return i / E * kWarp < left ? int(at) + i / E * (kWarp * E) + i % E : -1;
@@ -136,24 +147,20 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
   float dwe = 0.f, dbe = 0.f;
   const float inv = 1.f / float(dim);
   int parity = 0;
-  const int64_t rounds = row < a.n_rows ? (a.n_rows - row + step - 1) / step : 0;
   // Where groups share a warp, the warp's first has the most rows.
   const int64_t turns = S == Span::kPart ? __shfl_sync(kAll, rounds, 0) : rounds;
-  for (int64_t k = 0; k < turns; ++k, row += step) {
-    const bool held = S != Span::kPart || row < a.n_rows;
+  for (int64_t k = 0; k < turns; ++k, to += step_to) {
+    const bool held = S != Span::kPart || k < rounds;
     copy();
-    const float shift1 = -mean, scale1 = rstd;
-    const float xs = (xe - mean) * rstd, ys = ye;
-    look(row + step);
+    const F2 shift = pair(-mean), scale = pair(rstd);
+    const float rstd1 = rstd, xs = (xe - mean) * rstd, ys = ye;
+    look();
     if (a.stages == 4) copy_wait<3>();
     else if (a.stages == 3) copy_wait<2>();
     else copy_wait<1>();
-    const F2 shift = pair(shift1), scale = pair(scale1);
     const auto unit = [&](int m, Pack<XT, E>& x, Pack<YT, E>& y) {
-      const unsigned char* p = ring_x + size_t((out * M + m) * threads + tid) * BX;
-      const unsigned char* q = ring_y + size_t((out * M + m) * threads + tid) * BY;
-      x.load_kept(reinterpret_cast<const TX*>(p));
-      y.load_kept(reinterpret_cast<const TY*>(q));
+      load_shared(x, out + mine_x + m * (kWarp * BX));
+      load_shared(y, out + mine_y + m * (kWarp * BY));
     };
     F2 along1 = pair(0.f), alongx = pair(0.f);
 #pragma unroll
@@ -182,8 +189,6 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
       parity ^= 1;
       s *= inv, t *= inv;
       const F2 minus1 = pair(-s), minusx = pair(-t);
-      TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride;
-      asm volatile("" ::: "memory");  // read again, not kept
 #pragma unroll
       for (int m = 0; m < M; ++m) {
         if (m * kWarp >= left || !held) continue;
@@ -196,12 +201,12 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
           const F2 gw = mul2(get2(y, i), w[m * (E / 2) + i]);
           set2(o, i, mul2(fma2(d, minusx, add2(gw, minus1)), scale));
         }
-        o.store(to + at + m * (kWarp * E));
+        o.store(to + m * (kWarp * E));
       }
-      if (single >= 0)
-        to[single] = from_float<XT>(scale1 * (ys * we[0] - s - xs * t));
+      if (single >= 0) to[single - at] = from_float<XT>(rstd1 * (ys * we[0] - s - xs * t));
     }
-    out = out + 1 == a.stages ? 0 : out + 1;
+    out += stage;
+    if (out == ring_end) out = ring;
   }
   if (!a.partial) return;
   pdl_trigger();

@@ -124,7 +124,11 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
   const Group g{lanes, tid - index * lanes, index + 1, part + index * (lanes / kWarp)};
   const int dim = a.dim, width = staged_width(dim);
   float* staged = reinterpret_cast<float*>(smem);
-  uint4* ring = reinterpret_cast<uint4*>(smem + 8 * width);
+  // A stage of the ring: each warp's M times 32 units together.
+  const uint32_t stage = uint32_t(threads * M * 16);
+  const uint32_t ring = shared_address(smem) + 8 * width + (tid >> 5) * (kWarp * M * 16) +
+                        (tid & 31) * 16;
+  const uint32_t ring_end = ring + uint32_t(a.stages) * stage;
   const int turn = int(blockIdx.x) % a.period;
   const int head = (E - (a.phase + turn * a.row_phase) % E) % E;
   const int units = (dim - head) / E;
@@ -139,33 +143,38 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
   pdl_wait();
   const int64_t step = int64_t(int(gridDim.x) / a.period * groups) * a.period;
   int64_t row = int64_t(int(blockIdx.x) / a.period * groups + index) * a.period + turn;
-  const TX* next = static_cast<const TX*>(a.x) + row * a.x_stride;  // of the row to copy
-  int64_t next_row = row;
-  int in = 0;
+  // This thread's first unit, of the row to copy and of the row of y to write.
+  const int64_t at = head + first * E;
+  const TX* from = static_cast<const TX*>(a.x) + row * a.x_stride + at;
+  TY* y = static_cast<TY*>(a.y) + row * a.y_stride + at;
+  const int64_t step_x = step * a.x_stride, step_y = step * a.y_stride;
+  const int64_t rounds = row < a.n_rows ? (a.n_rows - row + step - 1) / step : 0;
+  int64_t to_copy = rounds;
+  uint32_t in = ring, out = ring;
   const auto copy = [&] {
-    if (next_row < a.n_rows) {
-      const TX* p = next + head + first * E;
+    if (to_copy > 0) {
 #pragma unroll
       for (int m = 0; m < M; ++m)
-        if (m * kWarp < left)
-          copy_async(ring + (in * M + m) * threads + tid, p + m * (kWarp * E));
+        if (m * kWarp < left) copy_async<16>(in + m * (kWarp * 16), from + m * (kWarp * E));
     }
     copy_commit();
-    next += step * a.x_stride, next_row += step;
-    in = in + 1 == a.stages ? 0 : in + 1;
+    from += step_x, --to_copy;
+    in += stage;
+    if (in == ring_end) in = ring;
   };
   for (int k = 1; k < a.stages; ++k) copy();
   const TX* edge = static_cast<const TX*>(a.x) + row * a.x_stride + single;
   float coming = 0.f;
-  if (single >= 0 && row < a.n_rows) coming = to_float<XT>(*edge);
+  if (single >= 0 && rounds > 0) coming = to_float<XT>(*edge);
   stage_params<E>(a, head, staged);
   const float inv = 1.f / float(dim);
-  int out = 0;
-  for (; row < a.n_rows; row += step) {
+  const float* w = staged + staged_at<E>(first * E, width);
+  float* stats = a.stats + row;
+  for (int64_t k = 1; k <= rounds; ++k, row += step, y += step_y, stats += step) {
     copy();
     float vs = coming;
-    edge += step * a.x_stride;
-    if (single >= 0 && row + step < a.n_rows) coming = to_float<XT>(*edge);
+    edge += step_x;
+    if (single >= 0 && k < rounds) coming = to_float<XT>(*edge);
     if (a.stages == 3) copy_wait<2>();
     else copy_wait<1>();
     F2 v[C];
@@ -174,17 +183,15 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
     for (int m = 0; m < M; ++m) {
       Pack<XT, E> x;
       x.clear();
-      if (m * kWarp < left) {
-        const uint4 q = ring[(out * M + m) * threads + tid];
-        x.w[0] = q.x, x.w[1] = q.y, x.w[2] = q.z, x.w[3] = q.w;
-      }
+      if (m * kWarp < left) load_shared(x, out + m * (kWarp * 16));
 #pragma unroll
       for (int i = 0; i < E / 2; i += 2) {
         v[m * (E / 2) + i] = get2(x, i), v[m * (E / 2) + i + 1] = get2(x, i + 1);
         t = add2(t, v[m * (E / 2) + i]), u = add2(u, v[m * (E / 2) + i + 1]);
       }
     }
-    out = out + 1 == a.stages ? 0 : out + 1;
+    out += stage;
+    if (out == ring_end) out = ring;
     const float mean = g.sum<S>(sum2(add2(t, u)), 0) * inv;
     // From here on v is the difference to the mean.
     vs = single >= 0 ? vs - mean : 0.f;
@@ -207,9 +214,7 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
       continue;
     }
     const float rstd = rstd_of(var, a.eps);
-    if (a.stats && g.lane == 0) a.stats[row] = mean, a.stats[a.n_rows + row] = rstd;
-    TY* y = static_cast<TY*>(a.y) + row * a.y_stride + head + first * E;
-    const float* w = staged + staged_at<E>(first * E, width);
+    if (a.stats && g.lane == 0) stats[0] = mean, stats[a.n_rows] = rstd;
     const F2 scale = pair(rstd);
 #pragma unroll
     for (int m = 0; m < M; ++m) {
@@ -227,7 +232,7 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
       o.store(y + m * (kWarp * E));
     }
     if (single >= 0)
-      static_cast<TY*>(a.y)[row * a.y_stride + single] = from_float<YT>(
+      y[single - at] = from_float<YT>(
           vs * rstd * staged[staged_at<E>(single - head, width)] +
           staged[width + staged_at<E>(single - head, width)]);
   }
