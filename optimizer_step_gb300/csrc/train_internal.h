@@ -207,7 +207,9 @@ __device__ __forceinline__ F2 get2(const Pack<DT, VEC>& p, int i) {
   if constexpr (DT == TRAIN_FP32) {
     return pair(__uint_as_float(p.w[2 * i]), __uint_as_float(p.w[2 * i + 1]));
   } else if constexpr (DT == TRAIN_BF16) {
-    return pair(__uint_as_float(p.w[i] << 16), __uint_as_float(p.w[i] & 0xffff0000u));
+    // Byte permutation: a shift may become a multiplication, in the pipe of the sums.
+    return pair(__uint_as_float(__byte_perm(p.w[i], 0u, 0x1044)),
+                __uint_as_float(p.w[i] & 0xffff0000u));
   } else {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p.w[i]));
     return pair(f.x, f.y);

@@ -77,30 +77,45 @@ struct Group {
   __device__ __forceinline__ float sum(float x, int slot) const {
     return join<S>(x, slot, 0.f, [](float a, float b) { return a + b; });
   }
-  // Two sums at once, of at most 16 warps: after the first step half of the lanes carry
-  // one and half the other.
-  template <Span S>
-  __device__ __forceinline__ void sums(float& x, float& y, int slot) const {
+  // N sums at once (2 or 4), of at most 24 warps.  In the first steps the lanes split
+  // the sums up among themselves: 32 / N lanes end with one each.
+  template <Span S, int N>
+  __device__ __forceinline__ void sums(float (&x)[N], int slot) const {
+    static_assert(N == 2 || N == 4, "");
     if constexpr (S == Span::kPart) {
       for (int d = 1; d < lanes; d *= 2)
-        x += __shfl_xor_sync(kAll, x, d), y += __shfl_xor_sync(kAll, y, d);
+#pragma unroll
+        for (int n = 0; n < N; ++n) x[n] += __shfl_xor_sync(kAll, x[n], d);
       return;
     }
+    constexpr int kShare = traingb::kWarp / N;  // lanes a sum
     const bool upper = lane & 16;
-    float v = upper ? y : x;
-    v += __shfl_xor_sync(kAll, upper ? x : y, 16);
-#pragma unroll
-    for (int d = 8; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
-    if constexpr (S == Span::kWarps) {
-      float* p = part + 2 * slot * traingb::kWarp + (upper ? traingb::kWarp : 0);
-      if ((lane & 15) == 0) p[lane >> 5] = v;
-      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(lanes) : "memory");
-      v = (lane & 15) < lanes / traingb::kWarp ? p[lane & 15] : 0.f;
-#pragma unroll
-      for (int d = 8; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
+    float v = upper ? x[1] : x[0];
+    v += __shfl_xor_sync(kAll, upper ? x[0] : x[1], 16);
+    if constexpr (N == 4) {
+      float w = upper ? x[3] : x[2];
+      w += __shfl_xor_sync(kAll, upper ? x[2] : x[3], 16);
+      const bool odd = lane & 8;
+      const float keep = odd ? w : v;
+      v = keep + __shfl_xor_sync(kAll, odd ? v : w, 8);
     }
-    const float w = __shfl_xor_sync(kAll, v, 16);
-    x = upper ? w : v, y = upper ? v : w;
+#pragma unroll
+    for (int d = kShare / 2; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
+    if constexpr (S == Span::kWarps) {
+      float* p = part + (slot * N + (lane & 31) / kShare) * traingb::kWarp;
+      if ((lane & (kShare - 1)) == 0) p[lane >> 5] = v;
+      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(lanes) : "memory");
+      const int warps = lanes / traingb::kWarp, k = lane & (kShare - 1);
+      v = k < warps ? p[k] : 0.f;
+#pragma unroll
+      for (int o = kShare; o < 24; o += kShare)
+        if (k + o < warps) v += p[k + o];
+#pragma unroll
+      for (int d = kShare / 2; d > 0; d /= 2) v += __shfl_xor_sync(kAll, v, d);
+    }
+    // Lanes 0 and 16 hold sums 0 and 1; of four, 8 and 24 hold 2 and 3.
+    x[0] = __shfl_sync(kAll, v, 0), x[1] = __shfl_sync(kAll, v, 16);
+    if constexpr (N == 4) x[2] = __shfl_sync(kAll, v, 8), x[3] = __shfl_sync(kAll, v, 24);
   }
   template <Span S>
   __device__ __forceinline__ float largest(float x, int slot) const {

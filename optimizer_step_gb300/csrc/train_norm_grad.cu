@@ -90,17 +90,28 @@ struct JoinArgs {
 
 // Adds the pieces of 32 columns in a fixed order.
 constexpr int kJoinWarps = 16;
+constexpr int kJoinAtOnce = 10;
 __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const JoinArgs a) {
   __shared__ float part[2][kJoinWarps][kWarp];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t column = int64_t(blockIdx.x) * kWarp + lane;
   float s = 0.f, t = 0.f;
-  if (column < a.dim)
-    for (int64_t k = warp; k < a.pieces; k += kJoinWarps) {
-      s += a.partial[2 * k * a.dim + column];
-      t += a.partial[(2 * k + 1) * a.dim + column];
+  if (column < a.dim) {
+    const float* p = a.partial + 2 * warp * a.dim + column;
+    // As many on their way together as most sizes have (152 pieces, 16 warps).
+    for (int64_t k = warp; k < a.pieces; k += kJoinAtOnce * kJoinWarps) {
+      float u[kJoinAtOnce][2];
+#pragma unroll
+      for (int i = 0; i < kJoinAtOnce; ++i) {
+        u[i][0] = u[i][1] = 0.f;
+        if (k + i * kJoinWarps < a.pieces) u[i][0] = p[0], u[i][1] = p[a.dim];
+        p += 2 * kJoinWarps * a.dim;
+      }
+#pragma unroll
+      for (int i = 0; i < kJoinAtOnce; ++i) s += u[i][0], t += u[i][1];
     }
+  }
   part[0][warp][lane] = s, part[1][warp][lane] = t;
   __syncthreads();
   void* out = warp == 0 ? a.weight_grad : a.bias_grad;
@@ -172,19 +183,22 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
     } else {
       m = (units * e <= 8 * kWarp ? 8 : units * e <= 16 * kMostLanes ? 16 : 24) / e;
       a.lanes = int32_t((units + m * kWarp - 1) / (m * kWarp)) * kWarp;
-      shape = a.lanes > kWarp ? 1 + m * e / 8 : m * e / 8;
+      shape = m * e == 24 ? 4 : a.lanes > kWarp ? 3 : int(m * e / 8);
     }
     if (a.lanes <= kMostLanes) {
-      const int64_t stage = m * e * a.lanes * (size_of(a.x_type) + size_of(a.dy_type));
+      const int64_t stage = grad_rows(shape == 0 ? 8 : int(m * e)) * m * e * a.lanes *
+                            (size_of(a.x_type) + size_of(a.dy_type));
+      const int64_t kept = shape == 4 ? m * e * a.lanes * 4 : 0;
       int64_t groups = std::min<int64_t>(kMostLanes / a.lanes, a.lanes > kWarp ? 15 : kMostLanes);
       // Few rows: CTAs of a few rounds each rather than many pieces.
       const int64_t fill = kWarp / std::min<int64_t>(a.lanes, kWarp);  // groups a warp
       groups = std::min(groups, ((a.n_rows + kSms - 1) / kSms + fill - 1) / fill * fill);
-      while (groups > fill && groups * std::max(2 * stage, 8 * dim) > kMostShared) groups -= fill;
-      if (groups * std::max(2 * stage, 8 * dim) <= kMostShared) {
-        a.stages = int32_t(std::min<int64_t>(4, kMostShared / (groups * stage)));
+      while (groups > fill && groups * std::max(2 * stage + kept, 8 * dim) > kMostShared)
+        groups -= fill;
+      if (groups * std::max(2 * stage + kept, 8 * dim) <= kMostShared) {
+        a.stages = int32_t(std::min<int64_t>(4, (kMostShared - groups * kept) / (groups * stage)));
         return go(k.ring[shape], std::min<int64_t>(kSms, (a.n_rows + groups - 1) / groups), groups,
-                  a.stages * groups * stage);
+                  groups * (a.stages * stage + kept));
       }
     }
     a.period = 1;

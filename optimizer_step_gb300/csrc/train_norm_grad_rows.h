@@ -23,6 +23,9 @@ struct NormGradArgs {
   int32_t stages;            // of the ring
 };
 
+// Rows that a group works on at once, by the elements a thread has of each.
+__host__ __device__ constexpr int grad_rows(int elements) { return elements == 8 ? 2 : 1; }
+
 // The weight's element at a column, or 1.
 template <int N, class At>
 __device__ __forceinline__ void load_weight(const NormGradArgs& a, float (&w)[N], At&& at) {
@@ -58,7 +61,7 @@ __device__ __forceinline__ void write_piece(const NormGradArgs& a, const float* 
 // elements: they are read from the ring once for the two sums along the row and the
 // sums down the columns, and again for x_grad.  At the end the CTA's groups are added
 // and written as one piece; join_kernel adds the pieces.
-template <int XT, int YT, int M, Span S>
+template <int XT, int YT, int M, int R, Span S, bool WS>
 __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ NormGradArgs a) {
   using TX = typename TypeOf<XT>::T;
   using TY = typename TypeOf<YT>::T;
@@ -66,15 +69,16 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
   constexpr int C = M * E / 2;  // pairs a thread
   constexpr int BX = E * int(sizeof(TX)), BY = E * int(sizeof(TY));
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float part[4 * kWarp];
+  __shared__ float part[4 * R * kWarp];
   const int tid = threadIdx.x, threads = blockDim.x;
   const int lanes = S == Span::kWarp ? kWarp : a.lanes;
   const int groups = threads / lanes, index = tid / lanes;
   const Group g{lanes, tid - index * lanes, index + 1, part + index * (lanes / kWarp)};
   const int dim = int(a.dim);
-  // A stage of the ring: x's units, then grad_out's; each warp's M times 32 together.
+  // A stage of the ring: R rows, of each x's units, then grad_out's; each warp's M times
+  // 32 together.
   const uint32_t half = uint32_t(threads * M * BX);
-  const uint32_t stage = half + uint32_t(threads * M * BY);
+  const uint32_t line = half + uint32_t(threads * M * BY), stage = R * line;
   const uint32_t ring = shared_address(smem), ring_end = ring + uint32_t(a.stages) * stage;
   const uint32_t mine = uint32_t((tid >> 5) * (kWarp * M) + (tid & 31));
   const uint32_t mine_x = mine * BX, mine_y = half + mine * BY;
@@ -104,106 +108,167 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
   TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride + at;
   const int64_t step_x = step * a.x_stride, step_y = step * a.dy_stride;
   const int64_t step_to = step * a.dx_stride;
-  const int64_t rounds = row < a.n_rows ? (a.n_rows - row + step - 1) / step : 0;
-  int64_t to_copy = rounds;
+  const int rounds = row < a.n_rows ? int((a.n_rows - row + step - 1) / step) : 0;
+  const bool ends = head > 0 || units * E < dim - head;
+  int to_copy = rounds;
   uint32_t in = ring, out = ring;
   const auto copy = [&] {
-    if (to_copy > 0) {
 #pragma unroll
-      for (int m = 0; m < M; ++m)
-        if (m * kWarp < left) {
-          copy_async<BX>(in + mine_x + m * (kWarp * BX), from_x + m * (kWarp * E));
-          copy_async<BY>(in + mine_y + m * (kWarp * BY), from_y + m * (kWarp * E));
-        }
+    for (int r = 0; r < R; ++r) {
+      if (to_copy > 0) {
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          if (m * kWarp < left) {
+            copy_async<BX>(in + r * line + mine_x + m * (kWarp * BX), from_x + m * (kWarp * E));
+            copy_async<BY>(in + r * line + mine_y + m * (kWarp * BY), from_y + m * (kWarp * E));
+          }
+      }
+      from_x += step_x, from_y += step_y, --to_copy;
     }
     copy_commit();
-    from_x += step_x, from_y += step_y, --to_copy;
     in += stage;
     if (in == ring_end) in = ring;
   };
   for (int k = 1; k < a.stages; ++k) copy();
   // What a row has besides: its stats and this thread's single elements.
   const float* stats = a.stats + row;
-  const TX* edge_x = static_cast<const TX*>(a.x) + row * a.x_stride + single;
-  const TY* edge_y = static_cast<const TY*>(a.dy) + row * a.dy_stride + single;
-  float mean = 0.f, rstd = 0.f, xe = 0.f, ye = 0.f;
-  int64_t to_look = rounds;
+  int64_t edge = row;
+  float mean[R], rstd[R], xe[R] = {}, ye[R] = {};
+  int to_look = rounds;
   const auto look = [&] {
-    if (to_look > 0) {
-      mean = stats[0], rstd = stats[a.n_rows];
-      if (single >= 0) xe = to_float<XT>(*edge_x), ye = to_float<YT>(*edge_y);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      mean[r] = rstd[r] = 0.f;
+      if (to_look > 0) {
+        mean[r] = stats[0], rstd[r] = stats[a.n_rows];
+        if (ends && single >= 0) {
+          xe[r] = to_float<XT>(static_cast<const TX*>(a.x)[edge * a.x_stride + single]);
+          ye[r] = to_float<YT>(static_cast<const TY*>(a.dy)[edge * a.dy_stride + single]);
+        }
+      }
+      stats += step, --to_look;
+      if (ends) edge += step;
     }
-    stats += step, edge_x += step_x, edge_y += step_y, --to_look;
   };
   look();
-  float wf[2 * C], we[1];
-  load_weight(a, wf, [&](int i) {
-    return i / E * kWarp < left ? int(at) + i / E * (kWarp * E) + i % E : -1;
-  });
+  float we[1];
   load_weight(a, we, [&](int) { return single; });
   F2 w[C], dw[C], db[C];
+  // In shared memory behind the ring: four elements of each thread's unit together.
+  const uint32_t kept = ring_end + mine * 16;
+  if constexpr (WS) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) w[c] = pair(wf[2 * c], wf[2 * c + 1]), dw[c] = db[c] = pair(0.f);
+    for (int m = 0; m < M; ++m) {
+      float wf[E];
+      load_weight(a, wf, [&](int i) {
+        return m * kWarp < left ? int(at) + m * (kWarp * E) + i : -1;
+      });
+#pragma unroll
+      for (int i = 0; i < E; i += 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                         kept + uint32_t(i / 4 * threads * M + m * kWarp) * 16),
+                     "f"(wf[i]), "f"(wf[i + 1]), "f"(wf[i + 2]), "f"(wf[i + 3])
+                     : "memory");
+    }
+  } else {
+    float wf[2 * C];
+    load_weight(a, wf, [&](int i) {
+      return i / E * kWarp < left ? int(at) + i / E * (kWarp * E) + i % E : -1;
+    });
+#pragma unroll
+    for (int c = 0; c < C; ++c) w[c] = pair(wf[2 * c], wf[2 * c + 1]);
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) dw[c] = db[c] = pair(0.f);
+  const auto weights = [&](int m) {
+    if constexpr (WS) {
+#pragma unroll
+      for (int i = 0; i < E; i += 4) {
+        Pack<TRAIN_FP32, 4> p;
+        load_shared(p, kept + uint32_t(i / 4 * threads * M + m * kWarp) * 16);
+        w[m * (E / 2) + i / 2] = get2(p, 0), w[m * (E / 2) + i / 2 + 1] = get2(p, 1);
+      }
+    }
+  };
   float dwe = 0.f, dbe = 0.f;
   const float inv = 1.f / float(dim);
   int parity = 0;
   // Where groups share a warp, the warp's first has the most rows.
-  const int64_t turns = S == Span::kPart ? __shfl_sync(kAll, rounds, 0) : rounds;
-  for (int64_t k = 0; k < turns; ++k, to += step_to) {
-    const bool held = S != Span::kPart || k < rounds;
+  const int turns = S == Span::kPart ? __shfl_sync(kAll, rounds, 0) : rounds;
+  for (int k = 0; k < turns; k += R) {
     copy();
-    const F2 shift = pair(-mean), scale = pair(rstd);
-    const float rstd1 = rstd, xs = (xe - mean) * rstd, ys = ye;
+    F2 shift[R], scale[R];
+    float rstd1[R], xs[R] = {}, ys[R] = {};
+    bool held[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      held[r] = (R == 1 && S != Span::kPart) || k + r < rounds;
+      shift[r] = pair(-mean[r]), scale[r] = pair(rstd[r]);
+      rstd1[r] = rstd[r];
+      if (ends) xs[r] = (xe[r] - mean[r]) * rstd[r], ys[r] = ye[r];
+    }
     look();
     if (a.stages == 4) copy_wait<3>();
     else if (a.stages == 3) copy_wait<2>();
     else copy_wait<1>();
-    const auto unit = [&](int m, Pack<XT, E>& x, Pack<YT, E>& y) {
-      load_shared(x, out + mine_x + m * (kWarp * BX));
-      load_shared(y, out + mine_y + m * (kWarp * BY));
+    const auto unit = [&](int r, int m, Pack<XT, E>& x, Pack<YT, E>& y) {
+      load_shared(x, out + r * line + mine_x + m * (kWarp * BX));
+      load_shared(y, out + r * line + mine_y + m * (kWarp * BY));
     };
-    F2 along1 = pair(0.f), alongx = pair(0.f);
+    float along[2 * R];
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      if (m * kWarp >= left || !held) continue;
-      Pack<XT, E> x;
-      Pack<YT, E> y;
-      unit(m, x, y);
-#pragma unroll
-      for (int i = 0; i < E / 2; ++i) {
-        const int c = m * (E / 2) + i;
-        const F2 d = mul2(add2(get2(x, i), shift), scale), v = get2(y, i), gw = mul2(v, w[c]);
-        along1 = add2(along1, gw);
-        alongx = fma2(gw, d, alongx);
-        db[c] = add2(db[c], v);
-        dw[c] = fma2(v, d, dw[c]);
-      }
-    }
-    float s = sum2(along1), t = sum2(alongx);
-    if (single >= 0) {
-      s += ys * we[0], t += ys * we[0] * xs;
-      dbe += ys, dwe += ys * xs;
-    }
-    if (a.dx) {
-      g.sums<S>(s, t, parity);
-      parity ^= 1;
-      s *= inv, t *= inv;
-      const F2 minus1 = pair(-s), minusx = pair(-t);
+    for (int r = 0; r < R; ++r) {
+      F2 along1 = pair(0.f), alongx = pair(0.f);
 #pragma unroll
       for (int m = 0; m < M; ++m) {
-        if (m * kWarp >= left || !held) continue;
-        Pack<XT, E> x, o;
+        if (m * kWarp >= left || !held[r]) continue;
+        Pack<XT, E> x;
         Pack<YT, E> y;
-        unit(m, x, y);
+        unit(r, m, x, y);
+        weights(m);
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-          const F2 d = mul2(add2(get2(x, i), shift), scale);
-          const F2 gw = mul2(get2(y, i), w[m * (E / 2) + i]);
-          set2(o, i, mul2(fma2(d, minusx, add2(gw, minus1)), scale));
+          const int c = m * (E / 2) + i;
+          const F2 d = mul2(add2(get2(x, i), shift[r]), scale[r]);
+          const F2 v = get2(y, i), gw = mul2(v, w[c]);
+          along1 = add2(along1, gw);
+          alongx = fma2(gw, d, alongx);
+          db[c] = add2(db[c], v);
+          dw[c] = fma2(v, d, dw[c]);
         }
-        o.store(to + m * (kWarp * E));
       }
-      if (single >= 0) to[single - at] = from_float<XT>(rstd1 * (ys * we[0] - s - xs * t));
+      along[2 * r] = sum2(along1), along[2 * r + 1] = sum2(alongx);
+      if (ends && single >= 0 && held[r]) {
+        along[2 * r] += ys[r] * we[0], along[2 * r + 1] += ys[r] * we[0] * xs[r];
+        dbe += ys[r], dwe += ys[r] * xs[r];
+      }
+    }
+    if (a.dx) {
+      g.sums<S>(along, parity);
+      parity ^= 1;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float s = along[2 * r] * inv, t = along[2 * r + 1] * inv;
+        const F2 less1 = pair(-s * rstd1[r]), lessx = pair(-t);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          if (m * kWarp >= left || !held[r]) continue;
+          Pack<XT, E> x, o;
+          Pack<YT, E> y;
+          unit(r, m, x, y);
+          weights(m);
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i) {
+            const F2 d = mul2(add2(get2(x, i), shift[r]), scale[r]);
+            const F2 gw = mul2(get2(y, i), w[m * (E / 2) + i]);
+            set2(o, i, fma2(fma2(d, lessx, gw), scale[r], less1));
+          }
+          o.store(to + m * (kWarp * E));
+        }
+        if (ends && single >= 0 && held[r])
+          to[single - at] = from_float<XT>(rstd1[r] * (ys[r] * we[0] - s - xs[r] * t));
+        to += step_to;
+      }
     }
     out += stage;
     if (out == ring_end) out = ring;
@@ -264,9 +329,10 @@ __global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant_
       s += y[m], t += y[m] * x[m];
     }
     if (a.dx) {
-      g.sums<S>(s, t, parity);
+      float along[2] = {s, t};
+      g.sums<S>(along, parity);
       parity ^= 1;
-      s *= inv, t *= inv;
+      s = along[0] * inv, t = along[1] * inv;
       TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride + first;
 #pragma unroll
       for (int m = 0; m < M; ++m)
@@ -293,10 +359,10 @@ struct NormGradKernels {
 template <int XT, int YT>
 constexpr NormGradKernels norm_grad_kernels() {
   constexpr int M = XT == TRAIN_FP32 || YT == TRAIN_FP32 ? 2 : 1;  // units of 8 elements
-  return {{grad_ring_kernel<XT, YT, 1, Span::kPart>, grad_ring_kernel<XT, YT, M, Span::kWarp>,
-           grad_ring_kernel<XT, YT, 2 * M, Span::kWarp>,
-           grad_ring_kernel<XT, YT, 2 * M, Span::kWarps>,
-           grad_ring_kernel<XT, YT, 3 * M, Span::kWarps>},
+  return {{grad_ring_kernel<XT, YT, 1, grad_rows(8), Span::kPart, false>, grad_ring_kernel<XT, YT, M, grad_rows(8), Span::kWarp, false>,
+           grad_ring_kernel<XT, YT, 2 * M, grad_rows(16), Span::kWarp, false>,
+           grad_ring_kernel<XT, YT, 2 * M, grad_rows(16), Span::kWarps, false>,
+           grad_ring_kernel<XT, YT, 3 * M, grad_rows(24), Span::kWarps, true>},
           {grad_scalar_kernel<XT, YT, 8, Span::kWarp>, grad_scalar_kernel<XT, YT, 16, Span::kWarp>,
            grad_scalar_kernel<XT, YT, 16, Span::kWarps>}};
 }
