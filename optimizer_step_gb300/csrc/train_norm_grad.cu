@@ -119,12 +119,7 @@ __global__ void __launch_bounds__(kJoinWarps* kWarp) join_kernel(const JoinArgs 
     s = 0.f;
 #pragma unroll
     for (int w = 0; w < kJoinWarps; ++w) s += part[warp][w][lane];
-    by_type(a.type, [&](auto P) {
-      constexpr int PT = decltype(P)::value;
-      auto* p = static_cast<typename TypeOf<PT>::T*>(out) + column;
-      if (a.accumulate) s += to_float<PT>(*p);
-      *p = from_float<PT>(s);
-    });
+    write_grad(out, a.type, a.accumulate, column, s);
   }
 }
 
@@ -134,9 +129,12 @@ constexpr int kMostPieces = 256;
 constexpr int kMostLanes = 512;  // threads a CTA
 constexpr int64_t kMostShared = 224 * 1024;  // a CTA's dynamic shared memory
 
+// Sizes whose sums one cluster takes and adds by itself, without a workspace.
+bool one_cluster(int64_t n_rows, int64_t dim) { return dim <= 1024 && n_rows * dim <= (1 << 17); }
+
 // Pieces that any of the kernels below may write.
-int64_t most_pieces(int64_t n_rows) {
-  return n_rows == 0 ? 0 : std::min<int64_t>(kMostPieces, n_rows);
+int64_t most_pieces(int64_t n_rows, int64_t dim) {
+  return one_cluster(n_rows, dim) ? 0 : std::min<int64_t>(kMostPieces, n_rows);
 }
 
 // Launches the kernel for rows that stay on chip, if there is one; sets `pieces`.
@@ -151,6 +149,24 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
     return int64_t(reinterpret_cast<uintptr_t>(p) / uintptr_t(size_of(type))) % e;
   };
   const auto go = [&](NormGradKernel kernel, int64_t ctas, int64_t groups, int64_t smem) {
+    if (a.joined) {
+      // A power of two, so that each kind of row's beginning has as many CTAs.
+      a.joined = 1;
+      while (a.joined < kJoined && a.joined < ctas) a.joined *= 2;
+      a.joined = std::max(a.joined, a.period);
+      *pieces = 1;
+      smem = std::max(smem, groups * 2 * dim * 4);
+      const void* f = reinterpret_cast<const void*>(kernel);
+      cudaError_t ce = cudaSuccess;
+      if (smem > 40 * 1024)
+        ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  int(kMostShared));
+      if (ce == cudaSuccess && a.joined > 8)
+        ce = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (ce != cudaSuccess) return ce;
+      return launch(kernel, dim3(unsigned(a.joined)), int(groups * a.lanes), size_t(smem), stream,
+                    true, a.joined, a);
+    }
     // A CTA for each row that begins differently, but none without rows.
     ctas = std::min((ctas + a.period - 1) / a.period * a.period, a.n_rows);
     if (ctas < a.period) ctas = std::min<int64_t>(a.n_rows, a.period);
@@ -192,7 +208,8 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
       int64_t groups = std::min<int64_t>(kMostLanes / a.lanes, a.lanes > kWarp ? 15 : kMostLanes);
       // Few rows: CTAs of a few rounds each rather than many pieces.
       const int64_t fill = kWarp / std::min<int64_t>(a.lanes, kWarp);  // groups a warp
-      groups = std::min(groups, ((a.n_rows + kSms - 1) / kSms + fill - 1) / fill * fill);
+      const int64_t spread = a.joined ? kJoined : kSms;
+      groups = std::min(groups, ((a.n_rows + spread - 1) / spread + fill - 1) / fill * fill);
       while (groups > fill && groups * std::max(2 * stage + kept, 8 * dim) > kMostShared)
         groups -= fill;
       if (groups * std::max(2 * stage + kept, 8 * dim) <= kMostShared) {
@@ -209,7 +226,8 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
   a.lanes = int32_t((dim + span - 1) / span) * kWarp;
   if (a.lanes > 512 || dim * 8 > kMostShared) return cudaSuccess;
   int64_t groups = std::max<int64_t>(1, std::min<int64_t>(512 / a.lanes, a.lanes > kWarp ? 15 : 16));
-  groups = std::min(groups, (a.n_rows + kSms - 1) / kSms);
+  const int64_t spread = a.joined ? kJoined : kSms;
+  groups = std::min(groups, (a.n_rows + spread - 1) / spread);
   while (groups > 1 && groups * dim * 8 > kMostShared) --groups;
   return go(k.scalar[a.lanes > kWarp ? 2 : s],
             std::min<int64_t>(kSms, (a.n_rows + groups - 1) / groups), groups, 0);
@@ -233,7 +251,7 @@ LAMB_API int train_layer_norm_grad_workspace(int64_t n_rows, int64_t dim, int64_
   if (!bytes) return fail(LAMB_ERR_INVALID, "bytes is NULL");
   const int rc = check_sizes(n_rows, dim);
   if (rc != LAMB_OK) return rc;
-  *bytes = most_pieces(n_rows) * 2 * dim * 4;
+  *bytes = most_pieces(n_rows, dim) * 2 * dim * 4;
   return LAMB_OK;
 }
 
@@ -259,8 +277,9 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
     return fail(LAMB_ERR_INVALID, "accumulate must be 0 or 1");
   if (n_rows > 0 && !stats) return fail(LAMB_ERR_INVALID, "stats is NULL");
   const bool params = weight_grad || bias_grad;
-  if (params && n_rows > 0) {
-    if (!workspace || workspace_bytes < most_pieces(n_rows) * 2 * dim * 4)
+  const bool joined = params && n_rows > 0 && one_cluster(n_rows, dim);
+  if (params && most_pieces(n_rows, dim) > 0) {
+    if (!workspace || workspace_bytes < most_pieces(n_rows, dim) * 2 * dim * 4)
       return fail(LAMB_ERR_INVALID, "workspace is missing or too small");
     if (reinterpret_cast<uintptr_t>(workspace) % 16)
       return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
@@ -268,7 +287,10 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   NormGradArgs a{};
   a.dy = grad_out, a.x = x, a.weight = weight, a.stats = stats, a.dx = x_grad;
-  a.partial = params ? static_cast<float*>(workspace) : nullptr;
+  a.partial = params && !joined ? static_cast<float*>(workspace) : nullptr;
+  a.joined = joined;
+  a.weight_grad = weight_grad, a.bias_grad = bias_grad;
+  a.grad_type = param_grad_dtype, a.accumulate = accumulate;
   a.n_rows = n_rows, a.dim = dim;
   a.dy_stride = grad_out_stride, a.x_stride = x_stride, a.dx_stride = x_grad_stride;
   a.dy_type = grad_out_dtype, a.x_type = x_dtype, a.param_type = weight_dtype;
@@ -288,7 +310,7 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
         ce = launch(wide_dx_kernel, dim3(unsigned(n_rows)), kWideThreads, 0, st, true, 1, a);
     }
   }
-  if (ce == cudaSuccess && params && !(n_rows == 0 && accumulate)) {
+  if (ce == cudaSuccess && params && !joined && !(n_rows == 0 && accumulate)) {
     JoinArgs j{};
     j.partial = a.partial, j.weight_grad = weight_grad, j.bias_grad = bias_grad;
     j.dim = dim, j.pieces = pieces;

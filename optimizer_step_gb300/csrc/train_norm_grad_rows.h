@@ -2,6 +2,8 @@
 // compiled once for each type of x.  Not part of the public interface.
 #pragma once
 
+#include <cooperative_groups.h>
+
 #include "train_norm.h"
 
 namespace traingb {
@@ -21,7 +23,25 @@ struct NormGradArgs {
   int32_t period;            // rows this far apart begin equally far from a unit's boundary
   int32_t phase, row_phase;  // elements from one to the first row; from row to row
   int32_t stages;            // of the ring
+  // Where one cluster has all rows, it writes the sums itself; 0 CTAs: pieces are.
+  int32_t joined;
+  void* weight_grad;
+  void* bias_grad;
+  int32_t grad_type, accumulate;
 };
+
+constexpr int kJoined = 16;  // CTAs, at most
+
+// One sum into a parameter's gradient.
+__device__ __forceinline__ void write_grad(void* to, int type, bool accumulate, int64_t at,
+                                           float s) {
+  by_type(type, [&](auto P) {
+    constexpr int PT = decltype(P)::value;
+    auto* p = static_cast<typename TypeOf<PT>::T*>(to) + at;
+    if (accumulate) s += to_float<PT>(*p);
+    *p = from_float<PT>(s);
+  });
+}
 
 // Rows that a group works on at once, by the elements a thread has of each.
 __host__ __device__ constexpr int grad_rows(int elements) { return elements == 8 ? 2 : 1; }
@@ -43,16 +63,32 @@ __device__ __forceinline__ void load_weight(const NormGradArgs& a, float (&w)[N]
   });
 }
 
-// Adds up the groups' sums, each at [group][2][dim] in `sums`, for this CTA's piece.
-__device__ __forceinline__ void write_piece(const NormGradArgs& a, const float* sums, int groups) {
-  const int n = 2 * int(a.dim);
-  float* to = a.partial + int64_t(blockIdx.x) * n;
+// Adds up the groups' sums, each at [group][2][dim] in `sums`, and writes this CTA's
+// piece, or with the other CTAs of a cluster, a share of the columns each, the gradients.
+__device__ __forceinline__ void write_sums(const NormGradArgs& a, float* sums, int groups) {
+  const int dim = int(a.dim), n = 2 * dim;
+  float* to = a.joined ? sums : a.partial + int64_t(blockIdx.x) * n;
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     float s = sums[i];
     for (int k = 1; k < groups; ++k) s += sums[int64_t(k) * n + i];
     to[i] = s;
   }
+  if (!a.joined) return;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n; i += a.joined * blockDim.x) {
+    float s = 0.f, u[kJoined];
+#pragma unroll
+    for (int r = 0; r < kJoined; ++r)
+      u[r] = r < a.joined ? cluster.map_shared_rank(sums, r)[i] : 0.f;
+#pragma unroll
+    for (int r = 0; r < kJoined; ++r) s += u[r];
+    void* grad = i < dim ? a.weight_grad : a.bias_grad;
+    if (grad) write_grad(grad, a.grad_type, a.accumulate, i < dim ? i : i - dim, s);
+  }
+  cluster.sync();  // no CTA leaves while another reads from it
 }
 
 // Rows come through a ring of asynchronous copies as in the forward pass: units of E
@@ -60,7 +96,8 @@ __device__ __forceinline__ void write_piece(const NormGradArgs& a, const float* 
 // sums over the rows for its columns in registers, which leaves no room for the row's
 // elements: they are read from the ring once for the two sums along the row and the
 // sums down the columns, and again for x_grad.  At the end the CTA's groups are added
-// and written as one piece; join_kernel adds the pieces.
+// and written as one piece, and join_kernel adds the pieces; the CTAs of few rows are a
+// cluster that adds its sums by itself.
 template <int XT, int YT, int M, int R, Span S, bool WS>
 __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ NormGradArgs a) {
   using TX = typename TypeOf<XT>::T;
@@ -273,7 +310,7 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
     out += stage;
     if (out == ring_end) out = ring;
   }
-  if (!a.partial) return;
+  if (!a.partial && !a.joined) return;
   pdl_trigger();
   // The ring's memory is free when all groups are through.
   __syncthreads();
@@ -287,7 +324,7 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
     split(db[c], sums[dim + column], sums[dim + column + 1]);
   }
   if (single >= 0) sums[single] = dwe, sums[dim + single] = dbe;
-  write_piece(a, reinterpret_cast<const float*>(smem), groups);
+  write_sums(a, reinterpret_cast<float*>(smem), groups);
 }
 
 // Element by element, M a thread, straight from memory: for rows of x, grad_out and
@@ -339,13 +376,13 @@ __global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant_
         if (m * kWarp < left) to[m * kWarp] = from_float<XT>(rstd * (y[m] - s - x[m] * t));
     }
   }
-  if (!a.partial) return;
+  if (!a.partial && !a.joined) return;
   pdl_trigger();
   float* sums = reinterpret_cast<float*>(smem) + int64_t(index) * 2 * dim + first;
 #pragma unroll
   for (int m = 0; m < M; ++m)
     if (m * kWarp < left) sums[m * kWarp] = dw[m], sums[dim + m * kWarp] = db[m];
-  write_piece(a, reinterpret_cast<const float*>(smem), groups);
+  write_sums(a, reinterpret_cast<float*>(smem), groups);
 }
 
 // The kernels of two types.

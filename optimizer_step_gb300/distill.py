@@ -10,7 +10,7 @@ import torch
 
 from . import _lib
 from .embedding import _ID_TYPES, _TYPES, _code, _enqueue, _fits, _row_stride
-from .layernorm import _matrix, _same_rows
+from .layernorm import _matrix, _new_like, _same_rows
 
 
 def _arguments(logits, top_ids, top_logits, labels, temperature, soft_weight, hard_weight,
@@ -23,12 +23,14 @@ def _arguments(logits, top_ids, top_logits, labels, temperature, soft_weight, ha
     if top_ids is not None or top_logits is not None:
         i_code = _code("top_ids", top_ids, _ID_TYPES, index)
         t_code = _code("top_logits", top_logits, _TYPES, index)
-        if top_ids.shape[:-1] != lead or top_ids.dim() != logits.dim():
+        shape = top_ids.shape
+        if shape[:-1] != lead or len(shape) != len(lead) + 1:
             raise ValueError("top_ids: expected logits.shape[:-1] + (top_k,)")
-        if top_logits.shape != top_ids.shape:
+        if top_logits.shape != shape:
             raise ValueError("top_logits: expected the shape of top_ids")
-        top_k = top_ids.shape[-1]
-        i_stride, t_stride = _row_stride("top_ids", top_ids), _row_stride("top_logits", top_logits)
+        top_k = shape[-1]
+        i_stride = top_k if top_ids.is_contiguous() else _row_stride("top_ids", top_ids)
+        t_stride = top_k if top_logits.is_contiguous() else _row_stride("top_logits", top_logits)
         i_ptr, t_ptr = top_ids.data_ptr(), top_logits.data_ptr()
     if labels is not None:
         l_code = _code("labels", labels, _ID_TYPES, index)
@@ -126,7 +128,7 @@ def distill_loss_grad(logits: torch.Tensor, top_ids: torch.Tensor | None,
         o_code = args[1] if dtype is None else _TYPES.get(dtype)
         if o_code is None:
             raise TypeError(f"dtype: expected {', '.join(map(str, _TYPES))}")
-        out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=logits.device)
+        out = _new_like(logits, dtype)
         o_stride = args[4]
     else:
         o_code, o_stride = _same_rows("out", out, logits.shape, index)

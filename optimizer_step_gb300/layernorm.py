@@ -18,30 +18,49 @@ from .embedding import _TYPES, _code, _enqueue, _row_stride
 
 def _vector(name, t, dim, index):
     """Code and address of a vector of ``dim`` elements."""
-    code = _code(name, t, _TYPES, index)
-    if t.dim() != 1 or t.shape[0] != dim or not t.is_contiguous():
-        raise ValueError(f"{name}: expected {dim} consecutive elements")
-    return code, t.data_ptr()
+    try:
+        if (t.get_device() == index and t.numel() == dim and t.dim() == 1
+                and t.is_contiguous()):
+            return _TYPES[t.dtype], t.data_ptr()
+    except (AttributeError, KeyError):
+        pass
+    _code(name, t, _TYPES, index)
+    raise ValueError(f"{name}: expected {dim} consecutive elements")
 
 
 def _matrix(name, t):
     """Code, rows, width, row stride and device of a tensor's rows."""
+    try:
+        code, dim, index = _TYPES[t.dtype], t.shape[-1], t.get_device()
+        if dim > 0 and index >= 0:
+            return (code, t.numel() // dim, dim,
+                    dim if t.is_contiguous() else _row_stride(name, t), index)
+    except (AttributeError, KeyError, IndexError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dim() == 0:
         raise TypeError(f"{name}: expected a tensor of one dimension or more")
-    index = t.get_device()
-    code = _code(name, t, _TYPES, index)
-    dim = t.shape[-1]
-    if dim == 0:
-        raise ValueError(f"{name}: rows have no elements")
-    return code, t.numel() // dim, dim, _row_stride(name, t), index
+    _code(name, t, _TYPES, t.get_device())
+    raise ValueError(f"{name}: rows have no elements")
 
 
 def _same_rows(name, t, shape, index):
     """Code and row stride of another tensor with these rows."""
-    code = _code(name, t, _TYPES, index)
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}")
-    return code, _row_stride(name, t)
+    try:
+        if t.get_device() == index and t.shape == shape:
+            return _TYPES[t.dtype], shape[-1] if t.is_contiguous() else _row_stride(name, t)
+    except (AttributeError, KeyError):
+        pass
+    _code(name, t, _TYPES, index)
+    raise ValueError(f"{name}: expected shape {tuple(shape)}")
+
+
+def _new_like(x, dtype):
+    """An empty tensor of x's shape, rows one behind the other."""
+    if dtype is None:
+        dtype = x.dtype
+    if x.is_contiguous():
+        return torch.empty_like(x) if dtype is x.dtype else torch.empty_like(x, dtype=dtype)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
 
 
 class _LayerNorm(torch.autograd.Function):
@@ -116,14 +135,17 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
         o_code = code if out_dtype is None else _TYPES.get(out_dtype)
         if o_code is None:
             raise TypeError(f"out_dtype: expected {', '.join(map(str, _TYPES))}")
-        out = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+        out = _new_like(x, out_dtype)
         o_stride = dim
     else:
         o_code, o_stride = _same_rows("out", out, x.shape, index)
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError(f"out: expected {out_dtype}")
-    kept = (torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=x.device) if stats
-            else None)
+    kept = None
+    if stats:
+        shape = x.shape
+        kept = torch.empty((2, rows) if len(shape) == 2 else (2, *shape[:-1]),
+                           dtype=torch.float32, device=x.device)
     _enqueue(index, _lib.load().train_layer_norm, x.data_ptr(), code, stride, rows, dim, w_ptr,
              b_ptr, p_code, eps, out.data_ptr(), o_code, o_stride,
              kept.data_ptr() if stats else None)
@@ -161,12 +183,12 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     x_code, rows, dim, x_stride, index = _matrix("x", x)
     g_code, g_stride = _same_rows("grad_out", grad_out, x.shape, index)
     if (_code("stats", stats, _TYPES, index) != _lib.TRAIN_FP32 or not stats.is_contiguous()
-            or stats.shape != (2, *x.shape[:-1])):
+            or stats.shape[:1] != (2,) or stats.shape[1:] != x.shape[:-1]):
         raise ValueError(f"stats: expected float32 of shape {(2, *x.shape[:-1])}")
     w_code, w_ptr = (0, None) if weight is None else _vector("weight", weight, dim, index)
     device = x.device
     if x_grad is True:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=device)
+        dx = _new_like(x, None)
         dx_stride = dim
     elif x_grad is None or x_grad is False:
         dx, dx_stride = None, dim

@@ -54,13 +54,14 @@ def grad_args(**change):
     (dict(grad_out_dtype=3), INVALID), (dict(x_dtype=3), INVALID), (dict(weight_dtype=-1), INVALID),
     (dict(param_grad_dtype=3), INVALID), (dict(accumulate=2), INVALID), (dict(n_rows=-1), INVALID),
     (dict(dim=0), INVALID), (dict(grad_out_stride=7), INVALID), (dict(x_stride=7), INVALID),
-    (dict(x_grad_stride=7), INVALID), (dict(workspace=None), INVALID),
-    (dict(workspace_bytes=-1), INVALID), (dict(workspace_bytes=0), INVALID),
+    (dict(x_grad_stride=7), INVALID), (dict(n_rows=1 << 20, workspace=None), INVALID),
+    (dict(n_rows=1 << 20, workspace_bytes=-1), INVALID),
+    (dict(n_rows=1 << 20, workspace_bytes=0), INVALID),
     (dict(n_rows=1 << 30, dim=1 << 20, grad_out_stride=1 << 20, x_stride=1 << 20,
           x_grad_stride=1 << 20, workspace_bytes=1 << 62), INVALID),
     (dict(grad_out=P + 1), ALIGN), (dict(x=P + 1), ALIGN), (dict(x_grad=P + 1), ALIGN),
     (dict(weight=P + 1), ALIGN), (dict(weight_grad=P + 1), ALIGN), (dict(bias_grad=P + 1), ALIGN),
-    (dict(stats=P + 2), ALIGN), (dict(workspace=P + 8), ALIGN),
+    (dict(stats=P + 2), ALIGN), (dict(n_rows=1 << 20, workspace=P + 8), ALIGN),
     (dict(weight_grad=P + 2, param_grad_dtype=2), ALIGN),
 ])
 def test_layer_norm_grad_refuses(change, code):
