@@ -1,5 +1,7 @@
 // The loss against a teacher's top logits and the true labels, and its gradient
 // (train_ops.h).
+#include <mutex>
+
 #include "train_distill_rows.h"
 
 using namespace traingb;
@@ -138,6 +140,42 @@ constexpr int kSms = 152;
 constexpr int64_t kMostShared = 96 * 1024;  // a CTA's dynamic shared memory
 constexpr int64_t kSliceBytes = 64 * 1024;   // three CTAs an SM
 
+// Clusters of a kernel that the device holds at once.  They lie within the device's
+// groups of SMs, so there may be fewer than its SMs have room for, and one more would
+// wait for the others' last row.  The driver's answers are kept: it takes 10 us for one.
+int64_t clusters_at_once(const void* kernel, int threads, int64_t smem, int ctas) {
+  struct Known {
+    const void* kernel;
+    int device, threads, ctas, clusters;
+    int64_t smem;
+  };
+  static std::mutex lock;
+  static Known known[64];
+  int device = 0;
+  cudaGetDevice(&device);
+  const size_t at = (reinterpret_cast<uintptr_t>(kernel) / 64 + size_t(smem) / 16 * 31 +
+                     size_t(threads + ctas + device)) % 64;
+  std::lock_guard<std::mutex> hold(lock);
+  Known& k = known[at];
+  if (k.kernel == kernel && k.device == device && k.threads == threads && k.ctas == ctas &&
+      k.smem == smem)
+    return k.clusters;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(ctas));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = size_t(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = unsigned(ctas);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int clusters = 0;
+  if (cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) clusters = 1;
+  k = Known{kernel, device, threads, ctas, std::max(1, clusters), smem};
+  return k.clusters;
+}
+
 // Launches the kernel for rows that stay in shared memory, if one holds them; sets `done`.
 cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   *done = false;
@@ -175,7 +213,10 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   const int64_t resident = std::max<int64_t>(
       1, std::min<int64_t>(std::min(24, 3 * kDistillThreads / threads),
                            (227 * 1024) / (smem + 8 * 1024)));
-  const int64_t clusters = std::min<int64_t>(a.n_rows, std::max<int64_t>(1, resident * kSms / a.ctas));
+  int64_t clusters = resident * kSms;
+  if (a.ctas > 1)
+    clusters = std::min(clusters / a.ctas, clusters_at_once(f, threads, smem, a.ctas));
+  clusters = std::min<int64_t>(a.n_rows, std::max<int64_t>(1, clusters));
   *done = true;
   return launch(kernel, dim3(unsigned(clusters * a.ctas)), threads, size_t(smem), stream, true,
                 a.ctas, a);

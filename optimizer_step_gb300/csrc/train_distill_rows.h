@@ -178,8 +178,9 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   const int run = (a.slice + share - 1) / share * kWarp;
   const int at0 = rank * a.slice;  // the slice's first unit
   const auto first_of = [&](int part) { return (part * warps + warp) * run; };
+  const bool ends = a.phase != 0 || a.row_phase != 0 || vocab % E != 0;
   const auto head_of = [&](int64_t row) {
-    return (E - (a.phase + int(row % E) * a.row_phase) % E) % E;
+    return ends ? (E - (a.phase + int(row % E) * a.row_phase) % E) % E : 0;
   };
   const auto row_of = [&](int64_t row) {
     return static_cast<const TZ*>(a.logits) + row * a.stride;
@@ -222,39 +223,43 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   int64_t entry = -1;
   float entry_t = 0.f;
   int64_t row = int64_t(blockIdx.x) / a.ctas;
+  bool live = false;
   if (row < a.n_rows) {
     look(row, label, up);
+    live = live_of(label, up);
     if (has_entry) entry_of(row, tid, entry, entry_t);
     const int head = head_of(row);
-    const int mine = live_of(label, up) ? mine_of((vocab - head) / E) : 0;
+    const int mine = live ? mine_of((vocab - head) / E) : 0;
     for (int part = 0; part < kParts; ++part)
       copy_part(row_of(row) + head + int64_t(at0) * E, mine, part);
   }
   int parity = 0;
-  for (; row < a.n_rows; row += step, parity ^= 1) {
+  const TZ* z = row_of(row);
+  TG* grad = GRAD ? static_cast<TG*>(a.grad) + row * a.grad_stride : nullptr;
+  const int64_t step_z = step * a.stride, step_grad = GRAD ? step * a.grad_stride : 0;
+  for (; row < a.n_rows; row += step, parity ^= 1, z += step_z, grad += step_grad) {
     int32_t* id = reinterpret_cast<int32_t*>(lists) + parity * 3 * room;
     float* coef = reinterpret_cast<float*>(id + room);
     float* zed = coef + room;
-    const TZ* z = row_of(row);
-    TG* grad = GRAD ? static_cast<TG*>(a.grad) + row * a.grad_stride : nullptr;
     const int head = head_of(row), units = (vocab - head) / E;
     const int mine = mine_of(units);  // units here; < 0: none
-    const bool live = live_of(label, up);
     // The next row.
     const int64_t next = row + step;
     int64_t next_label = -1;
     float next_up = 0.f;
-    const TZ* next_from = row_of(next) + int64_t(at0) * E;
+    const TZ* next_from = z + step_z + int64_t(at0) * E;
+    bool next_live = false;
     int next_mine = 0;  // none if it is not read
     if (next < a.n_rows) {
       look(next, next_label, next_up);
       const int next_head = head_of(next);
       next_from += next_head;
-      if (live_of(next_label, next_up)) next_mine = mine_of((vocab - next_head) / E);
+      next_live = live_of(next_label, next_up);
+      if (next_live) next_mine = mine_of((vocab - next_head) / E);
     }
     // The column of this thread's single element, if it has one.
     int single = -1;
-    if (rank == 0 && tid < kWarp) {
+    if (ends && rank == 0 && tid < kWarp) {
       if (tid < head) single = tid;
       else if (kWarp - 1 - tid < (vocab - head) % E) single = vocab - kWarp + tid;
     }
@@ -415,8 +420,8 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     if constexpr (GRAD) {
       const bool zero = !work || up == 0.f;
       float w[N];  // weights of the exponentials
-      w[0] = soft && any ? up * a.soft_weight * a.temperature / soft_sum : 0.f;
-      w[N - 1] = (N == 1 ? w[0] : 0.f) + (hard ? up * a.hard_weight / hard_sum : 0.f);
+      w[0] = soft && any ? __fdividef(up * a.soft_weight * a.temperature, soft_sum) : 0.f;
+      w[N - 1] = (N == 1 ? w[0] : 0.f) + (hard ? __fdividef(up * a.hard_weight, hard_sum) : 0.f);
       const auto smooth = [&](F2 v) {
         const F2 d = add2(v, pair(-top));
         const F2 e = exp2_of(mul2(d, pair(c[0])));
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
       if (work && hard) loss += a.hard_weight * (logf(hard_sum) - (zed[a.top_k] - top));
       a.loss[row] = loss;
     }
-    label = next_label, up = next_up;
+    label = next_label, up = next_up, live = next_live;
   }
   // No CTA leaves while another may store into it.
   if (a.ctas > 1) cluster.sync();
