@@ -257,6 +257,11 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
       next_live = live_of(next_label, next_up);
       if (next_live) next_mine = mine_of((vocab - next_head) / E);
     }
+    // It is on its way to L2 from here on, and to shared memory as room is made there.
+    if (tid == 0 && next_mine > 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next_from),
+                   "r"(next_mine * 16)
+                   : "memory");
     // The column of this thread's single element, if it has one.
     int single = -1;
     if (ends && rank == 0 && tid < kWarp) {
@@ -309,10 +314,15 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
         const int first = first_of(part), end = min(mine, first + run);
         for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
           Unit<ZT> x[kAtOnce];
+          if (i + (kAtOnce - 1) * kWarp < end) {
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            x[k].none();
-            if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
+            for (int k = 0; k < kAtOnce; ++k) x[k].q = slot[i + k * kWarp];
+          } else {
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+              x[k].none();
+              if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
+            }
           }
           sums.raise(fmaxf(sums.top, largest(x)), c);
           const F2 down = pair(-sums.top);
@@ -450,10 +460,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
             for (int i = first + lane; i < end; i += U * kWarp, out += U * kWarp * E) {
               Unit<ZT> x[U];
 #pragma unroll
-              for (int k = 0; k < U; ++k) {
-                x[k].none();
-                if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
-              }
+              for (int k = 0; k < U; ++k) x[k].q = slot[min(i + k * kWarp, end - 1)];
 #pragma unroll
               for (int k = 0; k < U; ++k) {
                 Pack<GT, E> g;
