@@ -125,7 +125,6 @@ struct Sums {
 constexpr int kDistillThreads = 256;
 constexpr int kDistillWarps = kDistillThreads / kWarp;
 constexpr int kMostCtas = 16;
-constexpr int kParts = 2;   // of a row, each waited for by itself
 constexpr int kAtOnce = 4;  // units a thread reads together
 
 // A row's slice is copied into shared memory asynchronously, in units of 16 bytes, and
@@ -173,11 +172,10 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   pdl_wait();
 
   const int64_t step = int64_t(gridDim.x) / a.ctas;
-  // Of a slice's kParts parts each warp has a run of `run` units, 32 side by side at a time.
-  const int share = kParts * warps * kWarp;
-  const int run = (a.slice + share - 1) / share * kWarp;
+  // Each warp has a run of a slice's units, 32 side by side at a time.
+  const int run = (a.slice + threads - 1) / threads * kWarp;
+  const int first = warp * run;
   const int at0 = rank * a.slice;  // the slice's first unit
-  const auto first_of = [&](int part) { return (part * warps + warp) * run; };
   const bool ends = a.phase != 0 || a.row_phase != 0 || vocab % E != 0;
   const auto head_of = [&](int64_t row) {
     return ends ? (E - (a.phase + int(row % E) * a.row_phase) % E) % E : 0;
@@ -197,8 +195,8 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
            (soft || hard) && (a.loss || up != 0.f);
   };
   const auto mine_of = [&](int units) { return min(a.slice, units - at0); };
-  const auto copy_part = [&](const TZ* from, int mine, int part) {
-    const int first = first_of(part), end = min(mine, first + run);
+  const auto copy = [&](const TZ* from, int mine) {
+    const int end = min(mine, first + run);
     uint32_t to = slot_address + (first + lane) * 16;
     from += (first + lane) * E;
     for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
@@ -230,8 +228,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     if (has_entry) entry_of(row, tid, entry, entry_t);
     const int head = head_of(row);
     const int mine = live ? mine_of((vocab - head) / E) : 0;
-    for (int part = 0; part < kParts; ++part)
-      copy_part(row_of(row) + head + int64_t(at0) * E, mine, part);
+    copy(row_of(row) + head + int64_t(at0) * E, mine);
   }
   int parity = 0;
   const TZ* z = row_of(row);
@@ -257,11 +254,6 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
       next_live = live_of(next_label, next_up);
       if (next_live) next_mine = mine_of((vocab - next_head) / E);
     }
-    // It is on its way to L2 from here on, and to shared memory as room is made there.
-    if (tid == 0 && next_mine > 0)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next_from),
-                   "r"(next_mine * 16)
-                   : "memory");
     // The column of this thread's single element, if it has one.
     int single = -1;
     if (ends && rank == 0 && tid < kWarp) {
@@ -304,46 +296,39 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     // The largest value and the sums.
     Sums<TERMS> sums;
     if (live) {
-      for (int part = 0; part < kParts; ++part) {
-        if constexpr (GRAD) {
-          if (part == 0) copy_wait<kParts - 1>();
-          else copy_wait<0>();
+      copy_wait<0>();
+      const int end = min(mine, first + run);
+      for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
+        Unit<ZT> x[kAtOnce];
+        if (i + (kAtOnce - 1) * kWarp < end) {
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) x[k].q = slot[i + k * kWarp];
         } else {
-          copy_wait<kParts - 1>();
-        }
-        const int first = first_of(part), end = min(mine, first + run);
-        for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
-          Unit<ZT> x[kAtOnce];
-          if (i + (kAtOnce - 1) * kWarp < end) {
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) x[k].q = slot[i + k * kWarp];
-          } else {
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-              x[k].none();
-              if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
-            }
+          for (int k = 0; k < kAtOnce; ++k) {
+            x[k].none();
+            if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
           }
-          sums.raise(fmaxf(sums.top, largest(x)), c);
-          const F2 down = pair(-sums.top);
-          F2 t[N];
-#pragma unroll
-          for (int n = 0; n < N; ++n) t[n] = pair(sums.s[n], 0.f);
-#pragma unroll
-          for (int k = 0; k < kAtOnce; ++k)
-#pragma unroll
-            for (int h = 0; h < E / 2; ++h) {
-              const F2 d = add2(x[k].get(h), down);
-              const F2 e = exp2_of(mul2(d, pair(c[0])));
-              t[0] = add2(t[0], e);
-              if constexpr (TERMS == kTwo) t[1] = add2(t[1], exp2_of(mul2(d, pair(c[1]))));
-              if constexpr (TERMS == kSquares) t[1] = fma2(e, e, t[1]);
-            }
-#pragma unroll
-          for (int n = 0; n < N; ++n) sums.s[n] = sum2(t[n]);
         }
-        if constexpr (!GRAD) copy_part(next_from, next_mine, part);
+        sums.raise(fmaxf(sums.top, largest(x)), c);
+        const F2 down = pair(-sums.top);
+        F2 t[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) t[n] = pair(sums.s[n], 0.f);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+          for (int h = 0; h < E / 2; ++h) {
+            const F2 d = add2(x[k].get(h), down);
+            const F2 e = exp2_of(mul2(d, pair(c[0])));
+            t[0] = add2(t[0], e);
+            if constexpr (TERMS == kTwo) t[1] = add2(t[1], exp2_of(mul2(d, pair(c[1]))));
+            if constexpr (TERMS == kSquares) t[1] = fma2(e, e, t[1]);
+          }
+#pragma unroll
+        for (int n = 0; n < N; ++n) sums.s[n] = sum2(t[n]);
       }
+      if constexpr (!GRAD) copy(next_from, next_mine);
       if (single >= 0) {
         sums.raise(fmaxf(sums.top, edge), c);
         float f[N];
@@ -352,7 +337,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
         for (int n = 0; n < N; ++n) sums.s[n] += f[n];
       }
     } else if (!GRAD) {
-      for (int part = 0; part < kParts; ++part) copy_part(next_from, next_mine, part);
+      copy(next_from, next_mine);
     }
     // Over the warps of the row's CTAs; the teacher's, which each CTA has, over its own.
     const auto join_teacher = [&](int lanes) {
@@ -376,6 +361,11 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     }
     if (a.ctas > 1) cluster.sync();
     else __syncthreads();
+    // The next row is on its way to L2 from here on, and to shared memory as room is made there.
+    if (tid == 0 && next_mine > 0)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next_from),
+                   "r"(next_mine * 16)
+                   : "memory");
     if (soft) {
       best = -INFINITY, size = 0.f;
       if ((lane & (warps - 1)) < entry_warps) {
@@ -448,37 +438,35 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
       };
       TG* to = grad + head + int64_t(at0) * E;
       if (a.whole) {
-        for (int part = 0; part < kParts; ++part) {
-          const int first = first_of(part), end = min(mine, first + run);
-          TG* out = to + (first + lane) * E;
-          if (zero) {
-            Pack<GT, E> g;
-            g.clear();
-            for (int i = first + lane; i < end; i += kWarp, out += kWarp * E) g.store(out);
-          } else {
-            constexpr int U = 2;
-            for (int i = first + lane; i < end; i += U * kWarp, out += U * kWarp * E) {
-              Unit<ZT> x[U];
+        const int end = min(mine, first + run);
+        TG* out = to + (first + lane) * E;
+        if (zero) {
+          Pack<GT, E> g;
+          g.clear();
+          for (int i = first + lane; i < end; i += kWarp, out += kWarp * E) g.store(out);
+        } else {
+          constexpr int U = 2;
+          for (int i = first + lane; i < end; i += U * kWarp, out += U * kWarp * E) {
+            Unit<ZT> x[U];
 #pragma unroll
-              for (int k = 0; k < U; ++k) x[k].q = slot[min(i + k * kWarp, end - 1)];
+            for (int k = 0; k < U; ++k) x[k].q = slot[min(i + k * kWarp, end - 1)];
 #pragma unroll
-              for (int k = 0; k < U; ++k) {
-                Pack<GT, E> g;
+            for (int k = 0; k < U; ++k) {
+              Pack<GT, E> g;
 #pragma unroll
-                for (int h = 0; h < E / 2; ++h) set2(g, h, smooth(x[k].get(h)));
-                if (i + k * kWarp < end) g.store(out + k * (kWarp * E));
-              }
+              for (int h = 0; h < E / 2; ++h) set2(g, h, smooth(x[k].get(h)));
+              if (i + k * kWarp < end) g.store(out + k * (kWarp * E));
             }
           }
-          copy_part(next_from, next_mine, part);
         }
+        copy(next_from, next_mine);
       } else {
         // Element by element; the next row may come when all are through.
         const TZ* from = reinterpret_cast<const TZ*>(slot);
         for (int i = tid; i < mine * E; i += threads)
           to[i] = zero ? TG(0) : from_float<GT>(smooth1(to_float<ZT>(from[i])));
         __syncthreads();
-        for (int part = 0; part < kParts; ++part) copy_part(next_from, next_mine, part);
+        copy(next_from, next_mine);
       }
       if (single >= 0) grad[single] = zero ? TG(0) : from_float<GT>(smooth1(edge));
       __syncthreads();
