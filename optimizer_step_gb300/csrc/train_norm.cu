@@ -142,16 +142,17 @@ cudaError_t launch_rows(NormArgs& a, int32_t x_dtype, int32_t y_dtype, cudaStrea
   }
   // Element by element.
   int s = 0;
-  while (s < 2 && dim > kScalars[s] * kWarp) ++s;
+  while (s < 3 && dim > kScalars[s] * kWarp) ++s;
   a.lanes = int32_t((dim + kScalars[s] * kWarp - 1) / (kScalars[s] * kWarp)) * kWarp;
   // Threads without elements read behind the staged vectors' ends.
   const int64_t smem = params + int64_t(kScalars[s]) * kWarp * 4;
   if (a.lanes > 512 || smem > kMostShared) return cudaSuccess;
-  int64_t groups = std::max<int64_t>(1, std::min<int64_t>(256 / a.lanes, a.n_rows));
+  const int64_t rows = (a.n_rows + kScalarRows[s] - 1) / kScalarRows[s];
+  int64_t groups = std::max<int64_t>(1, std::min<int64_t>(256 / a.lanes, rows));
   const int64_t resident =
       std::max<int64_t>(1, std::min<int64_t>(1024 / (groups * a.lanes), kMostShared / smem));
-  return go(k.scalar[a.lanes > kWarp ? 3 : s],
-            std::min(resident * kSms, (a.n_rows + groups - 1) / groups),
+  return go(k.scalar[a.lanes > kWarp ? 4 : s],
+            std::min(resident * kSms, (rows + groups - 1) / groups),
             int(groups * a.lanes), smem);
 }
 

@@ -221,16 +221,18 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
     a.period = 1;
   }
   // Element by element.
-  const int s = dim <= kGradScalars[0] * kWarp ? 0 : 1;
+  int s = 0;
+  while (s < 2 && dim > kGradScalars[s] * kWarp) ++s;
+  const int64_t rows = (a.n_rows + kGradScalarRows[s] - 1) / kGradScalarRows[s];
   const int64_t span = kGradScalars[s] * kWarp;
   a.lanes = int32_t((dim + span - 1) / span) * kWarp;
   if (a.lanes > 512 || dim * 8 > kMostShared) return cudaSuccess;
   int64_t groups = std::max<int64_t>(1, std::min<int64_t>(512 / a.lanes, a.lanes > kWarp ? 15 : 16));
   const int64_t spread = a.joined ? kJoined : kSms;
-  groups = std::min(groups, (a.n_rows + spread - 1) / spread);
+  groups = std::min(groups, (rows + spread - 1) / spread);
   while (groups > 1 && groups * dim * 8 > kMostShared) --groups;
-  return go(k.scalar[a.lanes > kWarp ? 2 : s],
-            std::min<int64_t>(kSms, (a.n_rows + groups - 1) / groups), groups, 0);
+  return go(k.scalar[a.lanes > kWarp ? 3 : s],
+            std::min<int64_t>(kSms, (rows + groups - 1) / groups), groups, 0);
 }
 
 constexpr int64_t kMaxElements = int64_t(1) << 40;

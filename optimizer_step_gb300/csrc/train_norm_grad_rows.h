@@ -327,14 +327,15 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
   write_sums(a, reinterpret_cast<float*>(smem), groups);
 }
 
-// Element by element, M a thread, straight from memory: for rows of x, grad_out and
-// x_grad that do not begin equally far from a unit's boundary, and short odd ones.
-template <int XT, int YT, int M, Span S>
+// Element by element, M a thread and R rows at once, straight from memory: for rows of x,
+// grad_out and x_grad that do not begin equally far from a unit's boundary, and short odd
+// ones.
+template <int XT, int YT, int M, int R, Span S>
 __global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant__ NormGradArgs a) {
   using TX = typename TypeOf<XT>::T;
   using TY = typename TypeOf<YT>::T;
   extern __shared__ __align__(16) unsigned char smem[];
-  __shared__ float part[4 * kWarp];
+  __shared__ float part[8 * kWarp];
   const int tid = threadIdx.x;
   const int lanes = S == Span::kWarp ? kWarp : a.lanes;
   const int groups = int(blockDim.x) / lanes, index = tid / lanes;
@@ -346,34 +347,50 @@ __global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant_
   float w[M], dw[M] = {}, db[M] = {};
   load_weight(a, w, [&](int i) { return i * kWarp < left ? first + i * kWarp : -1; });
   const float inv = 1.f / float(dim);
-  const int64_t step = int64_t(gridDim.x) * groups;
+  const int64_t step = int64_t(gridDim.x) * groups * R;
   int parity = 0;
-  for (int64_t row = int64_t(blockIdx.x) * groups + index; row < a.n_rows; row += step) {
-    const float mean = a.stats[row], rstd = a.stats[a.n_rows + row];
+  for (int64_t row = (int64_t(blockIdx.x) * groups + index) * R; row < a.n_rows; row += step) {
+    const int rows = int(min(int64_t(R), a.n_rows - row));
     const TX* px = static_cast<const TX*>(a.x) + row * a.x_stride + first;
     const TY* py = static_cast<const TY*>(a.dy) + row * a.dy_stride + first;
-    float x[M], y[M], s = 0.f, t = 0.f;
+    float x[R][M], y[R][M], mean[R], rstd[R], along[2 * R];
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      x[m] = y[m] = 0.f;
-      if (m * kWarp < left) x[m] = to_float<XT>(px[m * kWarp]), y[m] = to_float<YT>(py[m * kWarp]);
+    for (int r = 0; r < R; ++r) {
+      mean[r] = rstd[r] = 0.f;
+      if (r < rows) mean[r] = a.stats[row + r], rstd[r] = a.stats[a.n_rows + row + r];
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        x[r][m] = y[r][m] = 0.f;
+        if (r < rows && m * kWarp < left)
+          x[r][m] = to_float<XT>(px[m * kWarp]), y[r][m] = to_float<YT>(py[m * kWarp]);
+      }
+      px += a.x_stride, py += a.dy_stride;
     }
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      x[m] = m * kWarp < left ? (x[m] - mean) * rstd : 0.f;
-      db[m] += y[m], dw[m] += y[m] * x[m];
-      y[m] *= w[m];
-      s += y[m], t += y[m] * x[m];
+    for (int r = 0; r < R; ++r) {
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        x[r][m] = r < rows && m * kWarp < left ? (x[r][m] - mean[r]) * rstd[r] : 0.f;
+        db[m] += y[r][m], dw[m] += y[r][m] * x[r][m];
+        y[r][m] *= w[m];
+        s += y[r][m], t += y[r][m] * x[r][m];
+      }
+      along[2 * r] = s, along[2 * r + 1] = t;
     }
     if (a.dx) {
-      float along[2] = {s, t};
       g.sums<S>(along, parity);
       parity ^= 1;
-      s = along[0] * inv, t = along[1] * inv;
       TX* to = static_cast<TX*>(a.dx) + row * a.dx_stride + first;
 #pragma unroll
-      for (int m = 0; m < M; ++m)
-        if (m * kWarp < left) to[m * kWarp] = from_float<XT>(rstd * (y[m] - s - x[m] * t));
+      for (int r = 0; r < R; ++r, to += a.dx_stride) {
+        if (r >= rows) break;
+        const float s = along[2 * r] * inv, t = along[2 * r + 1] * inv;
+#pragma unroll
+        for (int m = 0; m < M; ++m)
+          if (m * kWarp < left)
+            to[m * kWarp] = from_float<XT>(rstd[r] * (y[r][m] - s - x[r][m] * t));
+      }
     }
   }
   if (!a.partial && !a.joined) return;
@@ -387,11 +404,12 @@ __global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant_
 
 // The kernels of two types.
 using NormGradKernel = void (*)(NormGradArgs);
-constexpr int kGradScalars[2] = {8, 16};  // elements a thread
+constexpr int kGradScalars[3] = {2, 8, 16};    // elements a thread
+constexpr int kGradScalarRows[3] = {2, 2, 1};  // rows at once
 struct NormGradKernels {
   // Part of a warp or a warp with 8 elements a thread, a warp with 16, several with 16 or 24.
   NormGradKernel ring[5];
-  NormGradKernel scalar[3];  // a warp with 8 or 16 elements a thread, several with 16
+  NormGradKernel scalar[4];  // a warp with 2, 8 or 16 elements a thread, several with 16
 };
 template <int XT, int YT>
 constexpr NormGradKernels norm_grad_kernels() {
@@ -400,8 +418,10 @@ constexpr NormGradKernels norm_grad_kernels() {
            grad_ring_kernel<XT, YT, 2 * M, grad_rows(16), Span::kWarp, false>,
            grad_ring_kernel<XT, YT, 2 * M, grad_rows(16), Span::kWarps, false>,
            grad_ring_kernel<XT, YT, 3 * M, grad_rows(24), Span::kWarps, true>},
-          {grad_scalar_kernel<XT, YT, 8, Span::kWarp>, grad_scalar_kernel<XT, YT, 16, Span::kWarp>,
-           grad_scalar_kernel<XT, YT, 16, Span::kWarps>}};
+          {grad_scalar_kernel<XT, YT, kGradScalars[0], kGradScalarRows[0], Span::kWarp>,
+           grad_scalar_kernel<XT, YT, kGradScalars[1], kGradScalarRows[1], Span::kWarp>,
+           grad_scalar_kernel<XT, YT, kGradScalars[2], kGradScalarRows[2], Span::kWarp>,
+           grad_scalar_kernel<XT, YT, kGradScalars[2], kGradScalarRows[2], Span::kWarps>}};
 }
 
 // Each defined in a translation unit of its own.

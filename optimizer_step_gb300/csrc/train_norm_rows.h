@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(kNormThreads)
 
 // ------------------------------------------------------- rows element by element
 // For rows of x and y that do not begin equally far from a unit's boundary, and short
-// ones of odd widths: M elements a thread, in registers.
-template <int XT, int YT, int M, Span S>
-__global__ void __launch_bounds__(512) norm_scalar_kernel(const __grid_constant__ NormArgs a) {
+// ones of odd widths: M elements a thread and R rows at once, in registers.
+template <int XT, int YT, int M, int R, Span S>
+__global__ void __launch_bounds__(512, M > 8 ? 0 : 2) norm_scalar_kernel(const __grid_constant__ NormArgs a) {
   using TX = typename TypeOf<XT>::T;
   using TY = typename TypeOf<YT>::T;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -347,45 +347,68 @@ __global__ void __launch_bounds__(512) norm_scalar_kernel(const __grid_constant_
   pdl_wait();
   stage_params<1>(a, 0, staged);
   const float inv = 1.f / float(dim);
-  const int64_t step = int64_t(gridDim.x) * groups;
-  for (int64_t row = int64_t(blockIdx.x) * groups + index; row < a.n_rows; row += step) {
+  const float* w = staged + staged_at<1>(first, width);
+  const int64_t step = int64_t(gridDim.x) * groups * R;
+  for (int64_t row = (int64_t(blockIdx.x) * groups + index) * R; row < a.n_rows; row += step) {
+    const int rows = int(min(int64_t(R), a.n_rows - row));
     const TX* from = static_cast<const TX*>(a.x) + row * a.x_stride + first;
-    float v[M], s = 0.f, t = 0.f;
+    float v[R][M], mean[R], var[R];
 #pragma unroll
-    for (int m = 0; m < M; ++m) v[m] = m * kWarp < left ? to_float<XT>(from[m * kWarp]) : 0.f;
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
-    for (int m = 0; m < M; m += 2) s += v[m], t += v[m + 1];
-    const float mean = g.sum<S>(s + t, 0) * inv;
-    s = t = 0.f;
-#pragma unroll
-    for (int m = 0; m < M; ++m) {
-      v[m] = m * kWarp < left ? v[m] - mean : 0.f;
-      if (m & 1) s += v[m] * v[m];
-      else t += v[m] * v[m];
+      for (int m = 0; m < M; ++m)
+        v[r][m] = r < rows && m * kWarp < left ? to_float<XT>(from[m * kWarp]) : 0.f;
+      from += a.x_stride;
     }
-    const float var = g.sum<S>(s + t, 1) * inv;
-    if (!in_range(var, a.eps)) {
-      scaled_row<XT, YT, S>(a, row, true, g);
-      continue;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int m = 0; m < M; m += 2) s += v[r][m], t += v[r][m + 1];
+      mean[r] = s + t;
     }
-    const float rstd = rstd_of(var, a.eps);
-    if (a.stats && g.lane == 0) a.stats[row] = mean, a.stats[a.n_rows + row] = rstd;
+#pragma unroll
+    for (int r = 0; r < R; ++r) mean[r] = g.sum<S>(mean[r], 0) * inv;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float s = 0.f, t = 0.f;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        v[r][m] = m * kWarp < left ? v[r][m] - mean[r] : 0.f;
+        if (m & 1) s += v[r][m] * v[r][m];
+        else t += v[r][m] * v[r][m];
+      }
+      var[r] = s + t;
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) var[r] = g.sum<S>(var[r], 1) * inv;
     TY* y = static_cast<TY*>(a.y) + row * a.y_stride + first;
-    const float* w = staged + staged_at<1>(first, width);
 #pragma unroll
-    for (int m = 0; m < M; ++m)
-      if (m * kWarp < left)
-        y[m * kWarp] = from_float<YT>(v[m] * rstd * w[m * kWarp] + w[width + m * kWarp]);
+    for (int r = 0; r < R; ++r, y += a.y_stride) {
+      if (r >= rows) break;
+      if (!in_range(var[r], a.eps)) {
+        scaled_row<XT, YT, S>(a, row + r, true, g);
+        continue;
+      }
+      const float rstd = rstd_of(var[r], a.eps);
+      if (a.stats && g.lane == 0)
+        a.stats[row + r] = mean[r], a.stats[a.n_rows + row + r] = rstd;
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        if (m * kWarp < left)
+          y[m * kWarp] = from_float<YT>(v[r][m] * rstd * w[m * kWarp] + w[width + m * kWarp]);
+    }
   }
 }
 
 // The kernels of two types.
 using NormKernel = void (*)(NormArgs);
-constexpr int kScalars[3] = {2, 8, 32};  // elements a thread
+constexpr int kScalars[4] = {2, 4, 8, 32};     // elements a thread
+constexpr int kScalarRows[4] = {2, 2, 1, 1};  // rows at once
 struct NormKernels {
   NormKernel whole;       // short rows of whole units of 16 bytes of the wider type
   NormKernel ring[3];     // a warp with 16 or 32 elements a thread, several warps with 32
-  NormKernel scalar[4];   // a warp with kScalars elements a thread, several with 32
+  NormKernel scalar[5];   // a warp with kScalars elements a thread, several with 32
 };
 template <int XT, int YT>
 constexpr NormKernels norm_kernels() {
@@ -394,10 +417,11 @@ constexpr NormKernels norm_kernels() {
   return {norm_short_kernel<XT, YT, E, 4>,
           {norm_ring_kernel<XT, YT, M, Span::kWarp>, norm_ring_kernel<XT, YT, 2 * M, Span::kWarp>,
            norm_ring_kernel<XT, YT, 2 * M, Span::kWarps>},
-          {norm_scalar_kernel<XT, YT, kScalars[0], Span::kWarp>,
-           norm_scalar_kernel<XT, YT, kScalars[1], Span::kWarp>,
-           norm_scalar_kernel<XT, YT, kScalars[2], Span::kWarp>,
-           norm_scalar_kernel<XT, YT, kScalars[2], Span::kWarps>}};
+          {norm_scalar_kernel<XT, YT, kScalars[0], kScalarRows[0], Span::kWarp>,
+           norm_scalar_kernel<XT, YT, kScalars[1], kScalarRows[1], Span::kWarp>,
+           norm_scalar_kernel<XT, YT, kScalars[2], kScalarRows[2], Span::kWarp>,
+           norm_scalar_kernel<XT, YT, kScalars[3], kScalarRows[3], Span::kWarp>,
+           norm_scalar_kernel<XT, YT, kScalars[3], kScalarRows[3], Span::kWarps>}};
 }
 
 // Each defined in a translation unit of its own.
