@@ -1,7 +1,8 @@
 """A small language model trained with the operators around the LAMB step.
 
 Next-token prediction with a tied embedding: the lookup starts the forward
-pass, one hidden layer follows, and the table is the output head too.  Every
+pass, one hidden layer follows, and the table is the output head too, whose
+logits the loss turns into their gradient.  Every
 step sums the grads of a few micro-batches in fp32, where the table gets two
 contributions: the head's product, and on top of it the lookup's gradient by
 sorted tokens.  GradClip takes the fp32 sums to the bf16 grads that the step
@@ -20,7 +21,8 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
-from optimizer_step_gb300 import GradClip, Lamb, embed, embed_grad  # noqa: E402
+from optimizer_step_gb300 import (GradClip, Lamb, distill_loss_grad, embed,  # noqa: E402
+                                  embed_grad)
 
 ALIGN = 64  # elements between tensor starts
 
@@ -65,16 +67,14 @@ class TiedLM:
         x = embed(table, ids, scale=self.scale)
         h = torch.tanh((x @ hidden_w).float())
         y = (x.float() + h).to(torch.bfloat16)
-        logits = (y @ table.t()).float()
-        # The loss and its gradient.
+        logits = y @ table.t()
+        # The loss and its gradient, in place of the logits.
         used = targets != self.padding_id
         count = used.sum().clamp(min=1)
-        log_p = torch.log_softmax(logits, dim=-1)
-        picked = log_p.gather(-1, targets[..., None]).squeeze(-1)
-        loss = -(picked * used).sum() / count
-        d_logits = log_p.exp()
-        d_logits.scatter_add_(-1, targets[..., None], torch.full_like(picked, -1.0)[..., None])
-        d_logits = (d_logits * (used[..., None] * (weight / count))).to(torch.bfloat16)
+        losses, d_logits = distill_loss_grad(
+            logits, None, None, targets, hard_weight=1.0, ignore_id=self.padding_id,
+            row_grad=used * (weight / count), out=logits)
+        loss = losses.sum() / count
         # Backwards through the head, the hidden layer and the lookup.
         rows = d_logits.reshape(-1, self.vocab)
         flat_x, flat_y = x.reshape(-1, self.width), y.reshape(-1, self.width)

@@ -84,7 +84,8 @@ def distill_loss(logits: torch.Tensor, top_ids: torch.Tensor | None,
     the vocabulary, is left out: its loss and gradient are 0, whatever it holds.
 
     If ``logits`` require grad, so does the result; it can be differentiated once.
-    The teacher gets no gradient.
+    The teacher gets no gradient.  As with torch's own operators, a backward pass that is
+    captured into a CUDA graph needs leaves that no eager result still alive depends on.
     """
     args, index = _arguments(logits, top_ids, top_logits, labels, temperature, soft_weight,
                              hard_weight, ignore_id)

@@ -112,7 +112,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     eps)``, which ``layer_norm_grad`` takes.
 
     If ``x``, ``weight`` or ``bias`` requires grad, so does the result.  It can be
-    differentiated once, and ``out`` is refused then.  ``stats`` have no gradient.
+    differentiated once, and ``out`` is refused then.  ``stats`` have no gradient.  As
+    with torch's own operators, a backward pass that is captured into a CUDA graph needs
+    leaves that no eager result still alive depends on.
     """
     code, rows, dim, stride, index = _matrix("x", x)
     w_ptr = b_ptr = None

@@ -235,7 +235,7 @@ def test_in_place(dim):
         assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
-@pytest.mark.parametrize("dim", [24, 1023, 2048, 12288, 40001])
+@pytest.mark.parametrize("dim", [24, 33, 100, 250, 1023, 2048, 12288, 40001])
 @pytest.mark.parametrize("dtype,mean,std", [
     (FP32, 1000.0, 1.0), (FP32, -3e4, 0.1), (BF16, 100.0, 3.0), (FP32, 0.0, 1e-6),
     (FP32, 0.0, 1e19), (FP32, 1e30, 1e25), (BF16, 0.0, 2e37), (FP32, 4e37, 1e37), (FP16, 0, 1e4)])
@@ -246,7 +246,7 @@ def test_rows_far_from_zero_large_and_small(dim, dtype, mean, std):
         check_forward(x, None, None, eps, y, stats)
 
 
-@pytest.mark.parametrize("dim", [24, 1023, 2048, 12288, 40001])
+@pytest.mark.parametrize("dim", [24, 33, 100, 250, 1023, 2048, 12288, 40001])
 def test_small_rows_without_eps(dim):
     """Squares below fp32's range count where no eps covers them."""
     x = randn((40, dim), FP32, 5).mul(1e-30)
@@ -279,6 +279,42 @@ def test_inf_and_nan_stay_in_their_rows(dim, bad):
     assert bool(dx[4].isnan().all()) and bool(dw.isnan().all())
     check_backward(dy[keep], x[keep], None, stats[:, keep].contiguous(), (dx[keep], None, None))
     check_backward(dy, x, None, torch.zeros_like(stats), (None, None, db))
+
+
+@pytest.mark.parametrize("dim", [24, 33, 1023, 4096])
+@pytest.mark.parametrize("scale", [1e30, 1e-25])
+def test_scaled_rows_among_others(dim, scale):
+    """One row in three leaves fp32's squares; its neighbours keep their bits."""
+    x = randn((50, dim), FP32, 5)
+    plain, _ = og.layer_norm(x, stats=True, eps=1e-30)
+    x[::3] *= scale
+    y, stats = og.layer_norm(x, stats=True, eps=1e-30)
+    check_forward(x, None, None, 1e-30, y, stats)
+    keep = torch.arange(50, device="cuda") % 3 != 0
+    assert torch.equal(y[keep], plain[keep])
+
+
+@pytest.mark.parametrize("dim", [24, 33, 1023, 4096, 12288])
+@pytest.mark.parametrize("scale", [1e30, 1e-20])
+def test_backward_of_large_and_small_rows(dim, scale):
+    x, dy = randn((40, dim), FP32, 1).mul(scale), randn((40, dim), FP32, 2)
+    _, stats = og.layer_norm(x, stats=True, eps=1e-44)
+    got = og.layer_norm_grad(dy, x, None, stats)
+    check_backward(dy, x, None, stats, got)
+
+
+@pytest.mark.parametrize("n", [1, 3, 17, 500, 2000])
+@pytest.mark.parametrize("dim,pad", [(1000, 1), (300, 3), (4096, 5), (130, 3), (20, 1), (9000, 2)])
+def test_rows_apart_in_each_tensor(n, dim, pad):
+    """x, grad_out and x_grad begin differently from row to row."""
+    x, dy = randn((n, dim + pad), BF16, 1)[:, :dim], randn((n, dim), BF16, 2)
+    weight = randn((dim,), FP32, 3)
+    y, stats = og.layer_norm(x, weight, stats=True, out_dtype=FP32)
+    check_forward(x, weight, None, 1e-5, y, stats)
+    check_backward(dy, x, weight, stats, og.layer_norm_grad(dy, x, weight, stats))
+    dx = torch.empty((n, dim + pad), dtype=BF16, device="cuda")[:, :dim]
+    both = og.layer_norm_grad(torch.cat([dy, dy], 1)[:, dim:], x, weight, stats, x_grad=dx)
+    check_backward(dy, x, weight, stats, both)
 
 
 @pytest.mark.parametrize("n,dim", [(512, 256), (3000, 1023), (1000, 4096), (90, 40001)])
