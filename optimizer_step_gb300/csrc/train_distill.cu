@@ -63,12 +63,12 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
     const bool work = live && (any || hard) && (a.loss || up != 0.f);
     float top = -INFINITY, soft_sum = 0.f, hard_sum = 0.f;
     if (work) {
-      for (int j = tid; j < a.vocab; j += kThreads) top = fmaxf(top, to_float<ZT>(z[j]));
+      for (int64_t j = tid; j < a.vocab; j += kThreads) top = fmaxf(top, to_float<ZT>(z[j]));
     }
     top = cta_max<kThreads>(top, part[2]);
     const float c = a.inv_temperature * kLog2e;
     if (work) {
-      for (int j = tid; j < a.vocab; j += kThreads) {
+      for (int64_t j = tid; j < a.vocab; j += kThreads) {
         const float d = to_float<ZT>(z[j]) - top;
         if (any) soft_sum += exp2f(d * c);
         if (hard) hard_sum += exp2f(d * kLog2e);
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
         if (hard) g += ss * exp2f(d * kLog2e);
         return g;
       };
-      for (int j = tid; j < a.vocab; j += kThreads)
+      for (int64_t j = tid; j < a.vocab; j += kThreads)
         grad[j] = zero ? TG(0) : from_float<GT>(up * smooth(to_float<ZT>(z[j])));
       if (zero) return;
       __syncthreads();

@@ -92,6 +92,7 @@ cudaError_t launch_rows(NormArgs& a, int32_t x_dtype, int32_t y_dtype, cudaStrea
                         bool* done) {
   *done = false;
   const int64_t dim = a.dim;
+  if (dim > 32768) return cudaSuccess;
   const NormKernels& k = x_dtype == TRAIN_BF16   ? norm_kernels_bf16(y_dtype)
                          : x_dtype == TRAIN_FP16 ? norm_kernels_fp16(y_dtype)
                                                  : norm_kernels_fp32(y_dtype);

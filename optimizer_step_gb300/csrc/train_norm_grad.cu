@@ -141,6 +141,7 @@ int64_t most_pieces(int64_t n_rows, int64_t dim) {
 cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
   *pieces = 0;
   const int64_t dim = a.dim;
+  if (dim > 32768) return cudaSuccess;
   const NormGradKernels& k = a.x_type == TRAIN_BF16   ? norm_grad_kernels_bf16(a.dy_type)
                              : a.x_type == TRAIN_FP16 ? norm_grad_kernels_fp16(a.dy_type)
                                                       : norm_grad_kernels_fp32(a.dy_type);

@@ -173,6 +173,33 @@ def test_types(dtype, out, teacher, id_type):
         assert grad.dtype == out
 
 
+@pytest.mark.parametrize("ids,labels", [(torch.int32, torch.int64), (torch.int64, torch.int32)])
+def test_types_of_ids_and_labels(ids, labels):
+    data = Data(40, 3000, 12, BF16, FP32, ids)
+    data.labels = data.labels.to(labels)
+    data.labels[::5] = -7
+    check(data, 2.0, 0.5, 0.5, ignore=-7, row_grad=data.row_grad)
+
+
+@pytest.mark.parametrize("scale", [0.0, -2.0, 1024.0, 1e-30])
+def test_scales(scale):
+    check(Data(40, 3000, 12, FP32), 2.0, 0.5, 0.5, scale=scale)
+
+
+def test_more_rows_than_are_held_at_once_with_some_left_out():
+    """Each CTA walks through many rows; those left out come anywhere between."""
+    for vocab in (64, 1001, 40000):
+        n = 9000 if vocab < 2000 else 1500
+        data = Data(n, vocab, 3)
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(1)
+        data.labels[torch.rand(n, generator=gen, device="cuda") < 0.5] = -100
+        data.row_grad[torch.rand(n, generator=gen, device="cuda") < 0.3] = 0.0
+        data.ids[torch.rand(n, generator=gen, device="cuda") < 0.3] = -1
+        check(data, 2.0, 0.5, 0.5, row_grad=data.row_grad)
+        check(data, 2.0, 1.0, 0.0, row_grad=data.row_grad)
+
+
 @pytest.mark.parametrize("n", [0, 1, 2, 150, 153, 1000, 5003])
 @pytest.mark.parametrize("vocab", [40, 513, 3000])
 def test_rows(n, vocab):
@@ -510,8 +537,9 @@ def test_refusals():
 
 
 # ----------------------------------------------------------- streams and graphs
-def test_another_stream_and_captured_graphs():
-    data = Data(200, 4096, 16)
+@pytest.mark.parametrize("vocab", [4096, 131071])
+def test_another_stream_and_captured_graphs(vocab):
+    data = Data(200, vocab, 16)
 
     def calls():
         return og.distill_loss_grad(*data.args(), hard_weight=0.5, row_grad=data.row_grad)
@@ -528,7 +556,7 @@ def test_another_stream_and_captured_graphs():
             outs = calls()
         graphs.append((graph, outs))
     for k in range(4):
-        new = Data(200, 4096, 16, seed=k + 1)
+        new = Data(200, vocab, 16, seed=k + 1)
         for name in ("logits", "ids", "teacher", "labels", "row_grad"):
             getattr(data, name).copy_(getattr(new, name))
         graph, (loss, grad) = graphs[k % 2]
