@@ -8,7 +8,8 @@ namespace {
 // ------------------------------------------------------------ rows of any width
 constexpr int kWideThreads = 512;
 
-// dx, one CTA a row.
+// For rows wider than 12,288, or than 8,192 where they begin differently in each matrix.
+// dx, one CTA a row; 8192 x 4096 bf16 took 177 us with this and the two below.
 __global__ void __launch_bounds__(kWideThreads) wide_dx_kernel(const NormGradArgs a) {
   __shared__ float part[2][kWideThreads / kWarp];
   pdl_wait();
@@ -129,7 +130,9 @@ constexpr int kMostPieces = 256;
 constexpr int kMostLanes = 512;  // threads a CTA
 constexpr int64_t kMostShared = 224 * 1024;  // a CTA's dynamic shared memory
 
-// Sizes whose sums one cluster takes and adds by itself, without a workspace.
+// Sizes whose sums one cluster takes and adds by itself, without a workspace: one launch
+// and one allocation less.  512 x 256 takes 16.6 us from Python and 22.5 with pieces; in a
+// captured graph, where launches cost little, 6.1 and 4.7.
 bool one_cluster(int64_t n_rows, int64_t dim) { return dim <= 1024 && n_rows * dim <= (1 << 17); }
 
 // Pieces that any of the kernels below may write.

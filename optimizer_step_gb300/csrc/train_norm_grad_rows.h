@@ -98,6 +98,14 @@ __device__ __forceinline__ void write_sums(const NormGradArgs& a, float* sums, i
 // sums down the columns, and again for x_grad.  At the end the CTA's groups are added
 // and written as one piece, and join_kernel adds the pieces; the CTAs of few rows are a
 // cluster that adds its sums by itself.
+//
+// WS: the weight lies in shared memory instead, which the widest rows need (24 elements a
+// thread: 8192 x 12288 bf16 takes 115 us so, 199 with spilled registers); with 16 elements
+// registers are quicker (45.4 and 47.7 us for 8192 x 4096).  Two rows at once pay for 8
+// elements a thread only (32768 x 512: 26 us and 27; with 16: 55 and 46 for 8192 x 4096).
+// What bounds it is the latency of a row's steps with 16 warps an SM, as many as the
+// registers allow, and instructions (24 an element, a third of them joins and addresses):
+// 8192 x 4096 bf16 takes 41 us and the join 4 more (4.4 TB/s), 32768 x 12288 391 (6.2).
 template <int XT, int YT, int M, int R, Span S, bool WS>
 __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ NormGradArgs a) {
   using TX = typename TypeOf<XT>::T;
@@ -329,7 +337,7 @@ __global__ void __launch_bounds__(512) grad_ring_kernel(const __grid_constant__ 
 
 // Element by element, M a thread and R rows at once, straight from memory: for rows of x,
 // grad_out and x_grad that do not begin equally far from a unit's boundary, and short odd
-// ones.
+// ones.  It waits for each row's loads: 50,021 x 1023 bf16 takes 132 us (2.3 TB/s).
 template <int XT, int YT, int M, int R, Span S>
 __global__ void __launch_bounds__(512) grad_scalar_kernel(const __grid_constant__ NormGradArgs a) {
   using TX = typename TypeOf<XT>::T;

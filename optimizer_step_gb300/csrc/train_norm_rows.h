@@ -110,6 +110,13 @@ __device__ __forceinline__ void stage_params(const NormArgs& a, int head, float*
 // each) goes to single threads of the first warp, one element each.  All rows of a
 // CTA begin equally far from a unit's boundary, so one layout of the parameters
 // holds for all.  CTAs stay and walk through the rows.
+//
+// The variance comes from the differences to the mean (two joins a row), in pairs of fp32
+// values.  Memory bounds it, with 15 instructions an element close behind: 8192 x 4096
+// bf16 takes 25.4 us (5.3 TB/s), 8192 x 12288 71 (5.7), 50,021 x 1023 from fp32 to bf16 56
+// (5.5); 3 us of each are the parameters' staging and the first rows.  Rows in registers,
+// a CTA each, without a ring, took 31 to 39 us for the first; parameters read again for
+// every row 57, since their loads waited for one another.
 template <int XT, int YT, int M, Span S>
 __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ NormArgs a) {
   using TX = typename TypeOf<XT>::T;
@@ -240,7 +247,8 @@ __global__ void __launch_bounds__(768) norm_ring_kernel(const __grid_constant__ 
 
 // ------------------------------------------------------------------- short rows
 // Less than a warp, or a warp, has R rows of one unit a thread each; a CTA has one
-// piece of work.
+// piece of work.  65,536 x 256 bf16 takes 18.5 us (3.6 TB/s), 131,072 x 64 9.8: the joins'
+// shuffles bound it.
 constexpr int kNormThreads = 256;
 
 template <int XT, int YT, int E, int R>
@@ -262,74 +270,94 @@ __global__ void __launch_bounds__(kNormThreads)
     x[r].clear();
     if (mine && r < rows) x[r].load_once(from + r * a.x_stride);
   }
-  float w[E], b[E];
+  F2 w[E / 2], b[E / 2];
 #pragma unroll
-  for (int i = 0; i < E; ++i) w[i] = 1.f, b[i] = 0.f;
+  for (int i = 0; i < E / 2; ++i) w[i] = pair(1.f), b[i] = pair(0.f);
   if (mine) {
     by_type(a.param_type, [&](auto P) {
       constexpr int PT = decltype(P)::value;
-      using TP = typename TypeOf<PT>::T;
+      const auto take = [&](const void* from, F2 (&to)[E / 2]) {
+        const auto* p = static_cast<const typename TypeOf<PT>::T*>(from) + g.lane * E;
+        Pack<PT, E> q;
+        if (reinterpret_cast<uintptr_t>(p) % (Pack<PT, E>::kBytes < 16 ? 8 : 16) == 0) {
+          q.load(p);
 #pragma unroll
-      for (int i = 0; i < E; ++i) {
-        if (a.weight) w[i] = to_float<PT>(static_cast<const TP*>(a.weight)[g.lane * E + i]);
-        if (a.bias) b[i] = to_float<PT>(static_cast<const TP*>(a.bias)[g.lane * E + i]);
-      }
+          for (int i = 0; i < E / 2; ++i) to[i] = get2(q, i);
+        } else {
+#pragma unroll
+          for (int i = 0; i < E / 2; ++i)
+            to[i] = pair(to_float<PT>(p[2 * i]), to_float<PT>(p[2 * i + 1]));
+        }
+      };
+      if (a.weight) take(a.weight, w);
+      if (a.bias) take(a.bias, b);
     });
   }
   const float inv = 1.f / float(dim);
+  F2 v[R][E / 2];
   float mean[R], rstd[R];
-  bool odd = false;
+  bool odd = false, fine[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    float s = 0.f;
+    F2 s = pair(0.f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) s += x[r].get(i);
-    mean[r] = s;
+    for (int i = 0; i < E / 2; ++i) v[r][i] = get2(x[r], i), s = add2(s, v[r][i]);
+    mean[r] = sum2(s);
   }
+  for (int d = 1; d < lanes; d *= 2)
 #pragma unroll
-  for (int r = 0; r < R; ++r) mean[r] = g.sum<Span::kPart>(mean[r], 0) * inv;
+    for (int r = 0; r < R; ++r) mean[r] += __shfl_xor_sync(kAll, mean[r], d);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    float s = 0.f;
+    mean[r] *= inv;
+    F2 s = pair(0.f);
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const float d = x[r].get(i) - mean[r];
-      s += d * d;
+    for (int i = 0; i < E / 2; ++i) {
+      v[r][i] = add2(v[r][i], pair(-mean[r]));
+      s = fma2(v[r][i], v[r][i], s);
     }
-    rstd[r] = mine ? s : 0.f;
+    rstd[r] = mine ? sum2(s) : 0.f;
   }
-  bool fine[R];
+  for (int d = 1; d < lanes; d *= 2)
+#pragma unroll
+    for (int r = 0; r < R; ++r) rstd[r] += __shfl_xor_sync(kAll, rstd[r], d);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const float var = g.sum<Span::kPart>(rstd[r], 1) * inv;
+    const float var = rstd[r] * inv;
     rstd[r] = rstd_of(var, a.eps);
     fine[r] = in_range(var, a.eps);
     odd = odd || (!fine[r] && r < rows);
   }
   if (__any_sync(kAll, odd)) {
+#pragma unroll 1
+    for (int r = 0; r < R; ++r) {
+      bool wanted = false;
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-      scaled_row<XT, YT, Span::kPart>(a, row0 + r, !fine[r] && r < rows, g);
+      for (int k = 0; k < R; ++k)
+        if (k == r) wanted = !fine[k] && k < rows;
+      scaled_row<XT, YT, Span::kPart>(a, row0 + r, wanted, g);
+    }
   }
   TY* to = static_cast<TY*>(a.y) + row0 * a.y_stride + g.lane * E;
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
+  for (int r = 0; r < R; ++r, to += a.y_stride) {
     if (!fine[r] || r >= rows) continue;
     if (a.stats && g.lane == 0)
       a.stats[row0 + r] = mean[r], a.stats[a.n_rows + row0 + r] = rstd[r];
     if (!mine) continue;
-    float v[E];
-#pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = (x[r].get(i) - mean[r]) * rstd[r] * w[i] + b[i];
     Pack<YT, E> o;
-    o.set(v);
-    o.store(to + r * a.y_stride);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+      set2(o, i, fma2(mul2(v[r][i], pair(rstd[r])), w[i], b[i]));
+    o.store(to);
   }
 }
 
 // ------------------------------------------------------- rows element by element
 // For rows of x and y that do not begin equally far from a unit's boundary, and short
-// ones of odd widths: M elements a thread and R rows at once, in registers.
+// ones of odd widths: M elements a thread and R rows at once, in registers.  The loads'
+// latency bounds it: 50,021 x 1023 bf16 takes 71 us (2.9 TB/s) where the ring takes 41,
+// 300,000 x 33 37 us with two rows at once and 50 with one.
 template <int XT, int YT, int M, int R, Span S>
 __global__ void __launch_bounds__(512, M > 8 ? 0 : 2) norm_scalar_kernel(const __grid_constant__ NormArgs a) {
   using TX = typename TypeOf<XT>::T;
