@@ -147,7 +147,8 @@ constexpr int64_t kSliceBytes = 104 * 1024;
 
 // Clusters of a kernel that the device holds at once.  They lie within the device's
 // groups of SMs, so there may be fewer than its SMs have room for, and one more would
-// wait for the others' last row.  The driver's answers are kept: it takes 10 us for one.
+// wait for the others' last row: 1021 x 131,071 fp16 took 167 us with 114 clusters and 128
+// with the 110 that fit.  CUDA is asked once for each shape of a launch.
 int64_t clusters_at_once(const void* kernel, int threads, int64_t smem, int ctas) {
   struct Known {
     const void* kernel;

@@ -113,23 +113,6 @@ struct Pack {
       w[0] = __ldcs(reinterpret_cast<const uint16_t*>(p));
     }
   }
-  // By a plain load that keeps its place among the stores around it.
-  __device__ __forceinline__ void load_kept(const T* p) {
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i) {
-        const uint4 q = reinterpret_cast<const uint4*>(p)[i];
-        w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-      }
-    } else if constexpr (kBytes == 8) {
-      const uint2 q = *reinterpret_cast<const uint2*>(p);
-      w[0] = q.x, w[1] = q.y;
-    } else if constexpr (kBytes == 4) {
-      w[0] = *reinterpret_cast<const uint32_t*>(p);
-    } else {
-      w[0] = *reinterpret_cast<const uint16_t*>(p);
-    }
-  }
   __device__ __forceinline__ void store(T* p) const {
     if constexpr (kBytes >= 16) {
 #pragma unroll

@@ -1,5 +1,5 @@
-// Helpers of layer norm's kernels (train_ops.h).  Not part of the public
-// interface.
+// Helpers of layer norm's and the distillation loss's kernels (train_ops.h).  Not part
+// of the public interface.
 #pragma once
 
 #include <cfloat>
