@@ -10,9 +10,9 @@ namespace {
 
 constexpr int kThreads = 512;
 
-// Rows that no cluster holds (above 1.6 MB), and vocabularies of less than a unit.  One CTA
-// a row, which it reads three times (from L1 or L2 after the first): 8192 x 32000 bf16 took
-// 572 us this way.
+// The gradient of rows that no cluster holds (above 1.6 MB), and vocabularies of less than
+// a unit.  One CTA a row, which it reads three times (from L1 or L2 after the first): 8192
+// x 32000 bf16 took 572 us this way.
 __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
   // The row's entries: the teacher's tokens and behind them the label.
   __shared__ int32_t id[kMaxTop + 1];
@@ -80,16 +80,14 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
     hard_sum = cta_sum<kThreads>(hard_sum, part[3]);
     // The loss, and what each entry takes off the gradient.
     float terms = 0.f;
-    const float log_size = logf(size), log_soft = logf(soft_sum);
+    const float logs = logf(soft_sum) - logf(size);
     for (int k = tid; k < top_k; k += kThreads) {
       if (id[k] < 0) {
         coef[k] = 0.f;
         continue;
       }
-      const float t = (coef[k] - best) * a.inv_temperature;
-      const float p = exp2f((coef[k] - best) * c) / size;
-      const float q = (zed[k] - top) * a.inv_temperature - log_soft;
-      terms += zed[k] == -INFINITY ? INFINITY : p * (t - log_size - q);
+      const float d = coef[k] - best, p = exp2f(d * c) / size;
+      terms += soft_term(a, p, d, zed[k] - top, logs);
       coef[k] = a.soft_weight * a.temperature * p;
     }
     const bool hits = work && hard;
@@ -103,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
       float loss = 0.f;
       // Without a distribution (soft_sum is NaN) a masked token's term means nothing.
       if (soft_sum != soft_sum) terms = soft_sum;
-      if (work && any) loss = a.soft_weight * a.temperature * a.temperature * terms;
+      if (work && any) loss = terms;
       if (hits) loss += a.hard_weight * (logf(hard_sum) - (zed[top_k] - top));
       a.loss[row] = loss;
     }
@@ -182,7 +180,13 @@ int64_t clusters_at_once(const void* kernel, int threads, int64_t smem, int ctas
   return k.clusters;
 }
 
-// Launches the kernel for rows that stay in shared memory, if one holds them; sets `done`.
+// Whether rows of so many units last for the stages that are on their way.
+bool ring_takes(int64_t units, int threads) {
+  return units >= int64_t(kRingStages - 1) * kAtOnce * threads;
+}
+
+// Launches the kernel for rows that stay in shared memory or pass through it, if there is
+// one; sets `done`.
 cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   *done = false;
   const int e = 16 / size_of(a.type);
@@ -192,15 +196,6 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   };
   a.phase = phase(a.logits, a.type), a.row_phase = int32_t(a.stride % e);
   a.whole = !a.grad || (phase(a.grad, a.grad_type) == a.phase && a.grad_stride % e == a.row_phase);
-  a.ctas = 1;
-  while (units * 16 > a.ctas * kSliceBytes) a.ctas *= 2;
-  if (a.ctas > kMostCtas || units == 0) return cudaSuccess;
-  a.slice = int32_t((units + a.ctas - 1) / a.ctas);
-  // At least 8 units a thread: 16384 x 4096 bf16 takes 72 us so, 103 with 4 and 80 with 16.
-  int threads = kDistillThreads;
-  while (threads > kWarp && a.slice < threads * 8) threads /= 2;
-  const int64_t smem = int64_t(a.slice) * 16 + 2 * 3 * 4 * int64_t((a.top_k + 4) / 4 * 4);
-  if (smem > kMostShared) return cudaSuccess;
   // Two softmaxes only where the terms are at two temperatures.
   const bool soft = a.top_k > 0 && a.soft_weight != 0.f, hard = a.labels && a.hard_weight != 0.f;
   const int terms = !soft || !hard || a.temperature == 1.f ? kOne
@@ -209,24 +204,62 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   const DistillKernels& k = a.type == TRAIN_BF16   ? distill_kernels_bf16()
                             : a.type == TRAIN_FP16 ? distill_kernels_fp16()
                                                    : distill_kernels_fp32();
-  const DistillKernel kernel = a.grad ? k.grad[a.grad_type][terms] : k.loss[terms];
-  const void* f = reinterpret_cast<const void*>(kernel);
-  cudaError_t ce = cudaSuccess;
-  if (smem > 32 * 1024)
-    ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
-  if (ce == cudaSuccess && a.ctas > 8)
-    ce = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (ce != cudaSuccess) return ce;
+  const int64_t lists = 2 * 3 * 4 * int64_t((a.top_k + 4) / 4 * 4);
+  a.ctas = 1;
+  while (units * 16 > a.ctas * kSliceBytes) a.ctas *= 2;
+  int64_t clusters = 0;  // none holds a row
+  if (a.ctas <= kMostCtas && units > 0) {
+    a.slice = int32_t((units + a.ctas - 1) / a.ctas);
+    // At least 8 units a thread: 16384 x 4096 bf16 takes 72 us so, 103 with 4 and 80 with 16.
+    int threads = kDistillThreads;
+    while (threads > kWarp && a.slice < threads * 8) threads /= 2;
+    const int64_t smem = int64_t(a.slice) * 16 + lists;
+    const DistillKernel kernel = a.grad ? k.grad[a.grad_type][terms] : k.loss[terms];
+    const void* f = reinterpret_cast<const void*>(kernel);
+    cudaError_t ce = cudaSuccess;
+    if (smem > 32 * 1024)
+      ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+    if (ce == cudaSuccess && a.ctas > 8)
+      ce = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (ce != cudaSuccess) return ce;
+    const int64_t resident = std::max<int64_t>(
+        1, std::min<int64_t>(std::min(24, 3 * kDistillThreads / threads),
+                             (227 * 1024) / (smem + 8 * 1024)));
+    clusters = resident * kSms;
+    if (a.ctas > 1)
+      clusters = std::min(clusters / a.ctas, clusters_at_once(f, threads, smem, a.ctas));
+    clusters = std::max<int64_t>(1, clusters);
+    if (a.grad || a.n_rows <= clusters || !ring_takes(units, kWarp)) {
+      *done = true;
+      return launch(kernel, dim3(unsigned(std::min(a.n_rows, clusters) * a.ctas)), threads,
+                    size_t(smem), stream, true, a.ctas, a);
+    }
+  }
+  if (a.grad || !ring_takes(units, kWarp)) return cudaSuccess;
+  // More rows than are held at once pass through the ring, as do the longest: 608 x 32000
+  // bf16 takes 11.0 us so and 14.5 held, 304 rows 8.2 and 8.1, 152 rows 7.2 and 6.3; 152 x
+  // 131,072 13.5 and 16.1, 64 rows 12.6 and 8.6.
+  // Up to 64 units a thread (8192 x 12800 bf16 takes 47 us with 32 threads and 52 with 64, 4096
+  // x 50,000 69 with 128 and 76 with 64), or more threads while all rows are there at once.
+  const int64_t room = int64_t(kSms) * kRingCtas * kRingThreads;
+  int threads = kWarp;
+  while (threads < kRingThreads && ring_takes(units, 2 * threads) &&
+         (units > 64 * threads || a.n_rows * 2 * threads <= room))
+    threads *= 2;
+  const int64_t smem = threads / kWarp * kRingBytes + lists;
   const int64_t resident = std::max<int64_t>(
-      1, std::min<int64_t>(std::min(24, 3 * kDistillThreads / threads),
-                           (227 * 1024) / (smem + 8 * 1024)));
-  int64_t clusters = resident * kSms;
-  if (a.ctas > 1)
-    clusters = std::min(clusters / a.ctas, clusters_at_once(f, threads, smem, a.ctas));
-  clusters = std::min<int64_t>(a.n_rows, std::max<int64_t>(1, clusters));
+      1, std::min<int64_t>(kRingCtas * kRingThreads / threads, (227 * 1024) / (smem + 2 * 1024)));
+  const DistillKernel kernel = k.ring[terms];
+  if (smem > 32 * 1024) {
+    const cudaError_t ce =
+        cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+    if (ce != cudaSuccess) return ce;
+  }
+  a.ctas = 1, a.slice = int32_t(units);
   *done = true;
-  return launch(kernel, dim3(unsigned(clusters * a.ctas)), threads, size_t(smem), stream, true,
-                a.ctas, a);
+  return launch(kernel, dim3(unsigned(std::min(a.n_rows, resident * kSms))), threads,
+                size_t(smem), stream, true, 1, a);
 }
 
 int check_ids(const char* name, const void* p, int32_t dtype, int64_t n) {

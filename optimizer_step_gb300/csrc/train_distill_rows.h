@@ -49,6 +49,16 @@ __device__ __forceinline__ F2 exp2_of(F2 x) {
   return pair(exp2_of(lo), exp2_of(hi));
 }
 
+// An entry's term of the loss, soft_weight T^2 p (log p - log q), from the teacher's and
+// the student's logit less the largest, and log of the student's sum less log of the
+// teacher's.  The weight goes to p and T into the difference, so that a named token of the
+// type's lowest value gives an infinite loss only where the loss is past fp32's range.
+__device__ __forceinline__ float soft_term(const DistillArgs& a, float p, float teacher,
+                                           float student, float logs) {
+  if (student == -INFINITY) return copysignf(INFINITY, a.soft_weight);
+  return a.soft_weight * a.temperature * p * (teacher - student + a.temperature * logs);
+}
+
 // A unit of logits: 16 bytes.
 template <int ZT>
 struct Unit {
@@ -127,6 +137,12 @@ constexpr int kDistillThreads = 256;
 constexpr int kDistillWarps = kDistillThreads / kWarp;
 constexpr int kMostCtas = 16;
 constexpr int kAtOnce = 4;  // units a thread reads together
+// Rows through a ring.
+constexpr int kRingThreads = 128;  // a row, at most
+constexpr int kRingCtas = 6;       // of as many, an SM
+constexpr int kRingStages = 3;
+constexpr int kChunk = kAtOnce * kWarp;  // units of a stage, a warp
+constexpr int kRingBytes = kRingStages * kChunk * 16;  // a warp
 
 // A row's slice is copied into shared memory asynchronously, in units of 16 bytes, and
 // read there twice: once for the running largest value and sums of exponentials, once
@@ -141,11 +157,18 @@ constexpr int kAtOnce = 4;  // units a thread reads together
 // sums or products of pairs each take 12 an element, some 700 a row and warp come on top,
 // and the warps that have entries keep the others waiting.  8192 x 32000 bf16 with 64
 // entries takes 192 us at one temperature and 200 at two (5.5 and 5.2 TB/s), without
-// entries 172 (6.1 TB/s); the loss alone 115 (4.6 TB/s).  Without the prefetch into L2 it
-// was 218.  128 threads a CTA took 197, more parts of a row waited for one by one 205.
+// entries 172 (6.1 TB/s).  Without the prefetch into L2 it was 218.  128 threads a CTA took
+// 197, more parts of a row waited for one by one 205.
+//
+// RING: the loss of more rows than there is room for.  It needs a row once, so units come
+// through a ring for each warp, those of the next row behind this one's without a pause; a
+// row has one to four warps, which makes what a row costs besides its elements small, and
+// may be of any length.  8192 x 32000 bf16 with 64 entries takes 86 us (6.1 TB/s; held whole
+// 115), 16384 x 8192 50 (87), 4096 x 50,000 70 (93), 1021 x 131,071 fp16 56 (74); with
+// four stages 90, 54, 71 and 54.
 //   ZT, GT  types of logits and grad        TERMS  the softmaxes (kOne and so on)
-template <int ZT, int GT, int TERMS, bool GRAD>
-__global__ void __launch_bounds__(kDistillThreads, 3)
+template <int ZT, int GT, int TERMS, bool GRAD, bool RING>
+__global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? kRingCtas : 3)
     distill_kernel(const __grid_constant__ DistillArgs a) {
   namespace cg = cooperative_groups;
   using TZ = typename TypeOf<ZT>::T;
@@ -155,7 +178,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   struct Part {
     float top, s[2], spare;
   };
-  __shared__ Part parts[2][kMostCtas * kDistillWarps];  // by the row's parity
+  __shared__ Part parts[2][RING ? kRingThreads / kWarp : kMostCtas * kDistillWarps];  // by the row's parity
   __shared__ float2 teacher[2][kDistillWarps];          // largest, sum
   __shared__ float terms[2][kDistillWarps];
   const int tid = threadIdx.x, threads = blockDim.x, warps = threads / kWarp;
@@ -164,7 +187,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
   const int rank = a.ctas == 1 ? 0 : int(blockIdx.x) % a.ctas;
   uint4* slot = reinterpret_cast<uint4*>(smem);
   const uint32_t slot_address = shared_address(smem);
-  unsigned char* lists = smem + size_t(a.slice) * 16;
+  unsigned char* lists = smem + (RING ? size_t(warps * kRingBytes) : size_t(a.slice) * 16);
 
   const bool soft = a.top_k > 0 && a.soft_weight != 0.f;
   const bool hard = a.labels && a.hard_weight != 0.f;
@@ -215,6 +238,26 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     }
     copy_commit();
   };
+  // The ring: a warp's stages are side by side, and each thread reads back its own units.
+  const uint4* stages = slot + warp * (kRingStages * kChunk) + lane;
+  const int chunks = (run + kChunk - 1) / kChunk;  // a row
+  const TZ* coming = nullptr;
+  int coming_at = 0, coming_end = 0;  // units
+  uint32_t in = 0, out = 0;           // stages
+  const auto begin = [&](const TZ* from, int mine) {
+    coming = from + int64_t(first + lane) * E;
+    coming_at = first + lane, coming_end = min(mine, first + run);
+  };
+  const auto request = [&] {
+    const uint32_t to = shared_address(stages + in * kChunk);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k)
+      if (coming_at + k * kWarp < coming_end)
+        copy_async<16>(to + k * (kWarp * 16), coming + k * (kWarp * E));
+    copy_commit();
+    coming += kChunk * E, coming_at += kChunk;
+    in = (in + 1) % kRingStages;
+  };
   // The teacher's entry that this thread has of the first `threads` of a row.
   const auto entry_of = [&](int64_t row, int k, int64_t& i, float& t) {
     i = read_id(a.top_ids, row * a.ids_stride + k, a.ids64);
@@ -236,8 +279,11 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     if (has_entry) entry_of(row, tid, entry, entry_t);
     const int head = head_of(row);
     const int mine = live ? mine_of((vocab - head) / E) : 0;
-    copy(row_of(row) + head + int64_t(at0) * E, mine);
+    if constexpr (RING) begin(row_of(row) + head, mine);
+    else copy(row_of(row) + head + int64_t(at0) * E, mine);
   }
+  if constexpr (RING)
+    for (int k = 1; k < kRingStages; ++k) request();
   int parity = 0;
   const TZ* z = row_of(row);
   TG* grad = GRAD ? static_cast<TG*>(a.grad) + row * a.grad_stride : nullptr;
@@ -303,40 +349,56 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     }
     // The largest value and the sums.
     Sums<TERMS> sums;
-    if (live) {
-      copy_wait<0>();
-      const int end = min(mine, first + run);
-      for (int i = first + lane; i < end; i += kAtOnce * kWarp) {
-        Unit<ZT> x[kAtOnce];
-        if (i + (kAtOnce - 1) * kWarp < end) {
+    // Adds kAtOnce units, 32 apart; `i` is the first's place among the `end` of this warp.
+    const auto add = [&](const uint4* from, int i, int end) {
+      Unit<ZT> x[kAtOnce];
+      if (i + (kAtOnce - 1) * kWarp < end) {
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) x[k].q = slot[i + k * kWarp];
-        } else {
+        for (int k = 0; k < kAtOnce; ++k) x[k].q = from[k * kWarp];
+      } else {
 #pragma unroll
-          for (int k = 0; k < kAtOnce; ++k) {
-            x[k].none();
-            if (i + k * kWarp < end) x[k].q = slot[i + k * kWarp];
-          }
+        for (int k = 0; k < kAtOnce; ++k) {
+          x[k].none();
+          if (i + k * kWarp < end) x[k].q = from[k * kWarp];
         }
-        sums.raise(fmaxf(sums.top, largest(x)), c);
-        const F2 down = pair(-sums.top);
-        F2 t[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) t[n] = pair(sums.s[n], 0.f);
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-#pragma unroll
-          for (int h = 0; h < E / 2; ++h) {
-            const F2 d = add2(x[k].get(h), down);
-            const F2 e = exp2_of(mul2(d, pair(c[0])));
-            t[0] = add2(t[0], e);
-            if constexpr (TERMS == kTwo) t[1] = add2(t[1], exp2_of(mul2(d, pair(c[1]))));
-            if constexpr (TERMS == kSquares) t[1] = fma2(e, e, t[1]);
-          }
-#pragma unroll
-        for (int n = 0; n < N; ++n) sums.s[n] = sum2(t[n]);
       }
-      if constexpr (!GRAD) copy(next_from, next_mine);
+      sums.raise(fmaxf(sums.top, largest(x)), c);
+      const F2 down = pair(-sums.top);
+      F2 t[N];  // of these alone, for short chains of additions
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+#pragma unroll
+        for (int h = 0; h < E / 2; ++h) {
+          const F2 d = add2(x[k].get(h), down);
+          const F2 e = exp2_of(mul2(d, pair(c[0])));
+          const bool begun = k + h > 0;
+          t[0] = begun ? add2(t[0], e) : e;
+          if constexpr (TERMS == kTwo) {
+            const F2 e1 = exp2_of(mul2(d, pair(c[1])));
+            t[1] = begun ? add2(t[1], e1) : e1;
+          }
+          if constexpr (TERMS == kSquares) t[1] = begun ? fma2(e, e, t[1]) : mul2(e, e);
+        }
+#pragma unroll
+      for (int n = 0; n < N; ++n) sums.s[n] += sum2(t[n]);
+    };
+    if constexpr (RING) {
+      const int end = min(mine, first + run);
+      for (int k = 0, i = first + lane; k < chunks; ++k, i += kChunk) {
+        if (k + kRingStages - 1 == chunks) begin(next_from, next_mine);
+        request();
+        copy_wait<kRingStages - 1>();
+        if (live && i < end) add(stages + out * kChunk, i, end);
+        out = (out + 1) % kRingStages;
+      }
+    }
+    if (live) {
+      if constexpr (!RING) {
+        copy_wait<0>();
+        const int end = min(mine, first + run);
+        for (int i = first + lane; i < end; i += kChunk) add(slot + i, i, end);
+        if constexpr (!GRAD) copy(next_from, next_mine);
+      }
       if (single >= 0) {
         sums.raise(fmaxf(sums.top, edge), c);
         float f[N];
@@ -344,7 +406,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
 #pragma unroll
         for (int n = 0; n < N; ++n) sums.s[n] += f[n];
       }
-    } else if (!GRAD) {
+    } else if (!GRAD && !RING) {
       copy(next_from, next_mine);
     }
     // Over the warps of the row's CTAs; the teacher's, which each CTA has, over its own.
@@ -370,7 +432,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     if (a.ctas > 1) cluster.sync();
     else __syncthreads();
     // The next row is on its way to L2 from here on, and to shared memory as room is made there.
-    if (tid == 0 && next_mine > 0)
+    if (!RING && tid == 0 && next_mine > 0)
       asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(next_from),
                    "r"(next_mine * 16)
                    : "memory");
@@ -406,7 +468,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
     // The terms of the loss, and what each entry takes off the gradient.
     if (warp < entry_warps && work && any) {
       float sum = 0.f;
-      const float log_size = logf(size), log_soft = logf(soft_sum), inv = 1.f / size;
+      const float logs = logf(soft_sum) - logf(size), inv = 1.f / size;
       const float weight = a.soft_weight * a.temperature * up;
       for (int k = tid; k < a.top_k; k += threads) {
         if (id[k] < 0) {
@@ -415,8 +477,7 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
         }
         const float d = coef[k] - best;
         const float p = exp2_of(d * ct) * inv;
-        const float q = (zed[k] - top) * a.inv_temperature - log_soft;
-        sum += zed[k] == -INFINITY ? INFINITY : p * (d * a.inv_temperature - log_size - q);
+        sum += soft_term(a, p, d, zed[k] - top, logs);
         coef[k] = weight * p;
       }
       sum = warp_sum(sum);
@@ -508,7 +569,6 @@ __global__ void __launch_bounds__(kDistillThreads, 3)
         for (int k = 0; k < entry_warps; ++k) loss += terms[parity][k];
         // Without a distribution a masked token's term means nothing.
         if (soft_sum != soft_sum) loss = soft_sum;
-        loss *= a.soft_weight * a.temperature * a.temperature;
       }
       if (work && hard) loss += a.hard_weight * (logf(hard_sum) - (zed[a.top_k] - top));
       a.loss[row] = loss;
@@ -524,17 +584,21 @@ using DistillKernel = void (*)(DistillArgs);
 struct DistillKernels {
   DistillKernel grad[3][3];
   DistillKernel loss[3];
+  DistillKernel ring[3];  // the loss of many rows
 };
 template <int ZT>
 constexpr DistillKernels distill_kernels() {
-  return {{{distill_kernel<ZT, TRAIN_BF16, kOne, true>, distill_kernel<ZT, TRAIN_BF16, kTwo, true>,
-            distill_kernel<ZT, TRAIN_BF16, kSquares, true>},
-           {distill_kernel<ZT, TRAIN_FP16, kOne, true>, distill_kernel<ZT, TRAIN_FP16, kTwo, true>,
-            distill_kernel<ZT, TRAIN_FP16, kSquares, true>},
-           {distill_kernel<ZT, TRAIN_FP32, kOne, true>, distill_kernel<ZT, TRAIN_FP32, kTwo, true>,
-            distill_kernel<ZT, TRAIN_FP32, kSquares, true>}},
-          {distill_kernel<ZT, TRAIN_FP32, kOne, false>, distill_kernel<ZT, TRAIN_FP32, kTwo, false>,
-           distill_kernel<ZT, TRAIN_FP32, kSquares, false>}};
+  return {{{distill_kernel<ZT, TRAIN_BF16, kOne, true, false>, distill_kernel<ZT, TRAIN_BF16, kTwo, true, false>,
+            distill_kernel<ZT, TRAIN_BF16, kSquares, true, false>},
+           {distill_kernel<ZT, TRAIN_FP16, kOne, true, false>, distill_kernel<ZT, TRAIN_FP16, kTwo, true, false>,
+            distill_kernel<ZT, TRAIN_FP16, kSquares, true, false>},
+           {distill_kernel<ZT, TRAIN_FP32, kOne, true, false>, distill_kernel<ZT, TRAIN_FP32, kTwo, true, false>,
+            distill_kernel<ZT, TRAIN_FP32, kSquares, true, false>}},
+          {distill_kernel<ZT, TRAIN_FP32, kOne, false, false>, distill_kernel<ZT, TRAIN_FP32, kTwo, false, false>,
+           distill_kernel<ZT, TRAIN_FP32, kSquares, false, false>},
+          {distill_kernel<ZT, TRAIN_FP32, kOne, false, true>,
+           distill_kernel<ZT, TRAIN_FP32, kTwo, false, true>,
+           distill_kernel<ZT, TRAIN_FP32, kSquares, false, true>}};
 }
 
 // Each defined in a translation unit of its own.

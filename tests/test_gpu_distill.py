@@ -580,3 +580,118 @@ def test_calls_on_several_streams_at_once():
         want = reference(data, 1.0, 1.0, 0.0)
         near(loss, *want[:2], "loss")
         near(grad, *want[2:], "grad")
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("n,vocab", [(20, 5), (20, 4096), (2500, 4096), (2, 1_300_000)])
+@pytest.mark.parametrize("temperature", [0.5, 1.0, 2.0])
+def test_a_loss_near_the_largest_number_is_finite(dtype, n, vocab, temperature):
+    """All of the teacher's weight on tokens of the type's lowest value."""
+    data = Data(n, vocab, 4, dtype)
+    data.ids[:] = torch.arange(4, device="cuda")
+    data.logits[:, :4] = torch.finfo(dtype).min
+    # soft T^2 sum of p 3.4e38 / T: 0.4 or 0.8 of the largest number.
+    loss, tol, _, _ = reference(data, temperature, 0.4, 0.0)
+    for got in (og.distill_loss(*data.args(), temperature=temperature, soft_weight=0.4),
+                og.distill_loss_grad(*data.args(), temperature=temperature, soft_weight=0.4)[0]):
+        near(got, loss, tol, "loss")
+
+
+# ------------------------------------------- the loss alone, of more rows than are held
+def check_loss(data, temperature=1.0, soft=1.0, hard=0.0, ignore=-100):
+    loss, tol, _, _ = reference(data, temperature, soft, hard, ignore)
+    got = og.distill_loss(*data.args(), temperature=temperature, soft_weight=soft,
+                          hard_weight=hard, ignore_id=ignore)
+    # A token of the type's lowest value that is named: soft T^2 times 3.4e38 / T, say, is
+    # past fp32's largest number at T = 2, and rounds to infinity.
+    past = (loss + 1.01 * tol > torch.finfo(FP32).max) & (got == math.inf)
+    near(got, torch.where(past, math.inf, loss), tol, "loss")
+    return got
+
+
+@pytest.mark.parametrize("n,vocab", [(3700, 2047), (3700, 2048), (2400, 4096), (2500, 5001),
+                                     (1300, 12007), (1000, 16384), (700, 32000), (1100, 32001),
+                                     (500, 50001), (200, 131071), (160, 262144)])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
+def test_the_loss_of_many_rows(n, vocab, dtype):
+    data = Data(n, vocab, 11, dtype)
+    data.labels[::9] = -100
+    data.labels[3::11] = vocab
+    data.ids[5::7, 4:] = -1
+    data.ids[6::8] = vocab
+    data.logits[1::13, 7:vocab // 2] = -math.inf
+    data.logits[2::13, vocab // 2:vocab - 9] = torch.finfo(dtype).min
+    data.ids[1::13] = torch.arange(11, device="cuda") % 7
+    data.labels[1::13] = 6
+    for temperature, soft, hard in ((1.0, 0.7, 0.3), (2.0, 0.7, 0.3), (3.0, 0.7, 0.3),
+                                    (2.0, 1.0, 0.0), (2.0, 0.0, 1.0)):
+        check_loss(data, temperature, soft, hard)
+
+
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_the_loss_of_the_longest_rows(n, dtype):
+    check_loss(Data(n, 3_000_001, 20, dtype), 2.0, 0.5, 0.5)
+
+
+@pytest.mark.parametrize("top", [0, 31, 33, 127, 257, 1024])
+def test_the_loss_of_many_rows_with_many_entries(top):
+    check_loss(Data(2500, 4096, top), 2.0, 0.5, 0.5)
+    check_loss(Data(700, 32000, top), 1.0, 0.5, 0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("vocab,stride,shift", [(4096, 4096, 1), (4096, 4104, 0), (4096, 4099, 3),
+                                                (4099, 4101, 1), (4099, 4099, 2)])
+def test_the_loss_of_many_rows_anywhere(dtype, vocab, stride, shift):
+    n = 2500
+    data = Data(n, vocab, 9, dtype)
+    held = torch.full((shift + n * stride,), math.nan, dtype=dtype, device="cuda")
+    rows = held[shift:].view(n, stride)[:, :vocab]
+    rows.copy_(data.logits)
+    data.logits = rows
+    check_loss(data, 2.0, 0.5, 0.5)
+
+
+@pytest.mark.parametrize("n,vocab", [(2500, 4096), (2000, 9001), (1000, 32000)])
+@pytest.mark.parametrize("bad", [math.inf, math.nan, -math.inf])
+def test_broken_rows_among_many_stay_alone(n, vocab, bad):
+    data = Data(n, vocab, 6)
+    how = dict(temperature=2.0, soft_weight=0.5, hard_weight=0.5)
+    whole = og.distill_loss(*data.args(), **how)
+    broken = torch.zeros(n, dtype=torch.bool, device="cuda")
+    broken[7::97] = True
+    if bad == -math.inf:
+        data.logits[broken] = bad
+    else:
+        data.logits[broken, vocab // 3] = bad
+    loss = og.distill_loss(*data.args(), **how)
+    assert bool(loss[broken].isnan().all())
+    assert torch.equal(loss[~broken], whole[~broken])
+
+
+@pytest.mark.parametrize("n,vocab", [(2500, 4096), (1000, 32000), (200, 131071)])
+def test_the_loss_of_many_rows_on_streams_and_in_graphs(n, vocab):
+    how = dict(temperature=2.0, soft_weight=0.5, hard_weight=0.5)
+    sets = [Data(n, vocab, 9, seed=k) for k in range(2)]
+    want = [og.distill_loss(*d.args(), **how) for d in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        got = []
+        for d, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                got.append(og.distill_loss(*d.args(), **how))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        caught = og.distill_loss(*sets[0].args(), **how)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(caught, want[0])
+    for to, other in zip(sets[0].args(), sets[1].args()):
+        to.copy_(other)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(caught, want[1])
