@@ -210,9 +210,10 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   int64_t clusters = 0;  // none holds a row
   if (a.ctas <= kMostCtas && units > 0) {
     a.slice = int32_t((units + a.ctas - 1) / a.ctas);
-    // At least 8 units a thread: 16384 x 4096 bf16 takes 72 us so, 103 with 4 and 80 with 16.
+    // At least 8 units a thread (16384 x 4096 bf16 takes 72 us so, 103 with 4 and 80 with 16)
+    // but at most 4 entries (6263 x 2688 fp16 with 179: 58 us so, 77 with 6 and 76 with 2).
     int threads = kDistillThreads;
-    while (threads > kWarp && a.slice < threads * 8) threads /= 2;
+    while (threads > kWarp && a.slice < threads * 8 && a.top_k <= threads * 2) threads /= 2;
     const int64_t smem = int64_t(a.slice) * 16 + lists;
     const DistillKernel kernel = a.grad ? k.grad[a.grad_type][terms] : k.loss[terms];
     const void* f = reinterpret_cast<const void*>(kernel);

@@ -1,4 +1,4 @@
-// The distillation loss of fp16 logits in rows that stay in shared memory.
+// The distillation loss of fp16 logits in rows that stay in shared memory or pass through it.
 #include "train_distill_rows.h"
 
 namespace traingb {

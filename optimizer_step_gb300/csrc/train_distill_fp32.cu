@@ -1,4 +1,4 @@
-// The distillation loss of fp32 logits in rows that stay in shared memory.
+// The distillation loss of fp32 logits in rows that stay in shared memory or pass through it.
 #include "train_distill_rows.h"
 
 namespace traingb {

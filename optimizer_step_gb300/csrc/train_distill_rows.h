@@ -1,4 +1,4 @@
-// The distillation loss of rows that stay in shared memory (train_ops.h): the
+// The distillation loss of rows in shared memory (train_ops.h): the
 // kernels, compiled once for each type of the logits.  Not part of the public
 // interface.
 #pragma once
