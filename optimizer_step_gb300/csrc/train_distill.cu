@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
 }
 
 constexpr int kSms = 152;
-constexpr int64_t kMostShared = 136 * 1024;  // a CTA's dynamic shared memory
+constexpr int64_t kMostShared = 168 * 1024;  // a CTA's dynamic shared memory
 // What a CTA holds of a row: up to 70 KB or so there are three of them an SM, up to this
 // two.  Longer rows go to clusters of CTAs: 4096 x 46000 bf16 takes 146 us with one CTA a
 // row and 167 with two, 4096 x 36000 129 and 148.
@@ -204,14 +204,20 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
   const DistillKernels& k = a.type == TRAIN_BF16   ? distill_kernels_bf16()
                             : a.type == TRAIN_FP16 ? distill_kernels_fp16()
                                                    : distill_kernels_fp32();
-  const int64_t lists = 2 * 3 * 4 * int64_t((a.top_k + 4) / 4 * 4);
+  // Four to eight buckets an entry, of two kinds: one entry in a hundred finds both taken.
+  int64_t lists = 2 * 3 * 4 * int64_t((a.top_k + 4) / 4 * 4);
+  if (a.grad) {
+    a.bucket_bits = 2;
+    while ((1 << a.bucket_bits) < 4 * (a.top_k + 1)) ++a.bucket_bits;
+    lists += 2 * int64_t((a.top_k + 4) / 4 * 4) + 2 * 2 * (int64_t(1) << a.bucket_bits);
+  }
   a.ctas = 1;
   while (units * 16 > a.ctas * kSliceBytes) a.ctas *= 2;
   int64_t clusters = 0;  // none holds a row
   if (a.ctas <= kMostCtas && units > 0) {
     a.slice = int32_t((units + a.ctas - 1) / a.ctas);
     // At least 8 units a thread (16384 x 4096 bf16 takes 72 us so, 103 with 4 and 80 with 16)
-    // but at most 4 entries (6263 x 2688 fp16 with 179: 58 us so, 77 with 6 and 76 with 2).
+    // but at most 4 entries (6263 x 2688 fp16 with 179: 38 us so, 49 with 6 and 50 with 2).
     int threads = kDistillThreads;
     while (threads > kWarp && a.slice < threads * 8 && a.top_k <= threads * 2) threads /= 2;
     const int64_t smem = int64_t(a.slice) * 16 + lists;
@@ -225,7 +231,7 @@ cudaError_t launch_rows(DistillArgs& a, cudaStream_t stream, bool* done) {
     if (ce != cudaSuccess) return ce;
     const int64_t resident = std::max<int64_t>(
         1, std::min<int64_t>(std::min(24, 3 * kDistillThreads / threads),
-                             (227 * 1024) / (smem + 8 * 1024)));
+                             (227 * 1024) / (smem + 6 * 1024)));
     clusters = resident * kSms;
     if (a.ctas > 1)
       clusters = std::min(clusters / a.ctas, clusters_at_once(f, threads, smem, a.ctas));

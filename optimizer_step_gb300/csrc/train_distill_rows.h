@@ -31,6 +31,7 @@ struct DistillArgs {
   int32_t slice;             // units of a row that each of them holds
   int32_t phase, row_phase;  // elements from a unit's boundary to the first row; row to row
   int32_t whole;             // grad's units are aligned where those of the logits are
+  int32_t bucket_bits;       // of a row's entries by their tokens
 };
 
 __device__ __forceinline__ int64_t read_id(const void* p, int64_t i, int32_t is64) {
@@ -99,7 +100,7 @@ __device__ __forceinline__ float largest(const Unit<ZT> (&x)[N]) {
 
 // The softmaxes that a row needs: one (one term, or both at temperature 1), two, or two
 // of which the hard term's exponentials are the squares of the soft term's (at temperature
-// 2: 200 us for 8192 x 32000, where two exponentials an element take 228 at temperature 3).
+// 2: 196 us for 8192 x 32000, where two exponentials an element take 214 at temperature 3).
 constexpr int kOne = 0, kTwo = 1, kSquares = 2;
 
 // Sums of exponentials relative to a largest value.  That starts at the lowest finite
@@ -151,14 +152,16 @@ constexpr int kRingBytes = kRingStages * kChunk * 16;  // a warp
 // the next row's in their place; that row has been on its way to L2 since the first
 // barrier.  What is left at the row's ends goes to single threads of the first CTA, one
 // element each.  The teacher's entries are fetched a row ahead; the tokens they name are
-// written again, all of a token's shares together, when the others are done.
+// written again, all of a token's shares together, when the others are done; entries that
+// name the same token find one another in a table of buckets.
 //
 // Instructions bound it, not memory: two readings with unpacking, an exponential and four
 // sums or products of pairs each take 12 an element, some 700 a row and warp come on top,
 // and the warps that have entries keep the others waiting.  8192 x 32000 bf16 with 64
-// entries takes 192 us at one temperature and 200 at two (5.5 and 5.2 TB/s), without
-// entries 172 (6.1 TB/s).  Without the prefetch into L2 it was 218.  128 threads a CTA took
-// 197, more parts of a row waited for one by one 205.
+// entries takes 196 us at one temperature and at two (5.3 TB/s), without entries 174 (6.0
+// TB/s).  Comparing all pairs of entries takes 4 us more; 4096 rows with 256 entries take 125
+// us (167), with 1000 186 (620).  Without the prefetch into L2 the first was 20 us slower;
+// 128 threads a CTA, or more parts of a row waited for one by one, were no quicker.
 //
 // RING: the loss of more rows than there is room for.  It needs a row once, so units come
 // through a ring for each warp, those of the next row behind this one's without a pause; a
@@ -187,6 +190,9 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
   const int rank = a.ctas == 1 ? 0 : int(blockIdx.x) % a.ctas;
   uint4* slot = reinterpret_cast<uint4*>(smem);
   const uint32_t slot_address = shared_address(smem);
+  // Of each row's entries, twice by the row's parity: tokens, what they take off the
+  // gradient, logits (`room` each), and for a gradient what is known of tokens named again;
+  // then an entry for each bucket, of two kinds.
   unsigned char* lists = smem + (RING ? size_t(warps * kRingBytes) : size_t(a.slice) * 16);
 
   const bool soft = a.top_k > 0 && a.soft_weight != 0.f;
@@ -198,6 +204,12 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
   if constexpr (N == 2) c[1] = kLog2e;
   const float ct = a.inv_temperature * kLog2e;
 
+  uint8_t* const marks = lists + 2 * 3 * 4 * room;
+  uint16_t* const buckets = reinterpret_cast<uint16_t*>(marks + 2 * room);
+  const auto bucket_of = [&](int token, int kind) {
+    const uint32_t x = uint32_t(token) * (kind ? 2038074743u : 1000000007u);
+    return (kind << a.bucket_bits) + int(x >> (32 - a.bucket_bits));
+  };
   cg::cluster_group cluster = cg::this_cluster();
   if (a.ctas > 1) cluster.sync();  // all of its CTAs run now
   pdl_wait();
@@ -292,6 +304,22 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
     int32_t* id = reinterpret_cast<int32_t*>(lists) + parity * 3 * room;
     float* coef = reinterpret_cast<float*>(id + room);
     float* zed = coef + room;
+    uint8_t* mark = marks + parity * room;
+    // Entries of one token meet in its buckets, where one of them stays: it stands for all,
+    // and is marked if there are others.  An entry that finds another token's in both buckets
+    // has to look through the list, as its token's others have.
+    constexpr uint8_t kAlone = 0, kSearch = 1, kStoodFor = 2;
+    const auto enter = [&](int k, int token) {
+      mark[k] = kAlone;
+      buckets[bucket_of(token, 0)] = buckets[bucket_of(token, 1)] = uint16_t(k);
+    };
+    const auto meet = [&](int k) {
+      const int token = id[k];
+      int held = buckets[bucket_of(token, 0)];
+      if (id[held] != token) held = buckets[bucket_of(token, 1)];
+      if (id[held] != token) mark[k] = kSearch;
+      else if (held != k) mark[k] = kStoodFor, mark[held] = kSearch;
+    };
     const int head = head_of(row), units = (vocab - head) / E;
     const int mine = mine_of(units);  // units here; < 0: none
     // The next row.
@@ -321,6 +349,7 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
       id[k] = valid ? int32_t(i) : -1;
       coef[k] = t;
       if (!valid) return false;
+      if constexpr (GRAD) enter(k, int32_t(i));
       if (t > best) {
         size = size * exp2_of((best - t) * ct) + 1.f;
         best = t;
@@ -345,7 +374,10 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
     float label_z = 0.f;
     if (tid == 0) {
       for (int k = a.top_k; k < room; ++k) id[k] = -1;
-      if (live && hard) id[a.top_k] = int32_t(label), label_z = to_float<ZT>(z[label]);
+      if (live && hard) {
+        id[a.top_k] = int32_t(label), label_z = to_float<ZT>(z[label]);
+        if constexpr (GRAD) enter(a.top_k, int32_t(label));
+      }
     }
     // The largest value and the sums.
     Sums<TERMS> sums;
@@ -364,14 +396,19 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
       }
       sums.raise(fmaxf(sums.top, largest(x)), c);
       const F2 down = pair(-sums.top);
-      F2 t[N];  // of these alone, for short chains of additions
+      // In a ring, where a thread has more of a row, of these alone, for short chains of
+      // additions.
+      F2 t[N];
+      if constexpr (!RING)
+#pragma unroll
+        for (int n = 0; n < N; ++n) t[n] = pair(sums.s[n], 0.f);
 #pragma unroll
       for (int k = 0; k < kAtOnce; ++k)
 #pragma unroll
         for (int h = 0; h < E / 2; ++h) {
           const F2 d = add2(x[k].get(h), down);
           const F2 e = exp2_of(mul2(d, pair(c[0])));
-          const bool begun = k + h > 0;
+          const bool begun = !RING || k + h > 0;
           t[0] = begun ? add2(t[0], e) : e;
           if constexpr (TERMS == kTwo) {
             const F2 e1 = exp2_of(mul2(d, pair(c[1])));
@@ -380,7 +417,7 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
           if constexpr (TERMS == kSquares) t[1] = begun ? fma2(e, e, t[1]) : mul2(e, e);
         }
 #pragma unroll
-      for (int n = 0; n < N; ++n) sums.s[n] += sum2(t[n]);
+      for (int n = 0; n < N; ++n) sums.s[n] = (RING ? sums.s[n] : 0.f) + sum2(t[n]);
     };
     if constexpr (RING) {
       const int end = min(mine, first + run);
@@ -479,13 +516,17 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
         const float p = exp2_of(d * ct) * inv;
         sum += soft_term(a, p, d, zed[k] - top, logs);
         coef[k] = weight * p;
+        if constexpr (GRAD) meet(k);
       }
       sum = warp_sum(sum);
       if (lane == 0) terms[parity][warp] = sum;
     } else if (GRAD && work && !any) {
       for (int k = tid; k < a.top_k; k += threads) id[k] = -1;
     }
-    if (GRAD && tid == 0) coef[a.top_k] = a.hard_weight * up;
+    if (GRAD && tid == 0) {
+      coef[a.top_k] = a.hard_weight * up;
+      if (work && any && id[a.top_k] >= 0) meet(a.top_k);
+    }
     if constexpr (GRAD) {
       const bool zero = !work || up == 0.f;
       float w[N];  // weights of the exponentials
@@ -540,22 +581,23 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
       if (single >= 0) grad[single] = zero ? TG(0) : from_float<GT>(smooth1(edge));
       __syncthreads();
       if (!zero) {
-        // All of a token's shares are taken off together, by each entry that names it.
+        // All of a token's shares are taken off together.
         const int lo = rank * a.slice * E + head, hi = lo + max(mine, 0) * E;
         for (int k = tid; k <= a.top_k; k += threads) {
           const int token = id[k];
           const bool inside = token >= lo && token < hi;
           const bool end = rank == 0 && (token < head || token >= head + units * E);
-          if (token < 0 || !(inside || end)) continue;
+          if (token < 0 || mark[k] == kStoodFor || !(inside || end)) continue;
           float off = coef[k];
-          int named = 0;
-          for (int o = 0; o < room; o += 4) {
-            const int4 i = *reinterpret_cast<const int4*>(id + o);
-            named += (i.x == token) + (i.y == token) + (i.z == token) + (i.w == token);
-          }
-          if (named > 1) {
+          if (mark[k] == kSearch) {
             off = 0.f;
-            for (int o = 0; o <= a.top_k; ++o) off += id[o] == token ? coef[o] : 0.f;
+            for (int o = 0; o < room; o += 4) {
+              const int4 i = *reinterpret_cast<const int4*>(id + o);
+              if (i.x == token) off += coef[o];
+              if (i.y == token) off += coef[o + 1];
+              if (i.z == token) off += coef[o + 2];
+              if (i.w == token) off += coef[o + 3];
+            }
           }
           grad[token] = from_float<GT>(smooth1(zed[k]) - off);
         }

@@ -304,6 +304,25 @@ def test_a_token_named_again(vocab, top):
     check(data, 1.0, 1.0, 0.0)
 
 
+@pytest.mark.parametrize("top", [3, 40, 100, 256, 1000, 1024])
+@pytest.mark.parametrize("n,vocab,range_", [(600, 700, 700), (400, 4100, 4100), (400, 4100, 90),
+                                            (40, 131071, 131071), (40, 131071, 2000)])
+def test_tokens_named_any_number_of_times(n, vocab, range_, top):
+    data = Data(n, vocab, 0)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    data.ids = torch.randint(range_, (n, top), generator=gen, device="cuda")
+    data.teacher = torch.randn(n, top, generator=gen, device="cuda")
+    data.ids[torch.rand(n, top, generator=gen, device="cuda") < 0.05] = -1
+    data.labels[::2] = data.ids[::2, top // 2]
+    data.ids[3] = -1
+    data.labels[3] = 8
+    first = check(data, 2.0, 0.5, 0.5)
+    check(data, 1.0, 1.0, 0.0)
+    again = og.distill_loss_grad(*data.args(), temperature=2.0, soft_weight=0.5, hard_weight=0.5)
+    assert all(torch.equal(a, b) for a, b in zip(first, again))
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP16, FP32])
 @pytest.mark.parametrize("vocab", [60, 2001, 32000])
 def test_masked_logits(dtype, vocab):
