@@ -9,7 +9,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .embedding import _ID_TYPES, _TYPES, _code, _enqueue, _fits, _row_stride
+from .embedding import _ID_TYPES, _TYPES, _code, _enqueue, _fits, _row_stride, _wrote
 from .layernorm import _matrix, _new_like, _same_rows
 
 
@@ -125,6 +125,7 @@ def distill_loss_grad(logits: torch.Tensor, top_ids: torch.Tensor | None,
                 or row_grad.shape != logits.shape[:-1] or not row_grad.is_contiguous()):
             raise ValueError("row_grad: expected float32 of logits.shape[:-1], contiguous")
         g_ptr = row_grad.data_ptr()
+    given = out
     if out is None:
         o_code = args[1] if dtype is None else _TYPES.get(dtype)
         if o_code is None:
@@ -138,6 +139,8 @@ def distill_loss_grad(logits: torch.Tensor, top_ids: torch.Tensor | None,
     loss = torch.empty(logits.shape[:-1], dtype=torch.float32, device=logits.device)
     _enqueue(index, _lib.load().train_distill, *args, loss.data_ptr(), g_ptr, scale,
              out.data_ptr(), o_code, o_stride)
+    if given is not None:
+        _wrote(given)
     return loss, out
 
 

@@ -93,6 +93,11 @@ def _enqueue(index, call, *args):
         check(rc)
 
 
+# Counts a change of a tensor that the caller gave and a call wrote to: a graph that saved
+# it then refuses its backward pass, as behind torch's own operators in place.
+_wrote = torch.autograd.graph.increment_version
+
+
 class _Embed(torch.autograd.Function):
     """The lookup of a table that requires grad."""
 
@@ -152,6 +157,7 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
             raise RuntimeError("embed: out= cannot be given for a table that requires grad")
         return _Embed.apply(table, ids, scale, first_row, out_dtype)
     t_stride = dim if table.is_contiguous() else _row_stride("table", table)
+    given = out
     if out is None:
         o_code = t_code if out_dtype is None else _TYPES.get(out_dtype)
         if o_code is None:
@@ -166,6 +172,8 @@ def embed(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1.0, first_r
     _enqueue(index, _lib.load().train_embed, table.data_ptr(), t_code, rows, dim, t_stride,
              ids.data_ptr(), i_code, ids.numel(), first_row, scale, out.data_ptr(), o_code,
              o_stride)
+    if given is not None:
+        _wrote(given)
     return out
 
 
@@ -197,6 +205,7 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
     g_stride = dim if grad_out.is_contiguous() else _row_stride("grad_out", grad_out)
     if grad_out.shape[:-1] != ids.shape:
         raise ValueError("grad_out: expected ids.shape + (dim,)")
+    given = out
     if out is None:
         if n_rows is None:
             raise ValueError("n_rows or out must be given")
@@ -221,6 +230,8 @@ def embed_grad(grad_out: torch.Tensor, ids: torch.Tensor, *, n_rows: int | None 
              ids.data_ptr(), i_code, n_ids, first_row, padding_id, scale, 1 if accumulate else 0,
              out.data_ptr(), o_code, rows, dim, o_stride,
              workspace.data_ptr() if need else None, need)
+    if given is not None:
+        _wrote(given)
     return out
 
 

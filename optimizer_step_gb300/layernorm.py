@@ -13,7 +13,7 @@ import torch
 
 from . import _lib
 from ._lib import check
-from .embedding import _TYPES, _code, _enqueue, _row_stride
+from .embedding import _TYPES, _code, _enqueue, _row_stride, _wrote
 
 
 def _vector(name, t, dim, index):
@@ -133,6 +133,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
             raise RuntimeError("layer_norm: out= cannot be given where a gradient is required")
         y, kept = _LayerNorm.apply(x, weight, bias, eps, out_dtype)
         return (y, kept) if stats else y
+    given = out
     if out is None:
         o_code = code if out_dtype is None else _TYPES.get(out_dtype)
         if o_code is None:
@@ -151,6 +152,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     _enqueue(index, _lib.load().train_layer_norm, x.data_ptr(), code, stride, rows, dim, w_ptr,
              b_ptr, p_code, eps, out.data_ptr(), o_code, o_stride,
              kept.data_ptr() if stats else None)
+    if given is not None:
+        _wrote(given)
     return (out, kept) if stats else out
 
 
@@ -217,6 +220,9 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
              None if dx is None else dx.data_ptr(), dx_stride,
              None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
              p_code, 1 if accumulate else 0, workspace.data_ptr() if need else None, need)
+    for asked, t in ((x_grad, dx), (weight_grad, dw), (bias_grad, db)):
+        if t is not None and asked is not True:
+            _wrote(t)
     return dx, dw, db
 
 
