@@ -17,6 +17,7 @@ import torch
 
 from . import _lib
 from ._lib import LambError, LambHParams, LambLossScaler, LambResult, LambWorkItem, check
+from .embedding import _wrote
 
 _GRAD_CODES = {torch.bfloat16: _lib.LAMB_GRAD_BF16, torch.float16: _lib.LAMB_GRAD_FP16}
 
@@ -130,6 +131,10 @@ class Lamb:
                     ctypes.c_void_p(self.stream.cuda_stream)))
         self._h = h
         self._n = n
+        # What a model's graph may have saved of the tensors that a step writes; slices of one
+        # buffer share its version.
+        self._counted = list({id(t): t for t in (
+            w if w._base is None else w._base for w in (*weights, *weights_bf16))}.values())
         self._grad_ptrs = None
         self._grads_keep = None
         self._result = LambResult()
@@ -166,6 +171,7 @@ class Lamb:
             raise ValueError("no grads: pass grads= or call set_grads first")
         check(self._lib.lamb_step(self._h, self._grad_ptrs, float(lr), int(t), float(clip),
                                   float(loss_scale), ctypes.byref(self._result)))
+        _wrote(self._counted)
         self.loss_scale = float(self._result.loss_scale)
         self.next_loss_scale = float(self._result.next_loss_scale)
         return bool(self._result.skipped), float(self._result.grad_norm)
@@ -184,6 +190,7 @@ class Lamb:
         seq = ctypes.c_int64()
         check(self._lib.lamb_step_async(self._h, self._grad_ptrs, float(lr), float(clip),
                                         float(loss_scale), ctypes.byref(seq)))
+        _wrote(self._counted)
         return int(seq.value)
 
     def result(self, seq: int, wait: bool = True):
@@ -213,12 +220,14 @@ class Lamb:
         tensors' {sum w^2, sum r^2} into ``tensor_exchange`` (sum them over the
         group before phase 3).  ``t`` 0: the GPU's step counter."""
         check(self._lib.lamb_split_moments(self._h, float(lr), int(t), float(clip)))
+        _wrote(self._counted)  # small tensors are finished here
 
     def split_apply(self) -> int:
         """Phase 3: the update from the summed ``tensor_exchange``; returns
         the step's sequence number for ``result``."""
         seq = ctypes.c_int64()
         check(self._lib.lamb_split_apply(self._h, ctypes.byref(seq)))
+        _wrote(self._counted)
         return int(seq.value)
 
     def split_step(self, lr: float, clip: float = 0.0, t: int = 0, grads=None,
