@@ -9,7 +9,8 @@ from __future__ import annotations
 import torch
 
 from . import _lib
-from .embedding import _ID_TYPES, _TYPES, _code, _enqueue, _fits, _row_stride, _wrote
+from .embedding import (_ID_TYPES, _TYPES, _code, _enqueue, _fits, _forward_mode, _no_tangent,
+                        _row_stride, _wrote)
 from .layernorm import _matrix, _new_like, _same_rows
 
 
@@ -84,11 +85,14 @@ def distill_loss(logits: torch.Tensor, top_ids: torch.Tensor | None,
     the vocabulary, is left out: its loss and gradient are 0, whatever it holds.
 
     If ``logits`` require grad, so does the result; it can be differentiated once.
-    The teacher gets no gradient.  As with torch's own operators, a backward pass that is
-    captured into a CUDA graph needs leaves that no eager result still alive depends on.
+    The teacher gets no gradient, and arguments with a forward-mode tangent are refused.
+    As with torch's own operators, a backward pass that is captured into a CUDA graph
+    needs leaves that no eager result still alive depends on.
     """
     args, index = _arguments(logits, top_ids, top_logits, labels, temperature, soft_weight,
                              hard_weight, ignore_id)
+    if _forward_mode():
+        _no_tangent("distill_loss", logits, top_logits)
     if torch.is_grad_enabled():
         if top_logits is not None and top_logits.requires_grad:
             raise RuntimeError("distill_loss: the teacher's logits get no gradient; detach them")

@@ -13,7 +13,8 @@ import torch
 
 from . import _lib
 from ._lib import check
-from .embedding import _TYPES, _code, _enqueue, _row_stride, _wrote
+from .embedding import (_TYPES, _code, _enqueue, _forward_mode, _no_tangent, _row_stride,
+                        _wrote)
 
 
 def _vector(name, t, dim, index):
@@ -112,9 +113,10 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
     eps)``, which ``layer_norm_grad`` takes.
 
     If ``x``, ``weight`` or ``bias`` requires grad, so does the result.  It can be
-    differentiated once, and ``out`` is refused then.  ``stats`` have no gradient.  As
-    with torch's own operators, a backward pass that is captured into a CUDA graph needs
-    leaves that no eager result still alive depends on.
+    differentiated once, and ``out`` is refused then.  ``stats`` have no gradient, and
+    arguments with a forward-mode tangent are refused.  As with torch's own operators, a
+    backward pass that is captured into a CUDA graph needs leaves that no eager result
+    still alive depends on.
     """
     code, rows, dim, stride, index = _matrix("x", x)
     w_ptr = b_ptr = None
@@ -126,6 +128,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
         if weight is not None and b_code != p_code:
             raise TypeError(f"bias: expected {weight.dtype}, the weight's type, got {bias.dtype}")
         p_code = b_code
+    if _forward_mode():
+        _no_tangent("layer_norm", x, weight, bias)
     if torch.is_grad_enabled() and (x.requires_grad
                                     or (weight is not None and weight.requires_grad)
                                     or (bias is not None and bias.requires_grad)):
