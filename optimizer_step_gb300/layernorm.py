@@ -224,9 +224,10 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
              None if dx is None else dx.data_ptr(), dx_stride,
              None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
              p_code, 1 if accumulate else 0, workspace.data_ptr() if need else None, need)
-    for asked, t in ((x_grad, dx), (weight_grad, dw), (bias_grad, db)):
-        if t is not None and asked is not True:
-            _wrote(t)
+    given = [t for asked, t in ((x_grad, dx), (weight_grad, dw), (bias_grad, db))
+             if asked is not True and t is not None]
+    if given:
+        _wrote(given)
     return dx, dw, db
 
 
