@@ -135,7 +135,8 @@ LAMB_API int train_embed_grad(const void* grad_out, int32_t grad_out_dtype,
  * zero keep their digits; rows whose squares leave fp32's range are scaled by a
  * power of two first (magnitudes up to 2^126).  An inf or NaN makes its row NaN.
  * Strides are at least dim; dim is at least 1, n_rows may be 0, both are at most
- * 2^31 - 1.
+ * 2^31 - 1.  y that lies partly over x, and y or stats that lie over anything else of
+ * the call, are refused.
  */
 LAMB_API int train_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n_rows,
                               int64_t dim, const void* weight, const void* bias,
@@ -169,7 +170,9 @@ LAMB_API int train_layer_norm_grad_workspace(int64_t n_rows, int64_t dim, int64_
  *                matter, and it is free again when the stream has passed the call
  *
  * The sums over the rows are fp32, in an order that only the sizes, types and
- * alignment fix; no atomic sum is used.  n_rows * dim is at most 2^40.
+ * alignment fix; no atomic sum is used.  n_rows * dim is at most 2^40.  Outputs and
+ * workspace that lie over one another are refused, and x_grad or workspace partly over
+ * what the call reads.
  */
 LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
                                    int64_t grad_out_stride, const void* x, int32_t x_dtype,
@@ -212,7 +215,9 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
  * Sums are fp32 or wider.  A logit of -inf (a masked token) has q = s = 0; if
  * the teacher or the label names it the loss is +inf.  A row with a NaN or +inf,
  * or with nothing but -inf, has a NaN loss and gradient.  vocab is at least 1,
- * n_rows may be 0, both are at most 2^31 - 1.
+ * n_rows may be 0, both are at most 2^31 - 1.  loss may be row_grad itself.  grad that
+ * lies partly over the logits, and grad or loss that lie over anything else of the call,
+ * are refused.
  */
 LAMB_API int train_distill(const void* logits, int32_t logits_dtype, int64_t logits_stride,
                            int64_t n_rows, int64_t vocab, const void* top_ids,

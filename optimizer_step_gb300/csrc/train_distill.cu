@@ -319,6 +319,26 @@ LAMB_API int train_distill(const void* logits, int32_t logits_dtype, int64_t log
   if (hard_weight != 0.f && !labels && n_rows > 0)
     return fail(LAMB_ERR_INVALID, "hard_weight needs labels");
   if (n_rows == 0 || (!loss && !grad)) return LAMB_OK;
+  const auto ids_of = [](const char* name, const void* p, int32_t type, int64_t n, int64_t dim,
+                         int64_t stride) {
+    return Rows{name, p, n, dim, stride, type == TRAIN_INT64 ? 8 : 4, -1};
+  };
+  const int64_t entries = soft_weight != 0.f ? top_k : 0;
+  const Rows read[] = {
+      rows_of("logits", logits, logits_dtype, n_rows, vocab, logits_stride),
+      ids_of("top_ids", top_ids, top_ids_dtype, n_rows, entries, top_ids_stride),
+      rows_of("top_logits", top_logits, top_logits_dtype, n_rows, entries, top_logits_stride),
+      ids_of("labels", labels, labels_dtype, 1, n_rows, 0),
+      rows_of("row_grad", row_grad, TRAIN_FP32, 1, n_rows)};
+  // A row's loss is written behind the last reading of its row_grad.
+  const Rows losses = rows_of("loss", loss, TRAIN_FP32, 1, n_rows);
+  const Rows slopes = rows_of("grad", grad, grad_dtype, n_rows, vocab, grad_stride);
+  rc = check_apart(slopes, losses);
+  for (int k = 0; k < 5 && rc == LAMB_OK; ++k) {
+    rc = check_apart(losses, read[k], k == 4);
+    if (rc == LAMB_OK) rc = check_apart(slopes, read[k], k == 0);
+  }
+  if (rc != LAMB_OK) return rc;
   DistillArgs a{};
   a.logits = logits, a.top_ids = top_ids, a.top_logits = top_logits, a.labels = labels;
   a.row_grad = row_grad, a.loss = loss, a.grad = grad;

@@ -269,6 +269,47 @@ inline int check_ids(const void* ids, int32_t ids_dtype, int64_t n_ids, int64_t 
   return LAMB_OK;
 }
 
+// What a call reads or writes: rows of `dim` elements, `stride` elements apart.
+struct Rows {
+  const char* name;
+  const void* p;  // NULL: nothing
+  int64_t n, dim, stride;
+  int size;       // bytes an element
+  int32_t type;
+};
+
+// Whether two of them have a byte in common.  Exact where the strides are alike or no two
+// rows can meet at any distance; at two strides whose rows could meet, the ranges decide.
+inline bool meet(const Rows& a, const Rows& b) {
+  using I = __int128;
+  if (!a.p || !b.p || a.n <= 0 || b.n <= 0 || a.dim <= 0 || b.dim <= 0) return false;
+  const I at = I(reinterpret_cast<uintptr_t>(a.p)), bt = I(reinterpret_cast<uintptr_t>(b.p));
+  const I wa = I(a.dim) * a.size, wb = I(b.dim) * b.size;
+  const I sa = a.n > 1 ? I(a.stride) * a.size : 0, sb = b.n > 1 ? I(b.stride) * b.size : 0;
+  if (at + (a.n - 1) * sa + wa <= bt || bt + (b.n - 1) * sb + wb <= at) return false;
+  // Row i of a and row j of b meet where i sa - j sb, a multiple of g, lies between
+  // bt - at - wa and bt - at + wb.
+  I g = sa, r = sb;
+  while (r) {
+    const I rest = g % r;
+    g = r, r = rest;
+  }
+  if (g == 0) return true;
+  const I last = bt - at + wb - 1;
+  const I most = last - ((last % g) + g) % g;  // the largest multiple that is not above
+  return most > bt - at - wa;
+}
+
+// Refuses an output that lies partly over something else of its call; `same`: it may be
+// that very matrix.
+inline int check_apart(const Rows& out, const Rows& other, bool same = false) {
+  if (!meet(out, other)) return LAMB_OK;
+  if (same && out.p == other.p && out.type == other.type &&
+      (out.stride == other.stride || out.n == 1))
+    return LAMB_OK;
+  return fail(LAMB_ERR_INVALID, std::string(out.name) + " overlaps " + other.name);
+}
+
 // Launches a kernel, if asked as a programmatic dependent of the one before
 // it in the stream, in clusters of `cluster` CTAs.
 template <class... A>

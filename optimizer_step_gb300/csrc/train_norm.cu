@@ -176,6 +176,19 @@ LAMB_API int train_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, 
   if (dim == 0) return fail(LAMB_ERR_INVALID, "dim must be at least 1");
   if (!(eps >= 0.f && eps <= FLT_MAX)) return fail(LAMB_ERR_INVALID, "eps must be finite and >= 0");
   if (n_rows == 0) return LAMB_OK;
+  const Rows in = rows_of("x", x, x_dtype, n_rows, dim, x_stride);
+  const Rows out = rows_of("y", y, y_dtype, n_rows, dim, y_stride);
+  const Rows kept = rows_of("stats", stats, TRAIN_FP32, 1, 2 * n_rows);
+  const Rows params[] = {rows_of("weight", weight, param_dtype, 1, dim),
+                         rows_of("bias", bias, param_dtype, 1, dim)};
+  rc = check_apart(out, in, true);
+  if (rc == LAMB_OK) rc = check_apart(out, kept);
+  if (rc == LAMB_OK) rc = check_apart(kept, in);
+  for (const Rows& p : params) {
+    if (rc == LAMB_OK) rc = check_apart(out, p);
+    if (rc == LAMB_OK) rc = check_apart(kept, p);
+  }
+  if (rc != LAMB_OK) return rc;
   NormArgs f{};
   f.x = x, f.weight = weight, f.bias = bias, f.y = y, f.stats = stats;
   f.n_rows = n_rows, f.x_stride = x_stride, f.y_stride = y_stride;

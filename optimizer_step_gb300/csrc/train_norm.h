@@ -187,6 +187,12 @@ inline int check_vector(const char* name, const void* p, int32_t dtype) {
   return LAMB_OK;
 }
 
+// A matrix, or one row of consecutive elements.
+inline Rows rows_of(const char* name, const void* p, int32_t type, int64_t n, int64_t dim,
+                    int64_t stride = 0) {
+  return {name, p, n, dim, stride, size_of(type), type};
+}
+
 inline int launched(const char* what, cudaError_t ce) {
   return ce == cudaSuccess
              ? LAMB_OK

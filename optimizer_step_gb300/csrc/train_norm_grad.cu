@@ -290,6 +290,26 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
     if (reinterpret_cast<uintptr_t>(workspace) % 16)
       return fail(LAMB_ERR_ALIGN, "workspace is not 16-byte aligned");
   }
+  if (n_rows > 0) {
+    const Rows read[] = {rows_of("grad_out", grad_out, grad_out_dtype, n_rows, dim,
+                                 grad_out_stride),
+                         rows_of("x", x, x_dtype, n_rows, dim, x_stride),
+                         rows_of("weight", weight, weight_dtype, 1, dim),
+                         rows_of("stats", stats, TRAIN_FP32, 1, 2 * n_rows)};
+    const int64_t held = params ? most_pieces(n_rows, dim) * 2 * dim : 0;
+    const Rows written[] = {rows_of("x_grad", x_grad, x_dtype, n_rows, dim, x_grad_stride),
+                            rows_of("workspace", workspace, TRAIN_FP32, 1, held),
+                            rows_of("weight_grad", weight_grad, param_grad_dtype, 1, dim),
+                            rows_of("bias_grad", bias_grad, param_grad_dtype, 1, dim)};
+    for (int i = 0; i < 4 && rc == LAMB_OK; ++i) {
+      for (int k = 0; k < i && rc == LAMB_OK; ++k) rc = check_apart(written[i], written[k]);
+      // The parameters' gradients are written when everything has been read.
+      if (i < 2)
+        for (int k = 0; k < 4 && rc == LAMB_OK; ++k)
+          rc = check_apart(written[i], read[k], i == 0 && k < 2);
+    }
+    if (rc != LAMB_OK) return rc;
+  }
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   NormGradArgs a{};
   a.dy = grad_out, a.x = x, a.weight = weight, a.stats = stats, a.dx = x_grad;
