@@ -204,7 +204,8 @@ LAMB_API int train_layer_norm_grad(const void* grad_out, int32_t grad_out_dtype,
  *   labels       NULL (then hard_weight is 0), or n_rows consecutive ids.  A row
  *                whose label is ignore_id or lies outside [0, vocab) is left
  *                out: its loss and gradient are 0 whatever its logits hold
- *   temperature  finite and > 0, as its reciprocal; the weights are finite
+ *   temperature  finite and > 0, as its reciprocal; the weights are finite.  With a
+ *                first term so are log2(e) / temperature and soft_weight * temperature
  *   loss         NULL, or n_rows floats
  *   row_grad     NULL (1 for every row), or n_rows floats: the gradient of what
  *                is minimised for each row's loss.  A row where it is 0 gets a

@@ -316,6 +316,11 @@ LAMB_API int train_distill(const void* logits, int32_t logits_dtype, int64_t log
     return fail(LAMB_ERR_INVALID, "temperature and its reciprocal must be finite and > 0");
   if (!(fabsf(soft_weight) <= FLT_MAX && fabsf(hard_weight) <= FLT_MAX))
     return fail(LAMB_ERR_INVALID, "soft_weight and hard_weight must be finite");
+  // What scales the exponents and the teacher's shares.
+  if (top_k > 0 && soft_weight != 0.f &&
+      !(inv * kLog2e <= FLT_MAX && fabsf(soft_weight * temperature) <= FLT_MAX))
+    return fail(LAMB_ERR_INVALID,
+                "log2(e) / temperature and soft_weight * temperature must be finite");
   if (hard_weight != 0.f && !labels && n_rows > 0)
     return fail(LAMB_ERR_INVALID, "hard_weight needs labels");
   if (n_rows == 0 || (!loss && !grad)) return LAMB_OK;
