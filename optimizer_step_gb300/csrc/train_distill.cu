@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
         continue;
       }
       const float d = coef[k] - best, p = exp2f(d * c) / size;
-      terms += soft_term(a, p, d, zed[k] - top, logs);
+      terms += soft_term(a, p, coef[k], best, zed[k], top, logs);
       coef[k] = a.soft_weight * a.temperature * p;
     }
     const bool hits = work && hard;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) row_kernel(const DistillArgs a) {
       // Without a distribution (soft_sum is NaN) a masked token's term means nothing.
       if (soft_sum != soft_sum) terms = soft_sum;
       if (work && any) loss = terms;
-      if (hits) loss += a.hard_weight * (logf(hard_sum) - (zed[top_k] - top));
+      if (hits) loss += hard_term(a, hard_sum, zed[top_k], top);
       a.loss[row] = loss;
     }
     if (!a.grad) return;

@@ -50,14 +50,25 @@ __device__ __forceinline__ F2 exp2_of(F2 x) {
   return pair(exp2_of(lo), exp2_of(hi));
 }
 
+// Half the difference of two logits; logits further apart than fp32's largest number have
+// one too.
+__device__ __forceinline__ float half_apart(float x, float y) { return 0.5f * x - 0.5f * y; }
+
 // An entry's term of the loss, soft_weight T^2 p (log p - log q), from the teacher's and
-// the student's logit less the largest, and log of the student's sum less log of the
+// the student's logit, the largest of each, and log of the student's sum less log of the
 // teacher's.  The weight goes to p and T into the difference, so that a named token of the
-// type's lowest value gives an infinite loss only where the loss is past fp32's range.
-__device__ __forceinline__ float soft_term(const DistillArgs& a, float p, float teacher,
-                                           float student, float logs) {
+// type's lowest value gives an infinite loss only where the loss is past fp32's range, and
+// an entry with p = 0 gives 0.
+__device__ __forceinline__ float soft_term(const DistillArgs& a, float p, float teacher, float best,
+                                           float student, float top, float logs) {
   if (student == -INFINITY) return copysignf(INFINITY, a.soft_weight);
-  return a.soft_weight * a.temperature * p * (teacher - student + a.temperature * logs);
+  const float half = half_apart(teacher, best) - half_apart(student, top);
+  return a.soft_weight * a.temperature * p * (half + 0.5f * a.temperature * logs) * 2.f;
+}
+// The label's, hard_weight (log of the sum - (the label's logit - the largest)).
+__device__ __forceinline__ float hard_term(const DistillArgs& a, float sum, float student,
+                                           float top) {
+  return a.hard_weight * (0.5f * logf(sum) - half_apart(student, top)) * 2.f;
 }
 
 // A unit of logits: 16 bytes.
@@ -514,7 +525,7 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
         }
         const float d = coef[k] - best;
         const float p = exp2_of(d * ct) * inv;
-        sum += soft_term(a, p, d, zed[k] - top, logs);
+        sum += soft_term(a, p, coef[k], best, zed[k], top, logs);
         coef[k] = weight * p;
         if constexpr (GRAD) meet(k);
       }
@@ -612,7 +623,7 @@ __global__ void __launch_bounds__(RING ? kRingThreads : kDistillThreads, RING ? 
         // Without a distribution a masked token's term means nothing.
         if (soft_sum != soft_sum) loss = soft_sum;
       }
-      if (work && hard) loss += a.hard_weight * (logf(hard_sum) - (zed[a.top_k] - top));
+      if (work && hard) loss += hard_term(a, hard_sum, zed[a.top_k], top);
       a.loss[row] = loss;
     }
     label = next_label, up = next_up, live = next_live;
