@@ -131,9 +131,16 @@ constexpr int kMostLanes = 512;  // threads a CTA
 constexpr int64_t kMostShared = 224 * 1024;  // a CTA's dynamic shared memory
 
 // Sizes whose sums one cluster takes and adds by itself, without a workspace: one launch
-// and one allocation less.  512 x 256 takes 16.6 us from Python and 22.5 with pieces; in a
-// captured graph, where launches cost little, 6.1 and 4.7.
-bool one_cluster(int64_t n_rows, int64_t dim) { return dim <= 1024 && n_rows * dim <= (1 << 17); }
+// and one allocation less, which from Python take 3 to 7 us.  On the GPU, in a captured
+// graph, it is as quick as the pieces or quicker up to some 32,000 elements and 500 rows (64
+// x 64 3.4 us and 4.0, 100 x 256 3.8 and 4.5), and loses where its 16 CTAs have more
+// rounds: 512 x 256 5.9 and 4.5, 128 x 1024 7.8 and 5.7, 131 x 1000 8.9 and 6.0; 4096 x 9, 8
+// rounds of two rows a warp, 7.9 and 3.9.  The limits stand where that comes to what the
+// call gains: 262 x 1000 loses 3.8 us, 8192 x 9 7.7, and 26,214 x 5 took 33 us where
+// pieces take 7.
+bool one_cluster(int64_t n_rows, int64_t dim) {
+  return dim <= 1024 && n_rows <= 4096 && n_rows * dim <= (1 << 17);
+}
 
 // Pieces that any of the kernels below may write.
 int64_t most_pieces(int64_t n_rows, int64_t dim) {
@@ -154,10 +161,9 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
   };
   const auto go = [&](NormGradKernel kernel, int64_t ctas, int64_t groups, int64_t smem) {
     if (a.joined) {
-      // A power of two, so that each kind of row's beginning has as many CTAs.
-      a.joined = 1;
-      while (a.joined < kJoined && a.joined < ctas) a.joined *= 2;
-      a.joined = std::max(a.joined, a.period);
+      // All of its CTAs, those without rows too: they write their share of the sums (1 x 1024
+      // takes 5.1 us so, 13.3 with one CTA).
+      a.joined = kJoined;
       *pieces = 1;
       smem = std::max(smem, groups * 2 * dim * 4);
       const void* f = reinterpret_cast<const void*>(kernel);
@@ -165,7 +171,7 @@ cudaError_t launch_rows(NormGradArgs& a, cudaStream_t stream, int64_t* pieces) {
       if (smem > 40 * 1024)
         ce = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   int(kMostShared));
-      if (ce == cudaSuccess && a.joined > 8)
+      if (ce == cudaSuccess)
         ce = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (ce != cudaSuccess) return ce;
       return launch(kernel, dim3(unsigned(a.joined)), int(groups * a.lanes), size_t(smem), stream,
