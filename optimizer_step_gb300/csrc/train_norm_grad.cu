@@ -8,8 +8,10 @@ namespace {
 // ------------------------------------------------------------ rows of any width
 constexpr int kWideThreads = 512;
 
-// For rows wider than 12,288, or than 8,192 where they begin differently in each matrix.
-// dx, one CTA a row; 8192 x 4096 bf16 took 177 us with this and the two below.
+// For rows wider than 12,288 (than 10,752 where x and grad_out are both fp32: two stages of
+// the ring and the weight fill a CTA's shared memory there), or than 8,192 where they begin
+// differently in each matrix.  dx, one CTA a row; 8192 x 4096 bf16 took 177 us with this and
+// the two below, 8192 x 12288 fp32 takes 502, where 8192 x 10752 takes 179 on chip.
 __global__ void __launch_bounds__(kWideThreads) wide_dx_kernel(const NormGradArgs a) {
   __shared__ float part[2][kWideThreads / kWarp];
   pdl_wait();
