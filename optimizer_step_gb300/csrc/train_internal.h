@@ -272,21 +272,28 @@ inline int check_ids(const void* ids, int32_t ids_dtype, int64_t n_ids, int64_t 
 // What a call reads or writes: rows of `dim` elements, `stride` elements apart.
 struct Rows {
   const char* name;
-  const void* p;  // NULL: nothing
+  const void* p;
   int64_t n, dim, stride;
-  int size;       // bytes an element
+  int size;  // bytes an element
   int32_t type;
+  __int128 end;  // behind the last byte; 0 if there is none
+
+  Rows(const char* name, const void* p, int64_t n, int64_t dim, int64_t stride, int size,
+       int32_t type)
+      : name(name), p(p), n(n), dim(dim), stride(stride), size(size), type(type), end(0) {
+    if (p && n > 0 && dim > 0) end = begin() + (__int128(n - 1) * stride + dim) * size;
+  }
+  __int128 begin() const { return __int128(reinterpret_cast<uintptr_t>(p)); }
 };
 
 // Whether two of them have a byte in common.  Exact where the strides are alike or no two
 // rows can meet at any distance; at two strides whose rows could meet, the ranges decide.
 inline bool meet(const Rows& a, const Rows& b) {
   using I = __int128;
-  if (!a.p || !b.p || a.n <= 0 || b.n <= 0 || a.dim <= 0 || b.dim <= 0) return false;
-  const I at = I(reinterpret_cast<uintptr_t>(a.p)), bt = I(reinterpret_cast<uintptr_t>(b.p));
+  const I at = a.begin(), bt = b.begin();
+  if (a.end <= bt || b.end <= at) return false;
   const I wa = I(a.dim) * a.size, wb = I(b.dim) * b.size;
   const I sa = a.n > 1 ? I(a.stride) * a.size : 0, sb = b.n > 1 ? I(b.stride) * b.size : 0;
-  if (at + (a.n - 1) * sa + wa <= bt || bt + (b.n - 1) * sb + wb <= at) return false;
   // Row i of a and row j of b meet where i sa - j sb, a multiple of g, lies between
   // bt - at - wa and bt - at + wb.
   I g = sa, r = sb;

@@ -144,7 +144,7 @@ def distill_loss_grad(logits: torch.Tensor, top_ids: torch.Tensor | None,
     _enqueue(index, _lib.load().train_distill, *args, loss.data_ptr(), g_ptr, scale,
              out.data_ptr(), o_code, o_stride)
     if given is not None:
-        _wrote(given)
+        _wrote((given,))
     return loss, out
 
 

@@ -157,7 +157,7 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
              b_ptr, p_code, eps, out.data_ptr(), o_code, o_stride,
              kept.data_ptr() if stats else None)
     if given is not None:
-        _wrote(given)
+        _wrote((given,))
     return (out, kept) if stats else out
 
 
@@ -196,6 +196,7 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
         raise ValueError(f"stats: expected float32 of shape {(2, *x.shape[:-1])}")
     w_code, w_ptr = (0, None) if weight is None else _vector("weight", weight, dim, index)
     device = x.device
+    given = ()
     if x_grad is True:
         dx = _new_like(x, None)
         dx_stride = dim
@@ -203,6 +204,7 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
         dx, dx_stride = None, dim
     else:
         dx = x_grad
+        given = (dx,)
         d_code, dx_stride = _same_rows("x_grad", dx, x.shape, index)
         if d_code != x_code:
             raise TypeError(f"x_grad: expected {x.dtype}, the type of x")
@@ -217,6 +219,10 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
     for name, t in (("weight_grad", dw), ("bias_grad", db)):
         if t is not None and t.dtype != dtype:
             raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if dw is not None and dw is weight_grad:
+        given += (dw,)
+    if db is not None and db is bias_grad:
+        given += (db,)
     need = _workspace_bytes(rows, dim) if dw is not None or db is not None else 0
     workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
     _enqueue(index, _lib.load().train_layer_norm_grad, grad_out.data_ptr(), g_code, g_stride,
@@ -224,8 +230,6 @@ def layer_norm_grad(grad_out: torch.Tensor, x: torch.Tensor, weight: torch.Tenso
              None if dx is None else dx.data_ptr(), dx_stride,
              None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr(),
              p_code, 1 if accumulate else 0, workspace.data_ptr() if need else None, need)
-    given = [t for asked, t in ((x_grad, dx), (weight_grad, dw), (bias_grad, db))
-             if asked is not True and t is not None]
     if given:
         _wrote(given)
     return dx, dw, db
